@@ -19,7 +19,14 @@
  *   dspk_accept_greedy  - longest matching prefix plus the target's token;
  *   dspk_lmhead_argmax_accept_greedy - the two calls above in one launch;
  *   dspk_accept_sample  - min(1, p/q) acceptance with residual resampling.
- *   dspk_accept_sample_ex - the same over penalised, top-k/top-p truncated distributions.
+ *   dspk_accept_sample_ex - the same over penalised, top-k/top-p truncated distributions;
+ *   dspk_qkv_norm_rope_append, dspk_kv_append, dspk_kv_read - q/k/v rows normed,
+ *                         rotated and stored in a paged cache, and read back;
+ *   dspk_tree_attention - the rows of a round (a token, a chain or a tree of
+ *                         drafts) over that cache;
+ *   dspk_tree_layout, dspk_accept_tree_greedy, dspk_kv_commit - a tree's masks
+ *                         and positions, greedy acceptance along it, and the
+ *                         accepted path's cache entries moved together.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -472,6 +479,230 @@ int dspk_accept_sample_ex(const float *logits, int64_t ldz,
                           const dspk_sample_params *params, const int32_t *counts,
                           int32_t *accept_len, int32_t *committed,
                           void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * The attention side of a round
+ * -----------------------------
+ * Between the q/k/v and o projections of a layer the round's rows attend to
+ * what is cached and to each other.  Per layer: dspk_qkv_norm_rope_append,
+ * then dspk_tree_attention; per round: dspk_tree_layout before the layers,
+ * dspk_accept_tree_greedy and dspk_kv_commit after the head.  A chain of drafts
+ * (dspk_accept_greedy) needs no tree calls: its accepted entries are already
+ * in place, and the next round's cache_len says how many are kept ("mlx-dspark"
+ * wiki summary: the cache is trimmed to the accepted length).
+ *
+ * A paged k/v cache of one layer, in device memory of the caller.  Positions
+ * 0, 1, ... of a request lie in pages of page_tokens positions, whose numbers
+ * its page table gives.
+ *
+ *   kv_heads    : k/v heads;
+ *   head_dim    : 64, 128 or 256;
+ *   page_tokens : positions per page, a power of two, 64 .. 65536;
+ *   bits        : 16 (bf16) or 8 (signed codes with an fp32 scale per
+ *                 position and head, value = scale * code);
+ *   pages       : pages of the pools, 1 .. 2^31 - 1;
+ *   k, v        : pools of dspk_kv_cache_bytes(...) bytes each, 256-byte
+ *                 aligned; no particular contents at first;
+ *   k_scales,
+ *   v_scales    : float [pages][kv_heads][page_tokens], 16-byte aligned
+ *                 (8 bits; NULL for 16).
+ *
+ * Layout of the pools (W = 8 elements of 16 bits, 16 of 8 bits; t a position
+ * of its page, d a dimension), in the order the matrix cores take them:
+ *   k : [page][head][t / 16][d / 4W][d % 4W / W][t % 16][d % W]
+ *   v : [page][head][t / 4W][d / 16][t % 16 / 4][d % 16][t % 4W / 16][t % 4]
+ */
+#define DSPK_MAX_TREE 64      /* largest tree (rows of one request in an attention call) */
+
+typedef struct dspk_kv_cache {
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_tokens;
+    int32_t bits;
+    int64_t pages;
+    void *k;
+    void *v;
+    float *k_scales;
+    float *v_scales;
+} dspk_kv_cache;
+
+/* Bytes of the k pool (and of the v pool); 0 if the shape is not supported. */
+size_t dspk_kv_cache_bytes(int64_t pages, int32_t kv_heads, int32_t head_dim, int32_t page_tokens, int32_t bits);
+
+/*
+ * The requests of a call (host struct, read during the call only; its arrays
+ * are device memory).
+ *
+ *   b          : requests, 1 .. 65535;
+ *   max_rows   : rows of every request, or with row_start the most of one;
+ *   total_rows : rows the row arrays hold (>= b * max_rows without row_start);
+ *   max_pages  : entries per request of page_table;
+ *   row_start  : int32 [b + 1], request r owns rows row_start[r] ..
+ *                row_start[r + 1] - 1; or NULL: rows r * max_rows ..;
+ *   cache_len  : int32 [b], positions cached before the call's rows: row i of
+ *                a request has cache position cache_len + i;
+ *   page_table : int32 [b][max_pages], only the entries of positions that a
+ *                call reads or writes are looked at.
+ *
+ * Rows of no request are left as they are.  Data faults (seen on the device):
+ * a row range that is negative, longer than max_rows or past total_rows
+ * holds no rows; a cache_len that is negative or runs past the page table, or
+ * a page number outside the pools, is never followed: nothing is stored there,
+ * and rows that would read it come out as NaN.
+ */
+typedef struct dspk_attn_batch {
+    int32_t b;
+    int32_t max_rows;
+    int32_t total_rows;
+    int32_t max_pages;
+    const int32_t *row_start;
+    const int32_t *cache_len;
+    const int32_t *page_table;
+} dspk_attn_batch;
+
+/*
+ * What dspk_qkv_norm_rope_append does to q and k (host struct; arrays on the
+ * device).
+ *
+ *   eps, q_weight, k_weight : x * rsqrt(mean(x^2) + eps) * weight over each
+ *                 head, weights float32 [head_dim], 16-byte aligned; NULL: no
+ *                 norm of that operand;
+ *   inv_freq    : float32 [rotary_dim / 2], or NULL: no rotation.  Pair i of
+ *                 the first rotary_dim dimensions turns by position *
+ *                 inv_freq[i] (the angle is reduced in fp64, so far positions
+ *                 are exact);
+ *   rotary_dim  : a multiple of 16, at most head_dim;
+ *   interleaved : 0: pair i is dimensions (i, i + rotary_dim / 2); 1: (2i, 2i + 1);
+ *   positions   : int32 [total_rows], or NULL: the row's cache position (a
+ *                 chain or a prompt).  For a tree: dspk_tree_layout's.
+ */
+typedef struct dspk_qk_prep {
+    float eps;
+    const float *q_weight;
+    const float *k_weight;
+    const float *inv_freq;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    const int32_t *positions;
+} dspk_qk_prep;
+
+/*
+ * A layer's q/k/v rows made ready for attention, in one launch: q and k normed
+ * per head and rotated, q written to q_out, k and v stored in the cache at the
+ * rows' positions.  Any number of rows: a verify round's or a prompt's.
+ *
+ *   q, k, v : rows [total_rows][ld], element type dtype (DSPK_F32 | DSPK_BF16,
+ *             as the projections write them), q_heads * head_dim or kv_heads *
+ *             head_dim columns, ld a multiple of 4 (fp32) or 8 (bf16), 16-byte
+ *             aligned; head h is columns h * head_dim ..;
+ *   q_out   : bf16 [total_rows][ldqo]; may be q itself if that is bf16 with
+ *             the same ld.
+ * Arithmetic is fp32 throughout, rounded once on storing (bf16: nearest even;
+ * 8-bit: see dspk_kv_append).  Rows of one call must not share a cache
+ * position.  Errors: DSPK_EINVAL (pointers, alignment, sizes, leading
+ * dimensions, eps, rotary_dim), DSPK_EUNSUPPORTED (cache format, rotary_dim not a
+ * multiple of 16, more rows than one launch numbers), DSPK_EDEVICE.
+ */
+int dspk_qkv_norm_rope_append(const dspk_kv_cache *cache, const dspk_attn_batch *batch, const dspk_qk_prep *prep,
+                              const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                              int32_t dtype, int32_t q_heads, uint16_t *q_out, int64_t ldqo, void *stream);
+
+/*
+ * k and v rows stored as they are ("mlx-dspark 0.7.0", quick start: an 8-bit
+ * k/v cache for long contexts).  8-bit caches quantise each head's row by
+ * itself: scale = max|x| / 127, code = x * 127 / max|x| rounded half to even.
+ * A row holding a value that is not finite reads back as NaN; one whose
+ * largest magnitude is below 4e-37 reads back as zeros.
+ */
+int dspk_kv_append(const dspk_kv_cache *cache, const dspk_attn_batch *batch, const void *k, int64_t ldk, const void *v,
+                   int64_t ldv, int32_t dtype, void *stream);
+
+/* The rows that an append with the same batch stored, as dtype (DSPK_F32 |
+ * DSPK_BF16) rows: cache positions cache_len .. of each request.  Errors as above. */
+int dspk_kv_read(const dspk_kv_cache *cache, const dspk_attn_batch *batch, void *k, int64_t ldk, void *v, int64_t ldv,
+                 int32_t dtype, void *stream);
+
+/* Workspace of dspk_tree_attention for these heads and at most max_rows rows
+ * per request, for any cache contents and page-table width (0 if a size is
+ * not supported).  It needs no clearing; calls that share it must be ordered on one
+ * stream. */
+size_t dspk_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t b, int32_t max_rows);
+
+/*
+ * Attention of a round's rows over the cache, which already holds their own k
+ * and v (an append with the same batch):
+ *   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale * q_i . k_j - max),
+ * over the positions j row i sees: all cache_len cached ones, and of the
+ * request's rows those whose bit is set in the row's mask.  q head h uses k/v
+ * head h / (q_heads / kv_heads).
+ *
+ *   batch     : at most DSPK_MAX_TREE rows per request (one decode step: 1);
+ *   q         : bf16 [total_rows][ldq], q_heads * head_dim columns, 16-byte
+ *               aligned, ldq % 8 == 0;
+ *   scale     : > 0 and finite (usually 1 / sqrt(head_dim));
+ *   tree_mask : uint64 [total_rows], bit j: the row sees row j of its request
+ *               (dspk_tree_layout); NULL: a chain, row i sees rows 0 .. i;
+ *   out       : bf16 [total_rows][ldo], like q: the o projection's input.  Must
+ *               not overlap q;
+ *   workspace : >= dspk_attn_workspace_bytes(...) bytes, 256-byte aligned.
+ * A row that sees nothing comes out as zeros.  What a masked position holds
+ * does not reach a row, NaN and infinities included.  Scores, statistics and
+ * sums are fp32; the result is deterministic.  Errors: DSPK_EINVAL,
+ * DSPK_EUNSUPPORTED (cache format, more than DSPK_MAX_TREE rows per request, a
+ * page table too large for one launch), DSPK_EDEVICE.
+ */
+int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch, const uint16_t *q, int64_t ldq,
+                        int32_t q_heads, float scale, const uint64_t *tree_mask, uint16_t *out, int64_t ldo,
+                        void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Trees of drafts.  Each of b requests has m_rows nodes (1 .. DSPK_MAX_TREE):
+ * node 0 is the anchor, node j >= 1 the draft draft_ids[j - 1] that follows
+ * node parents[j - 1] < j.  A parent of -1 marks a node that is not there
+ * (requests with fewer drafts), and so is what follows it.  Any other parent
+ * is a data fault of its request.
+ *
+ * dspk_tree_layout:
+ *   parents   : int32 [b][m_rows - 1];
+ *   cache_len : int32 [b];
+ *   tree_mask : uint64 [b][m_rows] output: a node sees itself and what it
+ *               follows; 0 for nodes that are not there (a fault: all nodes);
+ *   positions : int32 [b][m_rows] output: cache_len plus the node's depth.
+ */
+int dspk_tree_layout(const int32_t *parents, int32_t b, int32_t m_rows, const int32_t *cache_len, uint64_t *tree_mask,
+                     int32_t *positions, void *stream);
+
+/*
+ * Greedy acceptance along a tree: from the anchor, the first node that follows
+ * the last accepted one and drafts the target's token there is accepted,
+ * until none does; as in dspk_accept_greedy one target token always follows.
+ *   target_ids : int32 [b][m_rows], node j's greedy token;
+ *   draft_ids, parents : int32 [b][m_rows - 1];
+ *   accept_len : int32 [b] output, committed tokens (1 .. m_rows; -1 on a fault);
+ *   committed  : int32 [b][m_rows] output: the target's tokens along the path,
+ *                then -1;
+ *   path       : int32 [b][m_rows] output: the accepted nodes, 0 first (as many
+ *                as committed tokens), then -1.
+ * The outputs may be pinned host memory.
+ */
+int dspk_accept_tree_greedy(const int32_t *target_ids, const int32_t *draft_ids, const int32_t *parents, int32_t b,
+                            int32_t m_rows, int32_t *accept_len, int32_t *committed, int32_t *path, void *stream);
+
+/*
+ * After acceptance: in each of `count` caches of one shape (a model's layers;
+ * host array of descriptors) the entry of node path[i] moves to cache position
+ * cache_len + i, for the accepted nodes, so that the next round's cache is
+ * contiguous.  Entries of other nodes past them are left as they are.
+ *   batch      : the round's, without row_start; max_rows = m_rows;
+ *   path, accept_len : of dspk_accept_tree_greedy (device memory);
+ *   new_len    : int32 [b] output, cache_len plus the accepted nodes, or NULL;
+ *                may be cache_len itself.
+ * A request whose path is not one (accept_len < 1, a node out of order) or
+ * whose cache_len plus max_rows runs past the page table is left as it is, and
+ * its length too.
+ */
+int dspk_kv_commit(int32_t count, const dspk_kv_cache *caches, const dspk_attn_batch *batch, const int32_t *path,
+                   const int32_t *accept_len, int32_t *new_len, void *stream);
 
 /*
  * Draft-cap policy (host code; no GPU, no workspace).

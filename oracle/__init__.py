@@ -10,3 +10,4 @@ from .dspk_oracle import (  # noqa: F401
     expected_committed, choose_cap, CapController,
     penalized_logits, truncate, accept_sample_filtered,
 )
+from . import attention  # noqa: F401,E402

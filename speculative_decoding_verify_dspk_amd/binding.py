@@ -23,6 +23,7 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 DSPK_F32, DSPK_BF16 = 0, 1
 MAX_ROWS = 32
 MAX_GROUPED = 4
+MAX_TREE = 64
 
 
 class DspkError(RuntimeError):
@@ -48,6 +49,24 @@ class CapControllerDesc(ctypes.Structure):
                 ("n", c_int32), ("decay", ctypes.c_double), ("hits", ctypes.c_double),
                 ("trials", ctypes.c_double), ("probe_every", c_int32), ("probe_cap", c_int32),
                 ("parked_rounds", c_int32)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """dspk_kv_cache: one layer's paged k/v cache."""
+    _fields_ = [("kv_heads", c_int32), ("head_dim", c_int32), ("page_tokens", c_int32), ("bits", c_int32),
+                ("pages", c_int64), ("k", c_void_p), ("v", c_void_p), ("k_scales", c_void_p), ("v_scales", c_void_p)]
+
+
+class AttnBatchDesc(ctypes.Structure):
+    """dspk_attn_batch (host struct)."""
+    _fields_ = [("b", c_int32), ("max_rows", c_int32), ("total_rows", c_int32), ("max_pages", c_int32),
+                ("row_start", c_void_p), ("cache_len", c_void_p), ("page_table", c_void_p)]
+
+
+class QKPrepDesc(ctypes.Structure):
+    """dspk_qk_prep (host struct)."""
+    _fields_ = [("eps", c_float), ("q_weight", c_void_p), ("k_weight", c_void_p), ("inv_freq", c_void_p),
+                ("rotary_dim", c_int32), ("interleaved", c_int32), ("positions", c_void_p)]
 
 
 class SampleParamsDesc(ctypes.Structure):
@@ -114,6 +133,22 @@ def lib() -> ctypes.CDLL:
         "dspk_accept_sample_ex": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int32,
                                             c_int32, P(SampleParamsDesc), c_void_p, c_void_p, c_void_p, c_void_p,
                                             c_size_t, c_void_p]),
+        "dspk_kv_cache_bytes": (c_size_t, [c_int64, c_int32, c_int32, c_int32, c_int32]),
+        "dspk_qkv_norm_rope_append": (c_int32, [P(KVCacheDesc), P(AttnBatchDesc), P(QKPrepDesc), c_void_p, c_int64,
+                                                c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32, c_void_p,
+                                                c_int64, c_void_p]),
+        "dspk_kv_append": (c_int32, [P(KVCacheDesc), P(AttnBatchDesc), c_void_p, c_int64, c_void_p, c_int64, c_int32,
+                                     c_void_p]),
+        "dspk_kv_read": (c_int32, [P(KVCacheDesc), P(AttnBatchDesc), c_void_p, c_int64, c_void_p, c_int64, c_int32,
+                                   c_void_p]),
+        "dspk_attn_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32, c_int32, c_int32]),
+        "dspk_tree_attention": (c_int32, [P(KVCacheDesc), P(AttnBatchDesc), c_void_p, c_int64, c_int32, c_float,
+                                          c_void_p, c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
+        "dspk_tree_layout": (c_int32, [c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "dspk_accept_tree_greedy": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p,
+                                              c_void_p, c_void_p]),
+        "dspk_kv_commit": (c_int32, [c_int32, P(KVCacheDesc), P(AttnBatchDesc), c_void_p, c_void_p, c_void_p,
+                                     c_void_p]),
         "dspk_choose_cap": (c_int32, [P(ctypes.c_double), P(ctypes.c_double), c_int32, ctypes.c_double,
                                       P(ctypes.c_double)]),
         "dspk_cap_init": (c_int32, [P(CapControllerDesc), P(ctypes.c_double), P(ctypes.c_double), c_int32,
@@ -211,6 +246,94 @@ def tiled_bytes(n: int, k: int, bits: int) -> int:
     return lib().dspk_tiled_bytes(n, k, bits)
 
 
+# ------------------------------------------------------- attention, k/v cache
+def kv_cache_bytes(pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, bits: int = 16) -> int:
+    """Bytes of the k pool (and of the v pool); 0 for a shape that is not supported."""
+    return lib().dspk_kv_cache_bytes(pages, kv_heads, head_dim, page_tokens, bits)
+
+
+class KVCache:
+    """One layer's paged k/v cache: the pools (any tensors of the right size
+    and device) and their C descriptor."""
+
+    def __init__(self, k, v, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, bits: int = 16,
+                 k_scales=None, v_scales=None):
+        need = kv_cache_bytes(pages, kv_heads, head_dim, page_tokens, bits)
+        if need == 0:
+            raise DspkError(-2, lib().dspk_last_error().decode())
+        for name, t, size in (("k", k, need), ("v", v, need),
+                              ("k_scales", k_scales, 4 * pages * kv_heads * page_tokens),
+                              ("v_scales", v_scales, 4 * pages * kv_heads * page_tokens)):
+            if t is not None and (not t.is_contiguous() or t.numel() * t.element_size() < size):
+                raise ValueError(f"{name}: expected a contiguous tensor of at least {size} bytes")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.pages, self.kv_heads, self.head_dim = pages, kv_heads, head_dim
+        self.page_tokens, self.bits = page_tokens, bits
+        self.desc = KVCacheDesc(kv_heads, head_dim, page_tokens, bits, pages, _ptr(k), _ptr(v), _ptr(k_scales),
+                                _ptr(v_scales))
+
+    @classmethod
+    def alloc(cls, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, bits: int = 16, device="cuda"):
+        import torch
+        need = kv_cache_bytes(pages, kv_heads, head_dim, page_tokens, bits)
+        if need == 0:
+            raise DspkError(-2, lib().dspk_last_error().decode())
+        pool = lambda: torch.empty(need, dtype=torch.uint8, device=device)
+        scales = lambda: torch.empty((pages, kv_heads, page_tokens), dtype=torch.float32, device=device)
+        return cls(pool(), pool(), pages, kv_heads, head_dim, page_tokens, bits,
+                   *((scales(), scales()) if bits == 8 else (None, None)))
+
+
+def _int32(t, name: str):
+    if t is not None and (t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous int32 tensor")
+    return t
+
+
+class AttnBatch:
+    """The requests of an attention or cache call: cached lengths [b], page
+    table [b][max_pages], and each request's rows (max_rows each, or by
+    row_start [b + 1])."""
+
+    def __init__(self, cache_len, page_table, max_rows: int, total_rows: int | None = None, row_start=None):
+        if page_table.dim() != 2 or page_table.shape[0] != cache_len.shape[0]:
+            raise ValueError("page_table: expected [b][max_pages] with the b of cache_len")
+        b = cache_len.shape[0]
+        if row_start is not None and row_start.numel() != b + 1:
+            raise ValueError("row_start: expected b + 1 entries")
+        if total_rows is None:
+            if row_start is not None:
+                raise ValueError("total_rows is needed with row_start")
+            total_rows = b * max_rows
+        self.total_rows = total_rows
+        self.keep = (_int32(cache_len, "cache_len"), _int32(page_table, "page_table"), _int32(row_start, "row_start"))
+        self.desc = AttnBatchDesc(b, max_rows, total_rows, page_table.shape[1], _ptr(row_start),
+                                  cache_len.data_ptr(), page_table.data_ptr())
+
+
+def _row_array(t, name: str, rows: int):
+    """(address, leading dimension, element type) of rows [>= rows][ld]."""
+    ld = _rows(t, name)
+    if t.shape[0] < rows:
+        raise ValueError(f"{name}: {t.shape[0]} rows, {rows} needed")
+    return t.data_ptr(), ld, DSPK_BF16 if t.element_size() == 2 else DSPK_F32
+
+
+def _columns(t, name: str, need: int) -> None:
+    if t.shape[1] < need:
+        raise ValueError(f"{name}: {t.shape[1]} columns, {need} needed")
+
+
+def _kv_rows(cache: KVCache, batch: AttnBatch, k, v):
+    kp, ldk, dt = _row_array(k, "k", batch.total_rows)
+    vp, ldv, dv = _row_array(v, "v", batch.total_rows)
+    if dt != dv:
+        raise ValueError("k and v: expected one element type")
+    for t, name in ((k, "k"), (v, "v")):
+        _columns(t, name, cache.kv_heads * cache.head_dim)
+    return kp, ldk, vp, ldv, dt
+
+
 # ------------------------------------------------------------ cap policy
 def _doubles(xs):
     return None if xs is None else (ctypes.c_double * len(xs))(*[float(x) for x in xs])
@@ -265,6 +388,11 @@ class Prepared:
                 conv.append(t(a))                # plain int / float -> its C type, once
         self.args = tuple(conv)
         self.keep = args            # descriptors and arrays the pointers refer to
+
+    def holding(self, *objs) -> "Prepared":
+        """Keeps what the descriptors point to alive as long as the call."""
+        self.keep += objs
+        return self
 
     def __call__(self) -> None:
         rc = self.fn(*self.args)
@@ -322,6 +450,86 @@ def prepare_accept_sample_ex(logits, q, draft_ids, uniforms, m_rows: int, v: int
                     _rows(q, "q"), draft_ids.data_ptr(), uniforms.data_ptr(), m_rows, v, ctypes.byref(params),
                     _ptr(counts), accept_len.data_ptr(), committed.data_ptr(), workspace.data_ptr(),
                     workspace.numel(), _stream(stream))
+
+
+def prepare_qkv_norm_rope_append(cache: KVCache, batch: AttnBatch, q, k, v, q_heads: int, q_out, q_weight=None,
+                                 k_weight=None, eps: float = 1e-6, inv_freq=None, rotary_dim: int | None = None,
+                                 interleaved: bool = False, positions=None, stream=None) -> Prepared:
+    """q/k norm, rotation and the k/v store of a layer; weights and inv_freq
+    are float32, rotary_dim defaults to 2 * len(inv_freq)."""
+    kp, ldk, vp, ldv, dt = _kv_rows(cache, batch, k, v)
+    qp, ldq, dq = _row_array(q, "q", batch.total_rows)
+    op, ldo, do = _row_array(q_out, "q_out", batch.total_rows)
+    if dq != dt or do != DSPK_BF16:
+        raise ValueError("q, k and v: expected one element type; q_out: bf16")
+    for t, name in ((q, "q"), (q_out, "q_out")):
+        _columns(t, name, q_heads * cache.head_dim)
+    for t, name, n in ((q_weight, "q_weight", cache.head_dim), (k_weight, "k_weight", cache.head_dim),
+                       (inv_freq, "inv_freq", 1 if rotary_dim is None else rotary_dim // 2)):
+        if t is not None and (t.element_size() != 4 or not t.is_floating_point() or not t.is_contiguous()
+                              or t.numel() < n):
+            raise ValueError(f"{name}: expected a contiguous float32 tensor of at least {n} entries")
+    if positions is not None and positions.numel() < batch.total_rows:
+        raise ValueError(f"positions: {batch.total_rows} entries needed")
+    if rotary_dim is None:
+        rotary_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+    prep = QKPrepDesc(float(eps), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), rotary_dim, int(interleaved),
+                      _ptr(_int32(positions, "positions")))
+    return Prepared("dspk_qkv_norm_rope_append", ctypes.byref(cache.desc), ctypes.byref(batch.desc),
+                    ctypes.byref(prep), qp, ldq, kp, ldk, vp, ldv, dt, q_heads, op, ldo,
+                    _stream(stream)).holding(cache, batch, q, k, v, q_out, q_weight, k_weight, inv_freq, positions)
+
+
+def prepare_kv_append(cache: KVCache, batch: AttnBatch, k, v, stream=None) -> Prepared:
+    kp, ldk, vp, ldv, dt = _kv_rows(cache, batch, k, v)
+    return Prepared("dspk_kv_append", ctypes.byref(cache.desc), ctypes.byref(batch.desc), kp, ldk, vp, ldv, dt,
+                    _stream(stream)).holding(cache, batch, k, v)
+
+
+def prepare_kv_read(cache: KVCache, batch: AttnBatch, k, v, stream=None) -> Prepared:
+    kp, ldk, vp, ldv, dt = _kv_rows(cache, batch, k, v)
+    return Prepared("dspk_kv_read", ctypes.byref(cache.desc), ctypes.byref(batch.desc), kp, ldk, vp, ldv, dt,
+                    _stream(stream)).holding(cache, batch, k, v)
+
+
+def prepare_tree_attention(cache: KVCache, batch: AttnBatch, q, q_heads: int, out, workspace, scale=None,
+                           tree_mask=None, stream=None) -> Prepared:
+    """scale defaults to 1 / sqrt(head_dim); tree_mask: int64 / uint64 bits [total_rows], None for a chain."""
+    qp, ldq, dq = _row_array(q, "q", batch.total_rows)
+    op, ldo, do = _row_array(out, "out", batch.total_rows)
+    if dq != DSPK_BF16 or do != DSPK_BF16:
+        raise ValueError("q and out: expected bf16 (2-byte elements)")
+    for t, name in ((q, "q"), (out, "out")):
+        _columns(t, name, q_heads * cache.head_dim)
+    if tree_mask is not None and (tree_mask.element_size() != 8 or not tree_mask.is_contiguous()
+                                  or tree_mask.numel() < batch.total_rows):
+        raise ValueError(f"tree_mask: expected a contiguous 64-bit tensor of at least {batch.total_rows} entries")
+    return Prepared("dspk_tree_attention", ctypes.byref(cache.desc), ctypes.byref(batch.desc), qp, ldq, q_heads,
+                    cache.head_dim ** -0.5 if scale is None else float(scale), _ptr(tree_mask), op, ldo,
+                    workspace.data_ptr(), workspace.numel(),
+                    _stream(stream)).holding(cache, batch, q, tree_mask, out, workspace)
+
+
+def prepare_tree_layout(parents, b: int, m_rows: int, cache_len, tree_mask, positions, stream=None) -> Prepared:
+    return Prepared("dspk_tree_layout", _ptr(_int32(parents, "parents")), b, m_rows,
+                    _int32(cache_len, "cache_len").data_ptr(), tree_mask.data_ptr(),
+                    _int32(positions, "positions").data_ptr(),
+                    _stream(stream)).holding(parents, cache_len, tree_mask, positions)
+
+
+def prepare_accept_tree_greedy(target_ids, draft_ids, parents, b: int, m_rows: int, accept_len, committed, path,
+                               stream=None) -> Prepared:
+    return Prepared("dspk_accept_tree_greedy", target_ids.data_ptr(), _ptr(draft_ids), _ptr(parents), b, m_rows,
+                    accept_len.data_ptr(), committed.data_ptr(), path.data_ptr(),
+                    _stream(stream)).holding(target_ids, draft_ids, parents, accept_len, committed, path)
+
+
+def prepare_kv_commit(caches: list, batch: AttnBatch, path, accept_len, new_len=None, stream=None) -> Prepared:
+    descs = (KVCacheDesc * len(caches))(*[c.desc for c in caches])
+    return Prepared("dspk_kv_commit", len(caches), descs, ctypes.byref(batch.desc),
+                    _int32(path, "path").data_ptr(), _int32(accept_len, "accept_len").data_ptr(),
+                    _ptr(_int32(new_len, "new_len")),
+                    _stream(stream)).holding(caches, batch, path, accept_len, new_len)
 
 
 # ------------------------------------------------------------ entry points
@@ -456,3 +664,38 @@ def accept_sample_ex(logits, q, draft_ids, uniforms, m_rows: int, v: int, params
                                        draft_ids.data_ptr(), uniforms.data_ptr(), m_rows, v, ctypes.byref(params),
                                        _ptr(counts), accept_len.data_ptr(), committed.data_ptr(), _ptr(workspace),
                                        0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+def attn_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, b: int, max_rows: int) -> int:
+    return lib().dspk_attn_workspace_bytes(q_heads, kv_heads, head_dim, b, max_rows)
+
+
+def qkv_norm_rope_append(cache: KVCache, batch: AttnBatch, q, k, v, q_heads: int, q_out, **options) -> None:
+    """options as in prepare_qkv_norm_rope_append."""
+    prepare_qkv_norm_rope_append(cache, batch, q, k, v, q_heads, q_out, **options)()
+
+
+def kv_append(cache: KVCache, batch: AttnBatch, k, v, stream=None) -> None:
+    prepare_kv_append(cache, batch, k, v, stream)()
+
+
+def kv_read(cache: KVCache, batch: AttnBatch, k, v, stream=None) -> None:
+    prepare_kv_read(cache, batch, k, v, stream)()
+
+
+def tree_attention(cache: KVCache, batch: AttnBatch, q, q_heads: int, out, workspace, scale=None, tree_mask=None,
+                   stream=None) -> None:
+    prepare_tree_attention(cache, batch, q, q_heads, out, workspace, scale, tree_mask, stream)()
+
+
+def tree_layout(parents, b: int, m_rows: int, cache_len, tree_mask, positions, stream=None) -> None:
+    prepare_tree_layout(parents, b, m_rows, cache_len, tree_mask, positions, stream)()
+
+
+def accept_tree_greedy(target_ids, draft_ids, parents, b: int, m_rows: int, accept_len, committed, path,
+                       stream=None) -> None:
+    prepare_accept_tree_greedy(target_ids, draft_ids, parents, b, m_rows, accept_len, committed, path, stream)()
+
+
+def kv_commit(caches: list, batch: AttnBatch, path, accept_len, new_len=None, stream=None) -> None:
+    prepare_kv_commit(caches, batch, path, accept_len, new_len, stream)()

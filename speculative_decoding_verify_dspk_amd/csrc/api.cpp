@@ -154,9 +154,17 @@ int qgemm_common(int32_t count, const dspk_tiled_weight *w, const uint16_t *x, i
 
 }  // namespace
 
+namespace dspk {
+// for the ABI's other source files (attn_api.cpp), which share the message
+int set_error(int code, const char *msg) {
+    g_err = msg;
+    return code;
+}
+}  // namespace dspk
+
 extern "C" {
 
-int dspk_version(void) { return 300; }
+int dspk_version(void) { return 400; }
 
 int dspk_set_projection_variant(int32_t variant) {
     const int prev = dspk::set_projection_variant(variant);

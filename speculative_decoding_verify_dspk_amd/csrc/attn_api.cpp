@@ -1,0 +1,383 @@
+// C ABI of the attention side of the pass: argument checks, launch plans and
+// launches.  As in the rest of the ABI, everything the host can see is checked
+// before anything is enqueued; nothing here allocates, frees or synchronises.
+#include <math.h>
+#include <stdarg.h>
+#include <stdio.h>
+
+#include "../../include/dspk.h"
+#include "attn_internal.h"
+#include "dspk_internal.h"
+
+namespace dspk {
+
+AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t bits, int32_t b, int32_t max_rows,
+                   int64_t capacity, int cus) {
+    AttnPlan p;
+    const int64_t rows = (int64_t)max_rows * (q_heads / kv_heads);    // rows over one k/v head
+    const int64_t tiles = (rows + 15) / 16;
+    // A wave holds up to 4 row tiles (2 of 256 dimensions): their q and
+    // outputs are what its registers can keep.  More rows go to further waves
+    // of the workgroup, which read the same k and v from its caches; beyond
+    // four row groups the rows are cut into blocks that read them again.
+    const int most = d == 256 ? 2 : 4;
+    p.rg = tiles <= most ? 1 : tiles <= 2 * most ? 2 : 4;
+    p.rt = (int)((tiles + p.rg - 1) / p.rg);
+    if (p.rt > most) p.rt = most;
+    if (p.rt == 3 && p.rg != 2) p.rt = 4;                             // instances: 1, 2, 4 tiles, and 3 in two groups
+    if (p.rg > 1 && p.rt < 3) p.rt = d == 256 ? 2 : 3;
+    const int br = 16 * p.rt * p.rg;
+    p.blocks = (int32_t)((rows + br - 1) / br);
+    p.unit = (bits == 8 ? 64 : 32) * (4 / p.rg);
+    const int64_t per_seg = capacity < 1 ? 1 : (capacity + p.unit - 1) / p.unit;
+    const int64_t segs = (int64_t)b * kv_heads * p.blocks;
+    const int64_t most_wg = (int64_t)cus * attn_occ(d, p.rt);
+    // segs < 2^31 / per_seg, without the product overflowing
+    p.fits = segs <= INT32_MAX / per_seg && segs * p.rg * p.rt * (d / 32) <= INT32_MAX;
+    const int64_t units = p.fits ? segs * per_seg : most_wg;
+    p.grid = (int32_t)(units < most_wg ? units : most_wg);
+    p.split = per_seg > 1;
+    const size_t slots = (size_t)most_wg * 2 * p.rg * p.rt;           // 16-row tiles of partial sums
+    p.off_ml = slots * d * 16 * sizeof(float);
+    p.ws_bytes = (p.off_ml + slots * 32 * sizeof(float) + 255) / 256 * 256;
+    return p;
+}
+
+}  // namespace dspk
+
+namespace {
+
+int fail(int code, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return dspk::set_error(code, buf);
+}
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+int launch_result(hipError_t e, const char *who) {
+    if (e != hipSuccess) return fail(DSPK_EDEVICE, "%s: launch failed: %s", who, hipGetErrorString(e));
+    return dspk::set_error(DSPK_OK, "");
+}
+
+bool pointer(const void *p, size_t a) { return p != nullptr && aligned(p, a); }
+
+int check_dim(int32_t d, const char *who) {
+    if (d != 64 && d != 128 && d != 256)
+        return fail(DSPK_EUNSUPPORTED, "%s: head_dim=%d (supported: 64, 128, 256)", who, d);
+    return DSPK_OK;
+}
+
+// The format of a cache; its pointers are checked where they are used.
+int check_format(const dspk_kv_cache *c, dspk::KvCache &out, const char *who) {
+    if (c == nullptr) return fail(DSPK_EINVAL, "%s: cache descriptor is NULL", who);
+    if (c->bits != 8 && c->bits != 16) return fail(DSPK_EUNSUPPORTED, "%s: cache bits=%d (supported: 8, 16)", who, c->bits);
+    int rc = check_dim(c->head_dim, who);
+    if (rc) return rc;
+    if (c->kv_heads < 1 || c->kv_heads > 65535) return fail(DSPK_EINVAL, "%s: kv_heads=%d out of 1..65535", who, c->kv_heads);
+    const int32_t pt = c->page_tokens;
+    if (pt < dspk::kBlockTokens || pt > 65536 || (pt & (pt - 1)))
+        return fail(DSPK_EUNSUPPORTED, "%s: page_tokens=%d (supported: powers of two, 64..65536)", who, pt);
+    if (c->pages < 1 || c->pages > INT32_MAX) return fail(DSPK_EINVAL, "%s: pages=%lld out of 1..2^31-1", who, (long long)c->pages);
+    out.heads = c->kv_heads;
+    out.d = c->head_dim;
+    out.bits = c->bits;
+    out.page_shift = 0;
+    while ((1 << out.page_shift) < pt) ++out.page_shift;
+    out.pages = c->pages;
+    return DSPK_OK;
+}
+
+int check_pools(const dspk_kv_cache *c, const char *who) {
+    if (!pointer(c->k, 256) || !pointer(c->v, 256))
+        return fail(DSPK_EINVAL, "%s: cache k and v must be non-NULL 256-byte aligned device pointers", who);
+    if (c->bits == 8 && (!pointer(c->k_scales, 16) || !pointer(c->v_scales, 16)))
+        return fail(DSPK_EINVAL, "%s: an 8-bit cache needs 16-byte aligned k_scales and v_scales", who);
+    if (c->bits == 16 && (c->k_scales != nullptr || c->v_scales != nullptr))
+        return fail(DSPK_EINVAL, "%s: a bf16 cache takes no scales", who);
+    return DSPK_OK;
+}
+
+int check_cache(const dspk_kv_cache *c, dspk::KvCache &out, const char *who) {
+    int rc = check_format(c, out, who);
+    if (rc) return rc;
+    rc = check_pools(c, who);
+    if (rc) return rc;
+    out.k = c->k;
+    out.v = c->v;
+    out.ks = c->k_scales;
+    out.vs = c->v_scales;
+    return DSPK_OK;
+}
+
+int check_batch(const dspk_attn_batch *B, dspk::AttnBatch &out, const char *who) {
+    if (B == nullptr) return fail(DSPK_EINVAL, "%s: batch descriptor is NULL", who);
+    if (B->b < 1 || B->b > 65535) return fail(DSPK_EINVAL, "%s: b=%d out of 1..65535", who, B->b);
+    if (B->max_rows < 1) return fail(DSPK_EINVAL, "%s: max_rows=%d must be >= 1", who, B->max_rows);
+    if (B->max_pages < 1) return fail(DSPK_EINVAL, "%s: max_pages=%d must be >= 1", who, B->max_pages);
+    if (B->total_rows < 0 || (B->row_start == nullptr && (int64_t)B->b * B->max_rows > B->total_rows))
+        return fail(DSPK_EINVAL, "%s: total_rows=%d holds fewer than b x max_rows rows", who, B->total_rows);
+    if (!pointer(B->cache_len, 4) || !pointer(B->page_table, 4) || !aligned(B->row_start, 4))
+        return fail(DSPK_EINVAL, "%s: cache_len or page_table NULL, or an array misaligned", who);
+    out.b = B->b;
+    out.max_rows = B->max_rows;
+    out.total_rows = B->total_rows;
+    out.max_pages = B->max_pages;
+    out.row_start = B->row_start;
+    out.cache_len = B->cache_len;
+    out.page_table = B->page_table;
+    return DSPK_OK;
+}
+
+// Row arrays [rows][ld]: 16-byte aligned rows of at least heads * d elements.
+int check_rows(const void *p, int64_t ld, int32_t heads, int32_t d, int32_t dtype, const char *name, const char *who) {
+    if (dtype != DSPK_F32 && dtype != DSPK_BF16) return fail(DSPK_EINVAL, "%s: bad element type %d", who, dtype);
+    const int64_t per = dtype == DSPK_F32 ? 4 : 8;
+    if (!pointer(p, 16)) return fail(DSPK_EINVAL, "%s: %s must be a non-NULL 16-byte aligned device pointer", who, name);
+    if (ld < (int64_t)heads * d || ld % per)
+        return fail(DSPK_EINVAL, "%s: leading dimension %lld of %s must be >= %lld and a multiple of %lld", who,
+                    (long long)ld, name, (long long)heads * d, (long long)per);
+    return DSPK_OK;
+}
+
+// Workgroups of a launch over (request, 64-position block, head), and one
+// per row besides.
+int check_grid(const dspk::AttnBatch &B, int32_t heads, int64_t per_row, const char *who) {
+    const int64_t nb = ((int64_t)B.max_rows + dspk::kBlockTokens - 2) / dspk::kBlockTokens + 1;
+    const int64_t per_request = nb * heads;
+    if (per_request > INT32_MAX / B.b || per_request * B.b + B.total_rows * per_row > INT32_MAX)
+        return fail(DSPK_EUNSUPPORTED, "%s: too many rows for one launch", who);
+    return DSPK_OK;
+}
+
+int append_common(const char *who, const dspk_kv_cache *cache, const dspk_attn_batch *batch, dspk::AppendArgs &A,
+                  const void *k, int64_t ldk, const void *v, int64_t ldv, int32_t dtype, void *stream) {
+    int rc = check_cache(cache, A.c, who);
+    if (rc) return rc;
+    rc = check_batch(batch, A.B, who);
+    if (rc) return rc;
+    rc = check_rows(k, ldk, A.c.heads, A.c.d, dtype, "k", who);
+    if (rc) return rc;
+    rc = check_rows(v, ldv, A.c.heads, A.c.d, dtype, "v", who);
+    if (rc) return rc;
+    // passes of 256 * 8 / d heads over a row's q heads, at most one workgroup each
+    const int64_t slices = A.q == nullptr ? 0 : ((int64_t)A.q_heads * A.c.d + 2047) / 2048;
+    rc = check_grid(A.B, A.c.heads, slices, who);
+    if (rc) return rc;
+    A.k = k;
+    A.v = v;
+    A.ldk = ldk;
+    A.ldv = ldv;
+    A.f32 = dtype == DSPK_F32;
+    return launch_result(dspk::launch_append(A, (hipStream_t)stream), who);
+}
+
+int check_tree(int32_t b, int32_t m_rows, const int32_t *parents, const char *who) {
+    if (b < 1) return fail(DSPK_EINVAL, "%s: b=%d must be >= 1", who, b);
+    if (m_rows < 1 || m_rows > DSPK_MAX_TREE)
+        return fail(DSPK_EINVAL, "%s: m_rows=%d out of 1..%d", who, m_rows, DSPK_MAX_TREE);
+    if (m_rows > 1 && !pointer(parents, 4)) return fail(DSPK_EINVAL, "%s: parents NULL or misaligned", who);
+    return DSPK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dspk_kv_cache_bytes(int64_t pages, int32_t kv_heads, int32_t head_dim, int32_t page_tokens, int32_t bits) {
+    dspk_kv_cache c = {kv_heads, head_dim, page_tokens, bits, pages, nullptr, nullptr, nullptr, nullptr};
+    dspk::KvCache out;
+    if (check_format(&c, out, "dspk_kv_cache_bytes")) return 0;
+    const size_t positions = (size_t)pages * kv_heads, row = (size_t)page_tokens * head_dim * (bits / 8);
+    return positions > SIZE_MAX / row ? 0 : positions * row;
+}
+
+int dspk_qkv_norm_rope_append(const dspk_kv_cache *cache, const dspk_attn_batch *batch, const dspk_qk_prep *prep,
+                              const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                              int32_t dtype, int32_t q_heads, uint16_t *q_out, int64_t ldqo, void *stream) {
+    const char *who = "dspk_qkv_norm_rope_append";
+    if (prep == nullptr) return fail(DSPK_EINVAL, "%s: prep is NULL", who);
+    if (cache == nullptr) return fail(DSPK_EINVAL, "%s: cache descriptor is NULL", who);
+    int rc = check_dim(cache->head_dim, who);
+    if (rc) return rc;
+    const int32_t d = cache->head_dim;
+    if (q_heads < 1 || q_heads > 65535) return fail(DSPK_EINVAL, "%s: q_heads=%d out of 1..65535", who, q_heads);
+    rc = check_rows(q, ldq, q_heads, d, dtype, "q", who);
+    if (rc) return rc;
+    rc = check_rows(q_out, ldqo, q_heads, d, DSPK_BF16, "q_out", who);
+    if (rc) return rc;
+    if (!aligned(prep->q_weight, 16) || !aligned(prep->k_weight, 16))
+        return fail(DSPK_EINVAL, "%s: norm weights must be 16-byte aligned", who);
+    if ((prep->q_weight != nullptr || prep->k_weight != nullptr) && !(prep->eps >= 0.f && isfinite(prep->eps)))
+        return fail(DSPK_EINVAL, "%s: eps must be finite and >= 0", who);
+    if (prep->inv_freq != nullptr) {
+        if (!aligned(prep->inv_freq, 4)) return fail(DSPK_EINVAL, "%s: inv_freq misaligned", who);
+        if (prep->rotary_dim < 2 || prep->rotary_dim > d || prep->rotary_dim % 2)
+            return fail(DSPK_EINVAL, "%s: rotary_dim=%d out of 2..%d, or odd", who, prep->rotary_dim, d);
+        if (prep->rotary_dim % 16)
+            return fail(DSPK_EUNSUPPORTED, "%s: rotary_dim=%d (supported: multiples of 16)", who, prep->rotary_dim);
+        if (prep->interleaved != 0 && prep->interleaved != 1)
+            return fail(DSPK_EINVAL, "%s: interleaved=%d (0 or 1)", who, prep->interleaved);
+        if (!aligned(prep->positions, 4)) return fail(DSPK_EINVAL, "%s: positions misaligned", who);
+    }
+    dspk::AppendArgs A{};
+    A.q = q;
+    A.ldq = ldq;
+    A.q_heads = q_heads;
+    A.q_out = q_out;
+    A.ldqo = ldqo;
+    A.eps = prep->eps;
+    A.qw = prep->q_weight;
+    A.kw = prep->k_weight;
+    A.inv_freq = prep->inv_freq;
+    A.rot = prep->rotary_dim;
+    A.interleaved = prep->interleaved;
+    A.positions = prep->positions;
+    return append_common(who, cache, batch, A, k, ldk, v, ldv, dtype, stream);
+}
+
+int dspk_kv_append(const dspk_kv_cache *cache, const dspk_attn_batch *batch, const void *k, int64_t ldk, const void *v,
+                   int64_t ldv, int32_t dtype, void *stream) {
+    dspk::AppendArgs A{};
+    return append_common("dspk_kv_append", cache, batch, A, k, ldk, v, ldv, dtype, stream);
+}
+
+int dspk_kv_read(const dspk_kv_cache *cache, const dspk_attn_batch *batch, void *k, int64_t ldk, void *v, int64_t ldv,
+                 int32_t dtype, void *stream) {
+    const char *who = "dspk_kv_read";
+    dspk::ReadArgs A{};
+    int rc = check_cache(cache, A.c, who);
+    if (rc) return rc;
+    rc = check_batch(batch, A.B, who);
+    if (rc) return rc;
+    rc = check_rows(k, ldk, A.c.heads, A.c.d, dtype, "k", who);
+    if (rc) return rc;
+    rc = check_rows(v, ldv, A.c.heads, A.c.d, dtype, "v", who);
+    if (rc) return rc;
+    rc = check_grid(A.B, A.c.heads, 0, who);
+    if (rc) return rc;
+    A.k = k;
+    A.v = v;
+    A.ldk = ldk;
+    A.ldv = ldv;
+    A.f32 = dtype == DSPK_F32;
+    return launch_result(dspk::launch_kv_read(A, (hipStream_t)stream), who);
+}
+
+size_t dspk_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t b, int32_t max_rows) {
+    if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || q_heads > 65535 || b < 1 || max_rows < 1 ||
+        max_rows > DSPK_MAX_TREE || (head_dim != 64 && head_dim != 128 && head_dim != 256))
+        return 0;
+    return dspk::attn_plan(q_heads, kv_heads, head_dim, 16, b, max_rows, 1, dspk::device_cus()).ws_bytes;
+}
+
+int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch, const uint16_t *q, int64_t ldq,
+                        int32_t q_heads, float scale, const uint64_t *tree_mask, uint16_t *out, int64_t ldo,
+                        void *workspace, size_t ws_bytes, void *stream) {
+    const char *who = "dspk_tree_attention";
+    dspk::AttnArgs A{};
+    int rc = check_cache(cache, A.c, who);
+    if (rc) return rc;
+    rc = check_batch(batch, A.B, who);
+    if (rc) return rc;
+    if (A.B.max_rows > DSPK_MAX_TREE)
+        return fail(DSPK_EUNSUPPORTED, "%s: max_rows=%d (at most %d rows of one request)", who, A.B.max_rows,
+                    DSPK_MAX_TREE);
+    if (q_heads < A.c.heads || q_heads % A.c.heads || q_heads > 65535)
+        return fail(DSPK_EINVAL, "%s: q_heads=%d must be a multiple of kv_heads=%d, at most 65535", who, q_heads, A.c.heads);
+    rc = check_rows(q, ldq, q_heads, A.c.d, DSPK_BF16, "q", who);
+    if (rc) return rc;
+    rc = check_rows(out, ldo, q_heads, A.c.d, DSPK_BF16, "out", who);
+    if (rc) return rc;
+    if (!(scale > 0.f) || !isfinite(scale)) return fail(DSPK_EINVAL, "%s: scale must be finite and > 0", who);
+    if (!aligned(tree_mask, 8)) return fail(DSPK_EINVAL, "%s: tree_mask misaligned", who);
+    const dspk::AttnPlan p = dspk::attn_plan(q_heads, A.c.heads, A.c.d, A.c.bits, A.B.b, A.B.max_rows,
+                                             (int64_t)A.B.max_pages << A.c.page_shift, dspk::device_cus());
+    if (!p.fits) return fail(DSPK_EUNSUPPORTED, "%s: page table too large for one launch", who);
+    if (!pointer(workspace, 256) || ws_bytes < p.ws_bytes)
+        return fail(DSPK_EINVAL, "%s: workspace of %zu bytes required (256-byte aligned)", who, p.ws_bytes);
+    A.q = q;
+    A.ldq = ldq;
+    A.out = out;
+    A.ldo = ldo;
+    A.rep = q_heads / A.c.heads;
+    A.scale = scale * 1.44269504088896340736f;
+    A.mask = tree_mask;
+    A.grid = p.grid;
+    A.part = (float *)workspace;
+    A.part_ml = (float *)((char *)workspace + p.off_ml);
+    return launch_result(dspk::launch_tree_attention(A, p, (hipStream_t)stream), who);
+}
+
+int dspk_tree_layout(const int32_t *parents, int32_t b, int32_t m_rows, const int32_t *cache_len, uint64_t *tree_mask,
+                     int32_t *positions, void *stream) {
+    const char *who = "dspk_tree_layout";
+    int rc = check_tree(b, m_rows, parents, who);
+    if (rc) return rc;
+    if (!pointer(cache_len, 4) || !pointer(tree_mask, 8) || !pointer(positions, 4))
+        return fail(DSPK_EINVAL, "%s: cache_len, tree_mask or positions NULL or misaligned", who);
+    return launch_result(
+        dspk::launch_tree_layout(parents, b, m_rows, cache_len, tree_mask, positions, (hipStream_t)stream), who);
+}
+
+int dspk_accept_tree_greedy(const int32_t *target_ids, const int32_t *draft_ids, const int32_t *parents, int32_t b,
+                            int32_t m_rows, int32_t *accept_len, int32_t *committed, int32_t *path, void *stream) {
+    const char *who = "dspk_accept_tree_greedy";
+    int rc = check_tree(b, m_rows, parents, who);
+    if (rc) return rc;
+    if (!pointer(target_ids, 4) || !pointer(accept_len, 4) || !pointer(committed, 4) || !pointer(path, 4))
+        return fail(DSPK_EINVAL, "%s: target_ids, accept_len, committed or path NULL or misaligned", who);
+    if (m_rows > 1 && !pointer(draft_ids, 4)) return fail(DSPK_EINVAL, "%s: draft_ids NULL or misaligned", who);
+    return launch_result(dspk::launch_accept_tree(target_ids, draft_ids, parents, b, m_rows, accept_len, committed, path,
+                                                  (hipStream_t)stream),
+                         who);
+}
+
+int dspk_kv_commit(int32_t count, const dspk_kv_cache *caches, const dspk_attn_batch *batch, const int32_t *path,
+                   const int32_t *accept_len, int32_t *new_len, void *stream) {
+    const char *who = "dspk_kv_commit";
+    if (count < 1 || caches == nullptr) return fail(DSPK_EINVAL, "%s: count=%d caches, or NULL", who, count);
+    dspk::CommitArgs A{};
+    for (int32_t i = 0; i < count; ++i) {
+        dspk::KvCache c;
+        int rc = check_cache(&caches[i], c, who);
+        if (rc) return rc;
+        if (i == 0) A.c = c;
+        if (c.heads != A.c.heads || c.d != A.c.d || c.bits != A.c.bits || c.page_shift != A.c.page_shift ||
+            c.pages != A.c.pages)
+            return fail(DSPK_EINVAL, "%s: caches of one call must have the same shape", who);
+    }
+    int rc = check_batch(batch, A.B, who);
+    if (rc) return rc;
+    if (A.B.row_start != nullptr || A.B.max_rows > DSPK_MAX_TREE)
+        return fail(DSPK_EUNSUPPORTED, "%s: every request has max_rows nodes, at most %d (row_start must be NULL)", who,
+                    DSPK_MAX_TREE);
+    if (!pointer(path, 4) || !pointer(accept_len, 4) || !aligned(new_len, 4))
+        return fail(DSPK_EINVAL, "%s: path or accept_len NULL, or an array misaligned", who);
+    if (new_len != nullptr && new_len != A.B.cache_len && new_len < A.B.cache_len + A.B.b &&
+        A.B.cache_len < new_len + A.B.b)
+        return fail(DSPK_EINVAL, "%s: new_len overlaps cache_len without being it", who);
+    A.path = path;
+    A.accept_len = accept_len;
+    // a new_len that is cache_len is written by a launch of its own, after
+    // every workgroup has read the old lengths
+    const bool in_place = new_len == A.B.cache_len;
+    for (int32_t i = 0; i < count; i += dspk::kMaxCaches) {
+        A.count = count - i < dspk::kMaxCaches ? count - i : dspk::kMaxCaches;
+        for (int32_t j = 0; j < A.count; ++j)
+            A.caches[j] = {caches[i + j].k, caches[i + j].v, caches[i + j].k_scales, caches[i + j].v_scales};
+        A.new_len = i == 0 && !in_place ? new_len : nullptr;
+        const hipError_t e = dspk::launch_kv_commit(A, (hipStream_t)stream);
+        if (e != hipSuccess) return launch_result(e, who);
+    }
+    if (in_place) {
+        A.new_len = new_len;
+        return launch_result(dspk::launch_new_len(A, (hipStream_t)stream), who);
+    }
+    return launch_result(hipSuccess, who);
+}
+
+}  // extern "C"

@@ -1,0 +1,114 @@
+// Internal declarations of the attention side of the pass (paged k/v cache,
+// attention over it, tree bookkeeping), shared by its C-ABI layer and kernels.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace dspk {
+
+constexpr int kBlockTokens = 64;    // positions per block of the cache: a page is 2^k blocks
+constexpr int kMaxTree = 64;        // rows of one request in an attention or tree call (one mask bit each)
+constexpr int kMaxCaches = 64;      // caches (layers) of one commit launch
+
+// The paged cache; see the layout at dspk_kv_cache.
+struct KvCache {
+    int32_t heads, d, bits;
+    int32_t page_shift;             // log2 of the positions per page
+    int64_t pages;
+    void *k, *v;
+    float *ks, *vs;                 // 8-bit caches
+};
+
+// The requests of a call; see dspk_attn_batch.
+struct AttnBatch {
+    int32_t b, max_rows, total_rows, max_pages;
+    const int32_t *row_start, *cache_len, *page_table;
+};
+
+struct AppendArgs {
+    KvCache c;
+    AttnBatch B;
+    const void *q, *k, *v;          // rows [total_rows][ld]; q NULL: none
+    int64_t ldq, ldk, ldv;
+    int32_t q_heads;
+    int32_t f32;                    // rows are fp32, else bf16
+    float eps;
+    const float *qw, *kw;           // norm weights [d], or NULL: no norm
+    const float *inv_freq;          // [rot/2], or NULL: no rotation
+    int32_t rot, interleaved;
+    const int32_t *positions;       // [total_rows], or NULL: cache position
+    uint16_t *q_out;
+    int64_t ldqo;
+};
+hipError_t launch_append(const AppendArgs &a, hipStream_t s);
+
+struct ReadArgs {
+    KvCache c;
+    AttnBatch B;
+    void *k, *v;                    // rows [total_rows][ld]
+    int64_t ldk, ldv;
+    int32_t f32;
+};
+hipError_t launch_kv_read(const ReadArgs &a, hipStream_t s);
+
+struct CachePtrs {
+    void *k, *v;
+    float *ks, *vs;
+};
+struct CommitArgs {
+    KvCache c;                      // geometry (its pointers are unused)
+    AttnBatch B;                    // max_rows: nodes per request
+    const int32_t *path, *accept_len;
+    int32_t *new_len;               // or NULL
+    int32_t count;
+    CachePtrs caches[kMaxCaches];
+};
+hipError_t launch_kv_commit(const CommitArgs &a, hipStream_t s);
+// new_len[r] alone, for a call whose new_len is its cache_len
+hipError_t launch_new_len(const CommitArgs &a, hipStream_t s);
+
+// Shape of an attention launch.  A workgroup's four waves are `rg` row groups
+// of rt 16-row tiles, times 4 / rg token groups; see tree_attn.hip.
+constexpr int attn_occ(int d, int rt) {           // workgroups per CU (registers: q and outputs of rt row tiles)
+    return d == 256 ? 1 : rt * d <= 128 ? 3 : rt * d <= 256 ? 2 : 1;
+}
+struct AttnPlan {
+    int32_t rt, rg;
+    int32_t unit;                   // tokens of one step of a workgroup
+    int32_t blocks;                 // row blocks of a request of max_rows rows
+    int32_t grid;                   // workgroups of the streaming kernel
+    bool fits;                      // its unit numbers fit 31 bits
+    bool split;                     // a segment may be shared between workgroups
+    size_t off_ml, ws_bytes;
+};
+AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t bits, int32_t b, int32_t max_rows,
+                   int64_t capacity, int cus);
+// workspace for any cache format and capacity
+size_t attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t b, int32_t max_rows, int cus);
+
+struct AttnArgs {
+    KvCache c;
+    AttnBatch B;
+    const uint16_t *q;
+    uint16_t *out;
+    int64_t ldq, ldo;
+    int32_t rep;                    // q heads per kv head
+    float scale;                    // of the scores, times log2(e)
+    const uint64_t *mask;           // [total_rows], or NULL: a chain
+    int32_t grid;                   // of the streaming kernel
+    float *part;                    // partial outputs
+    float *part_ml;                 // their row maxima and sums
+};
+hipError_t launch_tree_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s);
+
+hipError_t launch_tree_layout(const int32_t *parents, int32_t b, int32_t m, const int32_t *cache_len, uint64_t *mask,
+                              int32_t *positions, hipStream_t s);
+hipError_t launch_accept_tree(const int32_t *target, const int32_t *draft, const int32_t *parents, int32_t b, int32_t m,
+                              int32_t *accept_len, int32_t *committed, int32_t *path, hipStream_t s);
+
+// Stores the thread's error message (dspk_last_error) and returns `code`.
+int set_error(int code, const char *msg);
+
+}  // namespace dspk

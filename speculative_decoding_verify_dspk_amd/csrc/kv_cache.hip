@@ -1,0 +1,472 @@
+// Rows into the paged cache and out of it:
+//   append_kernel   q/k/v rows of the projections -> RMS norm of each q and k
+//                   head, rotation by position, q rows out, k/v rows into the
+//                   cache (8-bit caches: codes and one scale per position and
+//                   head), in one launch;
+//   kv_read_kernel  cache entries -> rows;
+//   kv_commit_kernel  the entries of a tree's accepted path moved together.
+//
+// The cache keeps k and v in the order the matrix cores take them
+// (kv_layout.h), so v's positions lie next to each other: a workgroup takes
+// the rows of one 64-position block of one request and head and turns v
+// through LDS, so that whole 16-byte pieces are written wherever the rows
+// fill them.  Everything here is bound by memory traffic (prompts) or by the
+// latency of one load-compute-store chain (verify rows).
+#include <hip/hip_runtime.h>
+
+#include "kv_layout.h"
+
+namespace dspk {
+namespace {
+
+using kv::u32x4;
+using kv::f32x4;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int TPB = 256;
+
+// Eight lanes' worth of geometry: a head's row is held by D / 8 lanes, eight
+// neighbouring dimensions each.
+template <int D>
+struct Geo {
+    static constexpr int L = D / 8;          // lanes per row
+    static constexpr int R = TPB / L;        // rows of a workgroup pass
+};
+
+template <bool F32>
+__device__ __forceinline__ void load8(const void *p, int64_t i, float (&x)[8]) {
+    if constexpr (F32) {
+        const f32x4 a = *(const f32x4 *)((const float *)p + i), b = *(const f32x4 *)((const float *)p + i + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = a[e], x[e + 4] = b[e];
+    } else {
+        const u32x4 a = *(const u32x4 *)((const uint16_t *)p + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(a[e] << 16);
+            x[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {      // round to nearest even
+    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
+}
+__device__ __forceinline__ u32x4 bf16_8(const float (&x)[8]) {
+    u32x4 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = bf16_pair(x[2 * e], x[2 * e + 1]);
+    return r;
+}
+
+// x * rsqrt(mean(x^2) + eps) * w over a head's row, the sum in fp32.
+template <int D>
+__device__ __forceinline__ void norm8(float (&x)[8], const float *w, float eps, int oct) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += x[e] * x[e];
+#pragma unroll
+    for (int o = 1; o < Geo<D>::L; o <<= 1) s += __shfl_xor(s, o);
+    const float f = rsqrtf(s * (1.f / D) + eps);
+    const f32x4 a = *(const f32x4 *)(w + oct * 8), b = *(const f32x4 *)(w + oct * 8 + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] *= f * a[e], x[e + 4] *= f * b[e];
+}
+
+// cos and sin of position * freq.  The angle's turns are counted in fp64 and
+// only their fraction is rounded to fp32: at position 10^6 an fp32 product
+// would be off by 0.06 radians.
+__device__ __forceinline__ void turn(int32_t position, float freq, float &c, float &s) {
+    const double rev = (double)position * (double)freq * 0.15915494309189533577;
+    sincospif((float)(2.0 * (rev - rint(rev))), &s, &c);
+}
+
+// Rotation of a head's row; cs points to the row's cosines, sn to its sines.
+// All lanes of the wave take part (the pair's other half comes from another
+// lane unless pairs are neighbours).
+template <int D>
+__device__ __forceinline__ void rotate8(float (&x)[8], int oct, int rot, int interleaved, const float *cs,
+                                        const float *sn) {
+    const int d0 = oct * 8, h = rot / 2;
+    if (interleaved) {
+        if (d0 >= rot) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float c = cs[d0 / 2 + e], s = sn[d0 / 2 + e], a = x[2 * e], b = x[2 * e + 1];
+            x[2 * e] = a * c - b * s;
+            x[2 * e + 1] = b * c + a * s;
+        }
+        return;
+    }
+    const bool first = d0 < h, in = d0 < rot;      // h is a multiple of 8
+    const int src = (threadIdx.x & 63) + (!in ? 0 : first ? h / 8 : -h / 8);
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = __shfl(x[e], src);
+    if (!in) return;
+    const int f = first ? d0 : d0 - h;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * cs[f + e] + (first ? -p[e] : p[e]) * sn[f + e];
+}
+
+// A head's row as 8-bit codes: scale = max|x| / 127, code = round(x * 127 /
+// max|x|), half to even.  A row with a value that is not finite has scale NaN
+// (every value reads back as NaN); one below 4e-37, whose 127 / max|x|
+// would overflow, reads back as zeros.
+template <int D>
+__device__ __forceinline__ u32x2 codes8(const float (&x)[8], float &scale) {
+    uint32_t top = 0;                              // bit patterns of magnitudes order like them, NaN on top
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 1; o < Geo<D>::L; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    const float t = __uint_as_float(top), inv = 127.f / t;
+    const bool held = top < 0x7f800000u && inv < __uint_as_float(0x7f800000u);
+    scale = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : held ? t / 127.f : 0.f;
+    u32x2 r = {0u, 0u};
+    if (held) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = (int)fminf(fmaxf(rintf(x[e] * inv), -127.f), 127.f);
+            r[e / 4] |= (uint32_t)(c & 0xff) << (8 * (e % 4));
+        }
+    }
+    return r;
+}
+
+// The rows of request q that lie in block tb of its touched blocks: positions
+// base + lo .. base + hi - 1.  Returns the chunk index page * heads + head, or
+// -1 where there are no rows or the page is none of the cache's.
+struct Span {
+    int32_t base, lo, hi;
+};
+__device__ __forceinline__ Span span(const kv::Req &q, int tb) {
+    Span s;
+    s.base = (q.len / kBlockTokens + tb) * kBlockTokens;
+    s.lo = max(q.len - s.base, 0);
+    s.hi = min(q.len + q.rows - s.base, kBlockTokens);
+    return s;
+}
+__device__ __forceinline__ int64_t page_of(const KvCache &c, const AttnBatch &B, int r, int32_t position) {
+    const int64_t p = B.page_table[(int64_t)r * B.max_pages + (position >> c.page_shift)];
+    return p >= 0 && p < c.pages ? p : -1;
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ int64_t chunk_elems(const KvCache &c) {
+    return (int64_t)D << c.page_shift;
+}
+
+template <int D, int BITS, bool F32>
+__global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const int kv_blocks, const int nb,
+                                                     const int slices) {
+    constexpr int L = Geo<D>::L, R = Geo<D>::R, W = BITS == 16 ? 8 : 16;
+    typedef typename std::conditional<BITS == 16, uint16_t, uint8_t>::type E;
+    constexpr int VS = D + 16 / (int)sizeof(E);                     // padded row of the turned v
+    __shared__ float s_cs[2][R * D / 2];
+    __shared__ __attribute__((aligned(16))) E s_v[kBlockTokens * VS];
+    const int tid = threadIdx.x, oct = tid % L, slot = tid / L, rot = A.inv_freq != nullptr ? A.rot : 0, h = rot / 2;
+
+    if ((int)blockIdx.x >= kv_blocks) {
+        // ---- one row's q heads, or a slice of them
+        const int row = (blockIdx.x - kv_blocks) / slices, sl = (blockIdx.x - kv_blocks) % slices;
+        int r = 0;
+        if (A.B.row_start == nullptr) {
+            r = row / A.B.max_rows;
+        } else {
+            int hi = A.B.b;                                         // last request that starts at or before the row
+            while (hi - r > 1) {
+                const int mid = (r + hi) / 2;
+                if (A.B.row_start[mid] <= row) r = mid; else hi = mid;
+            }
+        }
+        if (r >= A.B.b) return;
+        const kv::Req q = kv::request(A.B, A.c.page_shift, r);
+        if (row < q.row0 || row >= q.row0 + q.rows) return;         // a row of no request stays as it is
+        const int pos = A.positions != nullptr ? A.positions[row] : q.len + (row - q.row0);
+        if (tid < h) turn(pos, A.inv_freq[tid], s_cs[0][tid], s_cs[1][tid]);
+        __syncthreads();
+        for (int hd = sl * R + slot; hd - slot < A.q_heads; hd += slices * R) {
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            const bool in = hd < A.q_heads;
+            if (in) load8<F32>(A.q, row * A.ldq + hd * D + oct * 8, x);
+            if (A.qw != nullptr) norm8<D>(x, A.qw, A.eps, oct);
+            if (rot) rotate8<D>(x, oct, rot, A.interleaved, s_cs[0], s_cs[1]);
+            if (in) *(u32x4 *)(A.q_out + row * A.ldqo + hd * D + oct * 8) = bf16_8(x);
+        }
+        return;
+    }
+
+    // ---- the k/v rows of one block of one request and head
+    const int head = blockIdx.x % A.c.heads, tb = blockIdx.x / A.c.heads % nb, r = blockIdx.x / A.c.heads / nb;
+    const kv::Req q = kv::request(A.B, A.c.page_shift, r);
+    if (!q.ok) return;
+    const Span sp = span(q, tb);
+    if (sp.lo >= sp.hi) return;
+    const int64_t page = page_of(A.c, A.B, r, sp.base);
+    if (page < 0) return;
+    const int t0 = sp.base & ((1 << A.c.page_shift) - 1);
+    const int64_t chunk = page * A.c.heads + head;
+    E *const kd = (E *)A.c.k + chunk * chunk_elems<D, BITS>(A.c), *const vd = (E *)A.c.v + chunk * chunk_elems<D, BITS>(A.c);
+
+    for (int p0 = sp.lo / R * R; p0 < sp.hi; p0 += R) {
+        const int t = p0 + slot, row = q.row0 + sp.base + t - q.len;
+        const bool in = t >= sp.lo && t < sp.hi;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (in) {
+            load8<F32>(A.k, row * A.ldk + head * D + oct * 8, x);
+            load8<F32>(A.v, row * A.ldv + head * D + oct * 8, y);
+        }
+        if (rot) {
+            __syncthreads();                                        // the previous pass has read its table
+            for (int i = tid; i < R * h; i += TPB) {
+                const int tt = p0 + i / h;
+                if (tt >= sp.lo && tt < sp.hi) {
+                    const int rr = q.row0 + sp.base + tt - q.len;
+                    turn(A.positions != nullptr ? A.positions[rr] : sp.base + tt, A.inv_freq[i % h], s_cs[0][i],
+                         s_cs[1][i]);
+                }
+            }
+            __syncthreads();
+        }
+        if (A.kw != nullptr) norm8<D>(x, A.kw, A.eps, oct);
+        if (rot) rotate8<D>(x, oct, rot, A.interleaved, s_cs[0] + slot * h, s_cs[1] + slot * h);
+        E *const kp = kd + kv::k_piece<D, W>(t0 + t, oct * 8) + (BITS == 8 ? oct % 2 * 8 : 0);
+        if constexpr (BITS == 16) {
+            const u32x4 a = bf16_8(x), b = bf16_8(y);
+            if (in) {
+                *(u32x4 *)kp = a;
+                *(u32x4 *)(s_v + t * VS + oct * 8) = b;
+            }
+        } else {
+            float sk, sv;
+            const u32x2 a = codes8<D>(x, sk), b = codes8<D>(y, sv);
+            if (in) {
+                *(u32x2 *)kp = a;
+                *(u32x2 *)(s_v + t * VS + oct * 8) = b;
+                if (oct == 0) {
+                    const int64_t si = (chunk << A.c.page_shift) + t0 + t;
+                    A.c.ks[si] = sk;
+                    A.c.vs[si] = sv;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < kBlockTokens * D / W; i += TPB) {
+        const int sb = i / (64 * (D / 16)), vb = i / 64 % (D / 16), g = i / 16 % 4, d = vb * 16 + i % 16;
+        const int first = sb * 4 * W + g * 4;                       // the piece's positions: first + 16 jj + i
+        if (first >= sp.hi || first + 4 * W - 16 + 3 < sp.lo) continue;
+        E *const dst = vd + kv::v_elem<D, W>(t0 + first, d);
+        if (first >= sp.lo && first + 4 * W - 16 + 3 < sp.hi) {
+            E e[W];
+#pragma unroll
+            for (int j = 0; j < W; ++j) e[j] = s_v[(first + j / 4 * 16 + j % 4) * VS + d];
+            *(u32x4 *)dst = __builtin_bit_cast(u32x4, e);
+        } else {
+            for (int j = 0; j < W; ++j) {
+                const int t = first + j / 4 * 16 + j % 4;
+                if (t >= sp.lo && t < sp.hi) dst[j] = s_v[t * VS + d];
+            }
+        }
+    }
+}
+
+// Rows q.len .. of the requests, as an append with the same batch wrote them.
+// Rows whose length or page is a fault read back as NaN.
+template <int D, int BITS, bool F32>
+__global__ __launch_bounds__(TPB) void kv_read_kernel(const ReadArgs A, const int nb) {
+    constexpr int W = BITS == 16 ? 8 : 16;
+    typedef typename std::conditional<BITS == 16, uint16_t, uint8_t>::type E;
+    constexpr int VS = D + 16 / (int)sizeof(E);
+    __shared__ __attribute__((aligned(16))) E s_x[kBlockTokens * VS];
+    const int tid = threadIdx.x;
+    const int head = blockIdx.x % A.c.heads, tb = blockIdx.x / A.c.heads % nb, r = blockIdx.x / A.c.heads / nb;
+    kv::Req q = kv::request(A.B, A.c.page_shift, r);
+    if (!q.ok) q.len = 0;                                           // only for numbering the rows
+    const Span sp = span(q, tb);
+    if (sp.lo >= sp.hi) return;
+    const int64_t page = q.ok ? page_of(A.c, A.B, r, sp.base) : -1;
+    const int t0 = sp.base & ((1 << A.c.page_shift) - 1);
+    const int64_t chunk = page * A.c.heads + head;
+    for (int which = 0; which < 2; ++which) {
+        if (page >= 0) {
+            if (which) __syncthreads();                             // k's rows have left the buffer
+            const E *const src = (const E *)(which ? A.c.v : A.c.k) + chunk * chunk_elems<D, BITS>(A.c);
+            for (int i = tid; i < kBlockTokens * D / W; i += TPB) {
+                if (which == 0) {
+                    const int t = i / (16 * (D / W)) * 16 + i % 16;
+                    const int d = i / 64 % (D / (4 * W)) * 4 * W + i / 16 % 4 * W;
+                    if (t < sp.lo || t >= sp.hi) continue;
+                    *(u32x4 *)(s_x + t * VS + d) = *(const u32x4 *)(src + kv::k_piece<D, W>(t0 + t, d));
+                } else {
+                    const int sb = i / (64 * (D / 16)), vb = i / 64 % (D / 16), g = i / 16 % 4, d = vb * 16 + i % 16;
+                    const int first = sb * 4 * W + g * 4;
+                    if (first >= sp.hi || first + 4 * W - 16 + 3 < sp.lo) continue;
+                    struct { E e[W]; } x = __builtin_bit_cast(decltype(x),
+                                                              *(const u32x4 *)(src + kv::v_elem<D, W>(t0 + first, d)));
+#pragma unroll
+                    for (int j = 0; j < W; ++j) s_x[(first + j / 4 * 16 + j % 4) * VS + d] = x.e[j];
+                }
+            }
+            __syncthreads();
+        }
+        void *const out = which ? A.v : A.k;
+        const int64_t ld = which ? A.ldv : A.ldk;
+        for (int i = tid; i < (sp.hi - sp.lo) * (D / 8); i += TPB) {
+            const int t = sp.lo + i / (D / 8), d = i % (D / 8) * 8;
+            float x[8];
+            if (page < 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(0x7fc00000u);
+            } else if constexpr (BITS == 16) {
+                load8<false>(s_x, t * VS + d, x);
+            } else {
+                const float s = (which ? A.c.vs : A.c.ks)[(chunk << A.c.page_shift) + t0 + t];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = s * (float)(int8_t)s_x[t * VS + d + e];
+            }
+            const int64_t at = (int64_t)(q.row0 + sp.base + t - q.len) * ld + head * D + d;
+            if constexpr (F32) {
+                *(f32x4 *)((float *)out + at) = f32x4{x[0], x[1], x[2], x[3]};
+                *(f32x4 *)((float *)out + at + 4) = f32x4{x[4], x[5], x[6], x[7]};
+            } else {
+                *(u32x4 *)((uint16_t *)out + at) = bf16_8(x);
+            }
+        }
+    }
+}
+
+// A request's path is taken if it starts at the root, rises strictly and
+// stays below the nodes of a request; else nothing is moved and nothing kept.
+__device__ __forceinline__ int kept_nodes(const AttnBatch &B, int page_shift, const int32_t *path,
+                                          const int32_t *accept_len, int r) {
+    const int n = accept_len[r], lane = threadIdx.x & 63;
+    bool bad = n < 1 || n > B.max_rows;
+    if (!bad && lane < n) {
+        const int32_t *p = path + (int64_t)r * B.max_rows;
+        bad = lane == 0 ? p[0] != 0 : p[lane] <= p[lane - 1] || p[lane] >= B.max_rows;
+    }
+    const int32_t len = B.cache_len[r];
+    bad |= len < 0 || (int64_t)len + B.max_rows > ((int64_t)B.max_pages << page_shift);
+    return __any(bad) ? 0 : n;
+}
+
+__global__ __launch_bounds__(64) void new_len_kernel(const AttnBatch B, const int page_shift, const int32_t *path,
+                                                     const int32_t *accept_len, int32_t *new_len) {
+    const int r = blockIdx.x, n = kept_nodes(B, page_shift, path, accept_len, r);
+    if (threadIdx.x == 0) new_len[r] = B.cache_len[r] + n;
+}
+
+// Entry of node path[i] -> place i, for all i of a request, in one head of
+// one cache.  Places are read before any is written (a place may hold a later
+// node of the path).
+template <int D, int BITS>
+__global__ __launch_bounds__(TPB) void kv_commit_kernel(const CommitArgs A) {
+    constexpr int W = BITS == 16 ? 8 : 16;
+    typedef typename std::conditional<BITS == 16, uint16_t, uint8_t>::type E;
+    __shared__ __attribute__((aligned(16))) E s_k[kMaxTree * D];
+    __shared__ E s_v[kMaxTree * D];
+    __shared__ float s_s[2][kMaxTree];
+    __shared__ int64_t s_chunk[2][kMaxTree];                        // source and destination; -1: not moved
+    __shared__ int32_t s_t[2][kMaxTree];
+    const int tid = threadIdx.x, head = blockIdx.x, r = blockIdx.y;
+    const CachePtrs C = A.caches[blockIdx.z];
+    const int n = kept_nodes(A.B, A.c.page_shift, A.path, A.accept_len, r);
+    const int len = A.B.cache_len[r];
+    if (A.new_len != nullptr && head == 0 && blockIdx.z == 0 && tid == 0) A.new_len[r] = len + n;
+    if (n <= 1) return;                                             // the root is in place
+    if (tid < n) {
+        const int from = len + A.path[(int64_t)r * A.B.max_rows + tid], to = len + tid;
+        const int64_t a = from != to ? page_of(A.c, A.B, r, from) : -1, b = page_of(A.c, A.B, r, to);
+        const bool move = a >= 0 && b >= 0;
+        s_chunk[0][tid] = move ? a * A.c.heads + head : -1;
+        s_chunk[1][tid] = b * A.c.heads + head;
+        s_t[0][tid] = from & ((1 << A.c.page_shift) - 1);
+        s_t[1][tid] = to & ((1 << A.c.page_shift) - 1);
+        if (BITS == 8 && move) {
+            s_s[0][tid] = C.ks[(s_chunk[0][tid] << A.c.page_shift) + s_t[0][tid]];
+            s_s[1][tid] = C.vs[(s_chunk[0][tid] << A.c.page_shift) + s_t[0][tid]];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int i = tid; i < n * (D / W); i += TPB) {
+            const int j = i / (D / W), d = i % (D / W) * W;
+            if (s_chunk[0][j] < 0) continue;
+            u32x4 *const p = (u32x4 *)((E *)C.k + s_chunk[pass][j] * chunk_elems<D, BITS>(A.c) +
+                                       kv::k_piece<D, W>(s_t[pass][j], d));
+            if (pass) *p = *(u32x4 *)(s_k + j * D + d); else *(u32x4 *)(s_k + j * D + d) = *p;
+        }
+        for (int i = tid; i < n * D; i += TPB) {
+            const int j = i / D, d = i % D;
+            if (s_chunk[0][j] < 0) continue;
+            E *const p = (E *)C.v + s_chunk[pass][j] * chunk_elems<D, BITS>(A.c) + kv::v_elem<D, W>(s_t[pass][j], d);
+            if (pass) *p = s_v[i]; else s_v[i] = *p;
+        }
+        if (!pass) __syncthreads();
+    }
+    if (BITS == 8 && tid < n && s_chunk[0][tid] >= 0) {
+        C.ks[(s_chunk[1][tid] << A.c.page_shift) + s_t[1][tid]] = s_s[0][tid];
+        C.vs[(s_chunk[1][tid] << A.c.page_shift) + s_t[1][tid]] = s_s[1][tid];
+    }
+}
+
+// Calls f(std::integral_constant<int, D>, <int, BITS>) for the cache's format.
+template <typename F>
+void with_format(const KvCache &c, F f) {
+    using std::integral_constant;
+    const auto bits = [&](auto d) {
+        if (c.bits == 16) f(d, integral_constant<int, 16>()); else f(d, integral_constant<int, 8>());
+    };
+    if (c.d == 64) bits(integral_constant<int, 64>());
+    else if (c.d == 128) bits(integral_constant<int, 128>());
+    else bits(integral_constant<int, 256>());
+}
+
+// Blocks of 64 positions that a request of n rows can touch.
+int touched_blocks(int32_t n) { return (n + kBlockTokens - 2) / kBlockTokens + 1; }
+
+}  // namespace
+
+hipError_t launch_append(const AppendArgs &A, hipStream_t s) {
+    const int nb = touched_blocks(A.B.max_rows), kvb = A.B.b * nb * A.c.heads;
+    const int per = TPB * 8 / A.c.d, most = (A.q_heads + per - 1) / per;      // passes of a row's q heads
+    // few rows: a workgroup per pass, for latency; many: all of a row's, which share its cosines
+    const int slices = A.q == nullptr ? 0 : A.B.total_rows < 1024 ? most : 1;
+    const int grid = kvb + A.B.total_rows * slices;
+    with_format(A.c, [&](auto d, auto bits) {
+        if (A.f32)
+            hipLaunchKernelGGL((append_kernel<d(), bits(), true>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, slices);
+        else
+            hipLaunchKernelGGL((append_kernel<d(), bits(), false>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, slices);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const ReadArgs &A, hipStream_t s) {
+    const int nb = touched_blocks(A.B.max_rows), grid = A.B.b * nb * A.c.heads;
+    with_format(A.c, [&](auto d, auto bits) {
+        if (A.f32)
+            hipLaunchKernelGGL((kv_read_kernel<d(), bits(), true>), dim3(grid), dim3(TPB), 0, s, A, nb);
+        else
+            hipLaunchKernelGGL((kv_read_kernel<d(), bits(), false>), dim3(grid), dim3(TPB), 0, s, A, nb);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_commit(const CommitArgs &A, hipStream_t s) {
+    with_format(A.c, [&](auto d, auto bits) {
+        hipLaunchKernelGGL((kv_commit_kernel<d(), bits()>), dim3(A.c.heads, A.B.b, A.count), dim3(TPB), 0, s, A);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_new_len(const CommitArgs &A, hipStream_t s) {
+    hipLaunchKernelGGL(new_len_kernel, dim3(A.B.b), dim3(64), 0, s, A.B, A.c.page_shift, A.path, A.accept_len,
+                       A.new_len);
+    return hipGetLastError();
+}
+
+}  // namespace dspk

@@ -1,0 +1,91 @@
+// Bookkeeping of a drafted tree: ancestor masks and positions, and greedy
+// acceptance along the tree.  One wave per request, one lane per node (at
+// most 64); a parent's number is below its children's, so every walk over
+// parents or children ends after at most m steps.
+//
+// Bound by latency: a few hundred bytes per request, a dozen dependent steps.
+#include <hip/hip_runtime.h>
+
+#include "attn_internal.h"
+
+namespace dspk {
+namespace {
+
+// Parent of the lane's node: -1 at the root, for absent nodes and past m;
+// `fault` (wave-uniform): some parent is not -1 and not below its node.
+__device__ __forceinline__ int load_parent(const int32_t *parents, int r, int m, int j, bool &fault) {
+    const int p = j >= 1 && j < m ? parents[(int64_t)r * (m - 1) + j - 1] : -1;
+    fault = __ballot(p < -1 || p >= (j < 1 ? 1 : j)) != 0;
+    return p;
+}
+
+__global__ __launch_bounds__(64) void tree_layout_kernel(const int32_t *__restrict__ parents, int m,
+                                                         const int32_t *__restrict__ cache_len,
+                                                         uint64_t *__restrict__ mask,
+                                                         int32_t *__restrict__ positions) {
+    const int r = blockIdx.x, j = threadIdx.x;
+    bool fault;
+    const int p = load_parent(parents, r, m, j, fault);
+    uint64_t bits = 0;
+    int depth = -1, at = j < m && !fault ? j : -1;
+    bool root = false;
+    while (__any(at >= 0)) {                       // at strictly falls
+        const int up = __shfl(p, at < 0 ? 0 : at);
+        if (at >= 0) {
+            bits |= 1ull << at;
+            ++depth;
+            root = at == 0;
+            at = root ? -1 : up;
+        }
+    }
+    if (j < m) {
+        const int64_t i = (int64_t)r * m + j;
+        mask[i] = root ? bits : 0;                 // an absent node sees nothing
+        positions[i] = cache_len[r] + (root ? depth : 0);
+    }
+}
+
+__global__ __launch_bounds__(64) void accept_tree_kernel(const int32_t *__restrict__ target,
+                                                         const int32_t *__restrict__ draft,
+                                                         const int32_t *__restrict__ parents, int m,
+                                                         int32_t *__restrict__ accept_len,
+                                                         int32_t *__restrict__ committed,
+                                                         int32_t *__restrict__ path) {
+    const int r = blockIdx.x, j = threadIdx.x;
+    bool fault;
+    const int p = load_parent(parents, r, m, j, fault);
+    const int t = j < m ? target[(int64_t)r * m + j] : 0;
+    const int d = j >= 1 && j < m ? draft[(int64_t)r * (m - 1) + j - 1] : 0;
+    int n = fault ? 0 : 1, at = 0, mine = j == 0 && !fault ? 0 : -1;
+    while (n > 0) {
+        const int want = __shfl(t, at);
+        const uint64_t hit = __ballot(j >= 1 && j < m && p == at && d == want);
+        if (hit == 0) break;
+        at = __ffsll((unsigned long long)hit) - 1; // above its parent: at strictly grows
+        if (j == n) mine = at;
+        ++n;
+    }
+    const int tok = __shfl(t, mine < 0 ? 0 : mine);
+    if (j < m) {
+        path[(int64_t)r * m + j] = mine;
+        committed[(int64_t)r * m + j] = mine < 0 ? -1 : tok;
+    }
+    if (j == 0) accept_len[r] = fault ? -1 : n;
+}
+
+}  // namespace
+
+hipError_t launch_tree_layout(const int32_t *parents, int32_t b, int32_t m, const int32_t *cache_len, uint64_t *mask,
+                              int32_t *positions, hipStream_t s) {
+    hipLaunchKernelGGL(tree_layout_kernel, dim3(b), dim3(64), 0, s, parents, m, cache_len, mask, positions);
+    return hipGetLastError();
+}
+
+hipError_t launch_accept_tree(const int32_t *target, const int32_t *draft, const int32_t *parents, int32_t b, int32_t m,
+                              int32_t *accept_len, int32_t *committed, int32_t *path, hipStream_t s) {
+    hipLaunchKernelGGL(accept_tree_kernel, dim3(b), dim3(64), 0, s, target, draft, parents, m, accept_len, committed,
+                       path);
+    return hipGetLastError();
+}
+
+}  // namespace dspk

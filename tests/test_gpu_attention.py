@@ -1,0 +1,252 @@
+"""Attention of a round's rows over the paged cache against the fp64 reference."""
+import numpy as np
+import pytest
+
+from attnutil import Round, assert_attention, bf16, chain_masks, dev, i32, masks_dev, run_attention
+from oracle import attention as oa
+from speculative_decoding_verify_dspk_amd import binding
+
+pytestmark = pytest.mark.gpu
+
+
+def _tree_masks(rng, m):
+    par = [int(rng.integers(max(0, j - 3), j)) for j in range(1, m)]
+    return oa.tree_layout(par, 0)[0]
+
+
+def _check(R, hq, masks, got, q, what=""):
+    for r, (n, m) in enumerate(zip(R.lens, R.rows)):
+        a, e = R.starts[r], R.starts[r + 1]
+        ref, mag = oa.attention(q[a:e], R.k[r], R.v[r], n, masks[a:e], R.d ** -0.5)
+        assert_attention(got[a:e], ref, mag, f"{what} request {r}")
+
+
+def _q(R, hq, std=1.0):
+    return bf16(R.rng.normal(0, std, (R.total, hq, R.d)))
+
+
+CASES = [
+    # lens, rows, hq, hkv, d, bits, page
+    *[([n], [1], 32, 8, 128, 16, 64) for n in (0, 1, 31, 32, 63, 64, 127, 1021)],
+    *[([n], [1], 4, 1, 128, 8, 64) for n in (0, 1, 63, 64, 255, 256, 700)],
+    ([0, 7, 300], [5, 5, 5], 14, 2, 64, 8, 64),
+    ([0, 7, 300], [5, 5, 5], 14, 2, 64, 16, 128),
+    ([513, 100], [17, 17], 40, 8, 128, 8, 64),             # 85 rows of a head: two row groups
+    ([130], [17], 32, 8, 128, 16, 64),
+    ([200], [64], 8, 8, 64, 16, 64),
+    ([200], [32], 8, 8, 64, 8, 64),
+    ([100], [64], 40, 8, 128, 16, 64),                     # 320 rows: four groups, two blocks
+    ([70, 0], [33, 33], 16, 2, 128, 8, 256),
+    ([333], [1], 8, 1, 256, 16, 64),
+    ([40, 900], [8, 8], 8, 1, 256, 8, 64),
+    ([90], [20], 8, 1, 256, 16, 64),
+    ([90], [3], 8, 1, 256, 8, 64),
+    ([500, 61, 0, 64], [16] * 4, 8, 2, 128, 16, 64),
+    ([500, 61, 0, 64], [16] * 4, 8, 2, 128, 8, 1024),
+    ([150], [32], 32, 8, 128, 8, 64),
+    ([50 * i for i in range(70)], [2] * 70, 4, 2, 64, 16, 64),      # more requests than a wave has lanes
+]
+
+
+@pytest.mark.parametrize("lens,rows,hq,hkv,d,bits,page", CASES)
+@pytest.mark.parametrize("kind", ["chain", "tree"])
+def test_attention_matches_reference(lens, rows, hq, hkv, d, bits, page, kind):
+    R = Round(lens, rows, hkv, d, bits, page, seed=len(lens) + rows[0])
+    q = _q(R, hq)
+    if kind == "chain":
+        masks = sum((chain_masks(m) for m in rows), [])
+        got = run_attention(R, q, hq)
+    else:
+        masks = sum((_tree_masks(R.rng, m) for m in rows), [])
+        got = run_attention(R, q, hq, masks)
+    _check(R, hq, masks, got, q, kind)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_ragged_rows_and_rows_of_no_request(bits):
+    """Requests of 0, 1 and many rows; rows past the last request and
+    columns past the heads stay as they are; q and out have wider rows."""
+    import torch
+    R = Round([77, 5, 130, 0], [3, 0, 11, 1], 2, 128, bits, 64, seed=4, max_rows=16)
+    R.total += 5
+    R.batch = binding.AttnBatch(R.len_dev, R.table, 16, R.total, R.start_dev)
+    q = _q(R, 6)
+    qw = torch.full((R.total, 6 * 128 + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    qw[:, :6 * 128] = dev(q.reshape(R.total, -1), torch.bfloat16)
+    out = torch.full((R.total + 1, 6 * 128 + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = binding.alloc_workspace(binding.attn_workspace_bytes(6, 2, 128, 4, 16))
+    binding.tree_attention(R.cache, R.batch, qw, 6, out, ws)
+    o = out.float().cpu().numpy()
+    assert (o[15:] == 7).all() and (o[:, 6 * 128:] == 7).all()
+    masks = sum((chain_masks(m) for m in R.rows), [])
+    _check(R, 6, masks, o[:15, :6 * 128].reshape(15, 6, 128), q)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_masks_that_leave_rows_empty(bits, d):
+    """Any mask, not only a tree's: rows that see no row of their own see the
+    cached positions alone, and with nothing cached come out as zeros."""
+    R = Round([0, 40], [9, 9], 2, d, bits, 64, seed=7)
+    q = _q(R, 4)
+    masks = [int(x) for x in R.rng.integers(0, 1 << 9, 18)]
+    masks[2] = masks[5] = masks[9] = masks[17] = 0
+    masks[4] = (1 << 64) - 1                      # bits past the request's rows mean nothing
+    got = run_attention(R, q, 4, masks)
+    _check(R, 4, [x & (1 << 9) - 1 for x in masks], got, q)
+    assert (got[[2, 5]] == 0).all()
+    assert (run_attention(R, q, 4, [0] * 18)[:9] == 0).all()
+
+
+@pytest.mark.parametrize("what", ["nan", "inf", "lowest"])
+@pytest.mark.parametrize("bits", [16, 8])
+def test_masked_positions_do_not_reach_a_row(what, bits):
+    """A row of the tree with k and v that are not finite (or the type's lowest
+    value) changes only the rows that see it."""
+    import torch
+    hkv, d, m, n = 2, 128, 12, 45
+    R = Round([n], [m], hkv, d, bits, 64, seed=9)
+    q = _q(R, 4)
+    masks = _tree_masks(R.rng, m)
+    clean = run_attention(R, q, 4, masks)
+    x = {"nan": float("nan"), "inf": float("inf"), "lowest": torch.finfo(torch.bfloat16).min}[what]
+    node = 5
+    row = torch.full((1, hkv * d), x, dtype=torch.bfloat16, device="cuda")
+    binding.kv_append(R.cache, binding.AttnBatch(i32([n + node]), R.table, 1), row, row)
+    got = run_attention(R, q, 4, masks)
+    for i in range(m):
+        if masks[i] >> node & 1:
+            assert what == "lowest" or not np.isfinite(got[i]).any()
+        else:
+            assert np.array_equal(got[i], clean[i]), i
+
+
+def test_infinite_v_reaches_the_rows_that_see_it_alone():
+    import torch
+    R = Round([10], [6], 1, 64, 16, 64, seed=3)
+    q = _q(R, 2)
+    masks = [1, 3, 5, 9, 17, 33]                  # every draft follows the anchor
+    clean = run_attention(R, q, 2, masks)
+    v = torch.zeros((1, 64), dtype=torch.bfloat16, device="cuda")
+    v[0, 3], v[0, 40] = float("inf"), float("-inf")
+    binding.kv_append(R.cache, binding.AttnBatch(i32([12]), R.table, 1), torch.zeros_like(v), v)
+    got = run_attention(R, q, 2, masks)
+    assert np.isposinf(got[2, :, 3]).all() and np.isneginf(got[2, :, 40]).all()
+    assert np.isfinite(np.delete(got[2], [3, 40], axis=-1)).all()
+    keep = [0, 1, 3, 4, 5]
+    assert np.array_equal(got[keep], clean[keep])
+
+
+def test_bad_lengths_and_pages_come_out_as_nan():
+    """Faults of one request do not touch the others, and no address outside
+    the pools is followed."""
+    R = Round([70, 70, 70, 70, 70], [3] * 5, 2, 64, 16, 64, seed=6)
+    q = _q(R, 4)
+    good = run_attention(R, q, 4)
+    R.table[1, 0] = R.cache.pages
+    R.table[2, 1] = -5
+    R.len_dev[3] = -1
+    R.len_dev[4] = 64 * R.table.shape[1] - 2
+    got = run_attention(R, q, 4)
+    assert np.array_equal(got[:3], good[:3])
+    assert np.isnan(got[3:]).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d,bits,n,m", [(32, 8, 128, 16, 9000, 1), (8, 1, 128, 8, 20001, 6),
+                                               (4, 1, 64, 16, 33000, 17), (2, 1, 256, 8, 5000, 3)])
+def test_long_contexts_split_over_workgroups(hq, hkv, d, bits, n, m):
+    """Segments shared by many workgroups; peaked scores, so that maxima differ
+    between them; the same bits on every call."""
+    R = Round([n], [m], hkv, d, bits, 64, seed=n)
+    q = _q(R, hq, 2.0)
+    got = run_attention(R, q, hq)
+    for i in range(min(m, 2)):
+        for h in (0, hq - 1):
+            ref, mag = oa.attention(q[i:i + 1, h:h + 1], R.k[0][:, h // (hq // hkv)][:, None],
+                                    R.v[0][:, h // (hq // hkv)][:, None], n, [(2 << i) - 1], d ** -0.5) \
+                if m == 1 else _one(R, q, i, h, hq, hkv, n)
+            # scores here reach twice the size that the tolerance's score term is for
+            assert_attention(got[i:i + 1, h:h + 1], ref, 2 * mag)
+    assert np.array_equal(got, run_attention(R, q, hq))
+
+
+def _one(R, q, i, h, hq, hkv, n):
+    """Row i of a chain sees n + i + 1 positions: as one row after n + i cached ones."""
+    kv = h // (hq // hkv)
+    return oa.attention(q[i:i + 1, h:h + 1], R.k[0][:n + i + 1, kv][:, None], R.v[0][:n + i + 1, kv][:, None], n + i, [1],
+                        R.d ** -0.5)
+
+
+def test_pools_past_4_gib():
+    """Pages whose offsets do not fit 32 bits, in bytes or elements."""
+    import torch
+    heads, d, page = 8, 128, 64
+    pages = (5 << 30) // (heads * d * page)                   # 5 Gi elements of 2 bytes per pool
+    R = Round([150], [4], heads, d, 16, page, seed=8, pages=pages)
+    q = _q(R, 8)
+    got = run_attention(R, q, 8)
+    _check(R, 8, chain_masks(4), got, q)
+    high = R.table_np.copy()
+    high[0, :3] = [pages - 1, pages - 2, pages // 2]
+    full = binding.AttnBatch(i32([0]), dev(high), 154)
+    k, v = (dev(x[0].reshape(154, -1), torch.bfloat16) for x in (R.k, R.v))
+    binding.kv_append(R.cache, full, k, v)
+    R.batch = binding.AttnBatch(R.len_dev, dev(high), 4)
+    assert np.array_equal(run_attention(R, q, 8), got)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    binding.kv_read(R.cache, full, ko, vo)
+    assert torch.equal(ko, k) and torch.equal(vo, v)
+
+
+def test_graphs_replay_over_growing_lengths_and_share_a_workspace():
+    """Two captured calls that share a workspace, replayed while the lengths on
+    the device grow, equal eager calls."""
+    import torch
+    A = Round([900, 20], [4, 4], 2, 128, 16, 64, seed=1)
+    B = Round([300], [16], 2, 128, 8, 64, seed=2)
+    qa, qb = (dev(_q(R, 8).reshape(R.total, -1), torch.bfloat16) for R in (A, B))
+    oa_, ob = torch.empty_like(qa), torch.empty_like(qb)
+    ws = binding.alloc_workspace(max(binding.attn_workspace_bytes(8, 2, 128, 2, 4),
+                                     binding.attn_workspace_bytes(8, 2, 128, 1, 16)))
+    calls = [lambda: binding.tree_attention(A.cache, A.batch, qa, 8, oa_, ws),
+             lambda: binding.tree_attention(B.cache, B.batch, qb, 8, ob, ws)]
+    graphs = []
+    for call in calls:
+        g = torch.cuda.CUDAGraph()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call()
+        torch.cuda.current_stream().wait_stream(side)
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    for step in range(4):
+        A.len_dev.copy_(i32([900 - 100 * step, 20 - step]))
+        B.len_dev.fill_(300 - 64 * step)
+        for call in calls:
+            call()
+        torch.cuda.synchronize()
+        want = oa_.clone(), ob.clone()
+        for o in (oa_, ob):
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(oa_, want[0]) and torch.equal(ob, want[1]), step
+
+
+def test_on_another_stream():
+    import torch
+    R = Round([400], [5], 2, 128, 16, 64, seed=5)
+    q = _q(R, 8)
+    want = run_attention(R, q, 8)
+    qd = dev(q.reshape(R.total, -1), torch.bfloat16)
+    out = torch.zeros_like(qd)
+    ws = binding.alloc_workspace(binding.attn_workspace_bytes(8, 2, 128, 1, 5))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    binding.tree_attention(R.cache, R.batch, qd, 8, out, ws, stream=s)
+    s.synchronize()
+    assert np.array_equal(out.float().cpu().numpy().reshape(want.shape), want)
