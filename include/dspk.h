@@ -623,9 +623,12 @@ int dspk_kv_read(const dspk_kv_cache *cache, const dspk_attn_batch *batch, void 
                  int32_t dtype, void *stream);
 
 /* Workspace of dspk_tree_attention for these heads and at most max_rows rows
- * per request, for any cache contents and page-table width (0 if a size is
- * not supported).  It needs no clearing; calls that share it must be ordered on one
- * stream. */
+ * per request, for any cache format, lengths and page-table width (0 if a size
+ * is not supported): arrival counters and partial sums.  Zero-fill it once
+ * before its first use; every completed call leaves the counters at zero, so
+ * one buffer of the largest size serves any sequence of attention calls ordered
+ * on one stream (calls that overlap must not share it, nor calls of another
+ * kind). */
 size_t dspk_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t b, int32_t max_rows);
 
 /*

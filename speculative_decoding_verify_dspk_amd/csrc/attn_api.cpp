@@ -11,35 +11,24 @@
 
 namespace dspk {
 
-AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t bits, int32_t b, int32_t max_rows,
-                   int64_t capacity, int cus) {
+AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t b, int32_t max_rows, int64_t capacity,
+                   int cus) {
     AttnPlan p;
     const int64_t rows = (int64_t)max_rows * (q_heads / kv_heads);    // rows over one k/v head
     const int64_t tiles = (rows + 15) / 16;
-    // A wave holds up to 4 row tiles (2 of 256 dimensions): their q and
-    // outputs are what its registers can keep.  More rows go to further waves
-    // of the workgroup, which read the same k and v from its caches; beyond
-    // four row groups the rows are cut into blocks that read them again.
-    const int most = d == 256 ? 2 : 4;
-    p.rg = tiles <= most ? 1 : tiles <= 2 * most ? 2 : 4;
-    p.rt = (int)((tiles + p.rg - 1) / p.rg);
-    if (p.rt > most) p.rt = most;
-    if (p.rt == 3 && p.rg != 2) p.rt = 4;                             // instances: 1, 2, 4 tiles, and 3 in two groups
-    if (p.rg > 1 && p.rt < 3) p.rt = d == 256 ? 2 : 3;
-    const int br = 16 * p.rt * p.rg;
-    p.blocks = (int32_t)((rows + br - 1) / br);
-    p.unit = (bits == 8 ? 64 : 32) * (4 / p.rg);
-    const int64_t per_seg = capacity < 1 ? 1 : (capacity + p.unit - 1) / p.unit;
-    const int64_t segs = (int64_t)b * kv_heads * p.blocks;
-    const int64_t most_wg = (int64_t)cus * attn_occ(d, p.rt);
-    // segs < 2^31 / per_seg, without the product overflowing
-    p.fits = segs <= INT32_MAX / per_seg && segs * p.rg * p.rt * (d / 32) <= INT32_MAX;
-    const int64_t units = p.fits ? segs * per_seg : most_wg;
-    p.grid = (int32_t)(units < most_wg ? units : most_wg);
-    p.split = per_seg > 1;
-    const size_t slots = (size_t)most_wg * 2 * p.rg * p.rt;           // 16-row tiles of partial sums
-    p.off_ml = slots * d * 16 * sizeof(float);
-    p.ws_bytes = (p.off_ml + slots * 32 * sizeof(float) + 255) / 256 * 256;
+    p.tiles = tiles < attn_tiles(d) ? 1 : attn_tiles(d);
+    p.blocks = (int32_t)((tiles + p.tiles - 1) / p.tiles);
+    const int64_t unit = kAttnStep * kAttnWaves, per_seg = capacity < 1 ? 1 : (capacity + unit - 1) / unit;
+    const int64_t segs = (int64_t)b * kv_heads;
+    const int32_t most = cus > p.blocks ? cus / p.blocks : 1;         // one workgroup per CU
+    p.fits = segs <= INT32_MAX / per_seg;                             // segs * per_seg, without overflowing
+    const int64_t units = p.fits ? segs * per_seg : most;
+    p.groups = (int32_t)(units < most ? units : most);
+    const size_t wgs = cus > p.blocks ? cus : p.blocks;               // at least most * blocks
+    p.off_part = (wgs * kAttnWaves * sizeof(uint32_t) + 255) / 256 * 256;
+    // two pieces per workgroup: of the segment it did not start, and of the one it does not end
+    p.ws_bytes = p.off_part + wgs * 2 * attn_piece(d, p.tiles) * sizeof(float);
+    p.ws_bytes = (p.ws_bytes + 255) / 256 * 256;
     return p;
 }
 
@@ -268,10 +257,10 @@ int dspk_kv_read(const dspk_kv_cache *cache, const dspk_attn_batch *batch, void 
 }
 
 size_t dspk_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t b, int32_t max_rows) {
-    if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || q_heads > 65535 || b < 1 || max_rows < 1 ||
+    if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || q_heads / kv_heads > 256 || b < 1 || max_rows < 1 ||
         max_rows > DSPK_MAX_TREE || (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return 0;
-    return dspk::attn_plan(q_heads, kv_heads, head_dim, 16, b, max_rows, 1, dspk::device_cus()).ws_bytes;
+    return dspk::attn_plan(q_heads, kv_heads, head_dim, b, max_rows, 1, dspk::device_cus()).ws_bytes;
 }
 
 int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch, const uint16_t *q, int64_t ldq,
@@ -286,15 +275,17 @@ int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch
     if (A.B.max_rows > DSPK_MAX_TREE)
         return fail(DSPK_EUNSUPPORTED, "%s: max_rows=%d (at most %d rows of one request)", who, A.B.max_rows,
                     DSPK_MAX_TREE);
-    if (q_heads < A.c.heads || q_heads % A.c.heads || q_heads > 65535)
-        return fail(DSPK_EINVAL, "%s: q_heads=%d must be a multiple of kv_heads=%d, at most 65535", who, q_heads, A.c.heads);
+    if (q_heads < A.c.heads || q_heads % A.c.heads)
+        return fail(DSPK_EINVAL, "%s: q_heads=%d must be a multiple of kv_heads=%d", who, q_heads, A.c.heads);
+    if (q_heads / A.c.heads > 256)
+        return fail(DSPK_EUNSUPPORTED, "%s: q_heads=%d (at most 256 per k/v head)", who, q_heads);
     rc = check_rows(q, ldq, q_heads, A.c.d, DSPK_BF16, "q", who);
     if (rc) return rc;
     rc = check_rows(out, ldo, q_heads, A.c.d, DSPK_BF16, "out", who);
     if (rc) return rc;
     if (!(scale > 0.f) || !isfinite(scale)) return fail(DSPK_EINVAL, "%s: scale must be finite and > 0", who);
     if (!aligned(tree_mask, 8)) return fail(DSPK_EINVAL, "%s: tree_mask misaligned", who);
-    const dspk::AttnPlan p = dspk::attn_plan(q_heads, A.c.heads, A.c.d, A.c.bits, A.B.b, A.B.max_rows,
+    const dspk::AttnPlan p = dspk::attn_plan(q_heads, A.c.heads, A.c.d, A.B.b, A.B.max_rows,
                                              (int64_t)A.B.max_pages << A.c.page_shift, dspk::device_cus());
     if (!p.fits) return fail(DSPK_EUNSUPPORTED, "%s: page table too large for one launch", who);
     if (!pointer(workspace, 256) || ws_bytes < p.ws_bytes)
@@ -306,10 +297,12 @@ int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch
     A.rep = q_heads / A.c.heads;
     A.scale = scale * 1.44269504088896340736f;
     A.mask = tree_mask;
-    A.grid = p.grid;
-    A.part = (float *)workspace;
-    A.part_ml = (float *)((char *)workspace + p.off_ml);
-    return launch_result(dspk::launch_tree_attention(A, p, (hipStream_t)stream), who);
+    A.tiles = p.tiles;
+    A.blocks = p.blocks;
+    A.groups = p.groups;
+    A.counters = (uint32_t *)workspace;
+    A.part = (float *)((char *)workspace + p.off_part);
+    return launch_result(dspk::launch_tree_attention(A, (hipStream_t)stream), who);
 }
 
 int dspk_tree_layout(const int32_t *parents, int32_t b, int32_t m_rows, const int32_t *cache_len, uint64_t *tree_mask,

@@ -69,24 +69,20 @@ hipError_t launch_kv_commit(const CommitArgs &a, hipStream_t s);
 // new_len[r] alone, for a call whose new_len is its cache_len
 hipError_t launch_new_len(const CommitArgs &a, hipStream_t s);
 
-// Shape of an attention launch.  A workgroup's four waves are `rg` row groups
-// of rt 16-row tiles, times 4 / rg token groups; see tree_attn.hip.
-constexpr int attn_occ(int d, int rt) {           // workgroups per CU (registers: q and outputs of rt row tiles)
-    return d == 256 ? 1 : rt * d <= 128 ? 3 : rt * d <= 256 ? 2 : 1;
-}
+// Shape of an attention launch: groups of `blocks` workgroups, one per block of
+// `tiles` x 16 rows; see tree_attn.hip.
+constexpr int kAttnWaves = 8;
+constexpr int kAttnStep = 32;                       // positions of a wave's step
+constexpr int kAttnTile = 256 + 32;                 // floats of a 16 x 16 tile of partial sums, with m and sum of its rows
+constexpr int attn_tiles(int d) { return d == 256 ? 1 : 2; }         // most row tiles of a wave (its registers)
+constexpr int attn_piece(int d, int rt) { return rt * (d / 16) * kAttnTile; }  // floats of a row block's partial sums
 struct AttnPlan {
-    int32_t rt, rg;
-    int32_t unit;                   // tokens of one step of a workgroup
-    int32_t blocks;                 // row blocks of a request of max_rows rows
-    int32_t grid;                   // workgroups of the streaming kernel
-    bool fits;                      // its unit numbers fit 31 bits
-    bool split;                     // a segment may be shared between workgroups
-    size_t off_ml, ws_bytes;
+    int32_t tiles, blocks, groups;
+    bool fits;                      // unit numbers fit 31 bits
+    size_t off_part, ws_bytes;      // workspace: counters, then partial sums
 };
-AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t bits, int32_t b, int32_t max_rows,
-                   int64_t capacity, int cus);
-// workspace for any cache format and capacity
-size_t attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t b, int32_t max_rows, int cus);
+AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t b, int32_t max_rows, int64_t capacity,
+                   int cus);
 
 struct AttnArgs {
     KvCache c;
@@ -97,11 +93,11 @@ struct AttnArgs {
     int32_t rep;                    // q heads per kv head
     float scale;                    // of the scores, times log2(e)
     const uint64_t *mask;           // [total_rows], or NULL: a chain
-    int32_t grid;                   // of the streaming kernel
-    float *part;                    // partial outputs
-    float *part_ml;                 // their row maxima and sums
+    int32_t tiles, blocks, groups;  // see AttnPlan
+    uint32_t *counters;             // arrivals at shared segments [groups][blocks][waves], zero between calls
+    float *part;                    // partial sums [groups][blocks][2][attn_piece]
 };
-hipError_t launch_tree_attention(const AttnArgs &a, const AttnPlan &p, hipStream_t s);
+hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s);
 
 hipError_t launch_tree_layout(const int32_t *parents, int32_t b, int32_t m, const int32_t *cache_len, uint64_t *mask,
                               int32_t *positions, hipStream_t s);

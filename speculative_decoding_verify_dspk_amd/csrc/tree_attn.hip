@@ -4,11 +4,17 @@
 //
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i.k_j - max_j),
 //
-// j over the positions row i sees.  A (request, kv head, row block) is a
-// segment; its cache positions are cut into units, and a persistent grid
-// takes equal contiguous ranges of all segments' units, so ragged batches load
-// every CU alike.  A segment shared by workgroups leaves partial sums in the
-// workspace, which attn_join_kernel adds in workgroup order (deterministic).
+// j over the positions row i sees.  The rows of a request over one kv head are
+// cut into blocks of up to 32 (16 of 256 dimensions: what a wave's registers
+// hold).  A (request, kv head) is a segment, its cache positions are cut into
+// units of 256; groups of workgroups, one for each row block, take equal
+// contiguous ranges of all segments' units, so ragged batches load every CU
+// alike.  A group's workgroups sit on one XCD and stream the same k and v at the
+// same time, out of its L2 for all but the first.  A segment shared by groups
+// leaves partial sums in the workspace; the last to arrive adds them in order
+// (deterministic), each wave its own tiles, all pieces in flight at once.  (With
+// row groups as waves of one workgroup instead there were as many times more
+// pieces, and their addition took most of a call.)
 //
 // Within a workgroup each wave takes its own positions, so k and v go from
 // memory to the matrix cores without LDS or barriers: the cache is stored in
@@ -35,9 +41,24 @@ using dec::as_bf16x8;
 using dec::bf16x8;
 using kv::f32x4;
 using kv::u32x4;
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4, TPB = 64 * kWaves;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int WAVES = kAttnWaves, TPB = 64 * WAVES;
+constexpr int kStep = kAttnStep;        // positions of a wave's step
+constexpr int kTileFloats = kAttnTile;  // a tile of partial sums: 16 x 16 outputs, and m and sum of 16 rows
+constexpr int kUnit = kAttnStep * WAVES;
+
 #define NEG_INF (-__builtin_inff())
+// Limits of what a lane adds at a time, in units of its row's reference, before
+// the reference has to rise.  8 bits: a probability times its v scale goes into
+// the product as fp16, at most 2^15, 2^4 at the reference; it keeps its 11 bits
+// down to 2^-18 of the reference.  Sums, and bf16 pairs, have fp32's range.
+constexpr float kMostF16 = 32768.f, kMostSum = 0x1p60f, kBase8 = 4.f;
+// The reference of a row that has seen nothing yet, for 2^(-inf - ref) = 0.
+__device__ __forceinline__ float zero_if_none(float m) { return m == NEG_INF ? 0.f : m; }
 
 // Byte i of x, signed, as a float: one instruction (the compiler would
 // extract, extend and convert).
@@ -64,6 +85,28 @@ __device__ __forceinline__ bf16x8 codes_bf16(uint32_t a, uint32_t b) {
     return as_bf16x8(r);
 }
 
+// Eight signed codes as exact fp16 values: u = code + 128 under the exponent of
+// 1024 is 1024 + u, less 1152 the code.
+__device__ __forceinline__ f16x8 codes_f16(uint32_t a, uint32_t b) {
+    const f16x2 off = {(_Float16)-1152.f, (_Float16)-1152.f};
+    a ^= 0x80808080u;
+    b ^= 0x80808080u;
+    u32x4 r;
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, a, 0x04010400u)) + off);
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u)) + off);
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u)) + off);
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u)) + off);
+    return __builtin_bit_cast(f16x8, r);
+}
+
+// The largest of three, NaN left aside (written out: the compiler would first
+// quieten results of the matrix cores).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
 // max and sum over the four lanes of a row (lane % 16 is the row)
 __device__ __forceinline__ float row_max(float x) {
     x = fmaxf(x, __shfl_xor(x, 16));
@@ -74,29 +117,21 @@ __device__ __forceinline__ float row_sum(float x) {
     return x + __shfl_xor(x, 32);
 }
 
-__device__ __forceinline__ int wave_sum(int x) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
-    return x;
-}
-
 // Units of a request: per segment and in all.  A request with rows has at
 // least one unit per segment, so that its rows are written even if nothing is
 // cached or its length is a fault.
 struct Units {
-    int per_seg, blocks, total;
+    int per_seg, total;
 };
-__device__ __forceinline__ Units units_of(const AttnArgs &A, const kv::Req &q, int unit, int block_rows) {
+__device__ __forceinline__ Units units_of(const AttnArgs &A, const kv::Req &q) {
     Units u;
-    const int tokens = q.ok ? q.len + q.rows : 0;
-    u.per_seg = max(1, (tokens + unit - 1) / unit);
-    u.blocks = (q.rows * A.rep + block_rows - 1) / block_rows;
-    u.total = u.per_seg * u.blocks * A.c.heads;
+    u.per_seg = max(1, ((q.ok ? q.len + q.rows : 0) + kUnit - 1) / kUnit);
+    u.total = q.rows > 0 ? u.per_seg * A.c.heads : 0;
     return u;
 }
 
-// Range of a workgroup: the first rem workgroups take q + 1 units, the others
-// q.  The inverse gives the workgroup of a unit.
+// Range of a group: the first rem groups take q + 1 units, the others q.  The
+// inverse gives the group of a unit.
 struct Ranges {
     int q, rem;
     __device__ __forceinline__ int begin(int w) const { return w * q + min(w, rem); }
@@ -105,64 +140,137 @@ struct Ranges {
         return u < cut ? u / (q + 1) : rem + (u - cut) / q;
     }
 };
-// All units of the call; where > = 0 also the request that holds unit `where`
-// and that request's first unit.  The same on every lane; waves do it alone.
-__device__ __forceinline__ int scan_units(const AttnArgs &A, int unit, int block_rows, int where, int &req, int &first) {
+// First unit of a group's range and what holds it: the range's bounds,
+// the request and that request's first unit.  Every wave does it by itself;
+// requests are taken 64 at a time, one per lane.
+struct Start {
+    int u, u_end, req, first;
+};
+__device__ __forceinline__ Start find_start(const AttnArgs &A, int group, Ranges &R) {
     const int lane = threadIdx.x & 63;
-    int sum = 0;
-    req = A.B.b;
+    int total = 0, x = 0, u = 0;
     for (int base = 0; base < A.B.b; base += 64) {
-        int u = 0;
-        if (base + lane < A.B.b) u = units_of(A, kv::request(A.B, A.c.page_shift, base + lane), unit, block_rows).total;
-        if (where >= 0 && req == A.B.b) {
-            int x = u;                                              // inclusive prefix sum
+        u = 0;
+        if (base + lane < A.B.b) u = units_of(A, kv::request(A.B, A.c.page_shift, base + lane)).total;
+        x = u;                                                      // inclusive prefix sum
+        if (A.B.b > 1) {
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
                 const int y = __shfl_up(x, o);
                 if (lane >= o) x += y;
             }
-            const uint64_t past = __ballot(sum + x > where);
-            if (past) {
-                const int l = __ffsll((unsigned long long)past) - 1;
-                req = base + l;
-                first = sum + __shfl(x - u, l);
-                return -1;
+            total += __builtin_amdgcn_readlane(x, 63);
+        } else {
+            total = __builtin_amdgcn_readfirstlane(x);
+        }
+    }
+    // fewer than two units each: two to some, which is no slower and leaves fewer pieces
+    const int groups = total > A.groups && total < 2 * A.groups ? (total + 1) / 2 : A.groups;
+    R.q = total / groups;
+    R.rem = total - R.q * groups;
+    Start s;
+    s.u = min(R.begin(group), total);
+    s.u_end = min(R.begin(group + 1), total);
+    s.req = s.first = 0;
+    if (A.B.b == 1 || s.u >= s.u_end) return s;
+    int sum = 0;
+    for (int base = 0; base < A.B.b; base += 64) {
+        if (A.B.b > 64) {                                           // else x and u are those of the only 64
+            u = 0;
+            if (base + lane < A.B.b) u = units_of(A, kv::request(A.B, A.c.page_shift, base + lane)).total;
+            x = u;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int y = __shfl_up(x, o);
+                if (lane >= o) x += y;
             }
         }
-        sum += wave_sum(u);
+        const uint64_t past = __ballot(sum + x > s.u);
+        if (past) {
+            const int l = __ffsll((unsigned long long)past) - 1;
+            s.req = base + l;
+            s.first = sum + __builtin_amdgcn_readlane(x - u, l);
+            return s;
+        }
+        sum += __builtin_amdgcn_readlane(x, 63);
     }
-    return sum;
+    return s;
 }
 
-template <int D, int RT>
-constexpr int slot_floats() { return RT * D * 16; }                 // a wave's partial outputs
+// Device-scope accesses to partial sums: they reach the other workgroups (on
+// other XCDs too) without a cache flush.  A lane's 16 bytes go as two 64-bit
+// accesses, laid out [half][lane].
+__device__ __forceinline__ void put4(float *tile, int lane, f32x4 v) {
+    unsigned long long *q = (unsigned long long *)tile;
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    __hip_atomic_store(q + lane, __builtin_bit_cast(unsigned long long, f32x2{v[0], v[1]}), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(q + 64 + lane, __builtin_bit_cast(unsigned long long, f32x2{v[2], v[3]}), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4 get4(const float *tile, int lane) {
+    const unsigned long long *q = (const unsigned long long *)tile;
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 a = __builtin_bit_cast(f32x2, __hip_atomic_load(q + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    const f32x2 b = __builtin_bit_cast(f32x2, __hip_atomic_load(q + 64 + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    return f32x4{a[0], a[1], b[0], b[1]};
+}
+__device__ __forceinline__ void put2(float *p, float a, float b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    __hip_atomic_store((unsigned long long *)p, __builtin_bit_cast(unsigned long long, f32x2{a, b}), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void get2(const float *p, float &a, float &b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 x = __builtin_bit_cast(f32x2, __hip_atomic_load((const unsigned long long *)p, __ATOMIC_RELAXED,
+                                                                __HIP_MEMORY_SCOPE_AGENT));
+    a = x[0];
+    b = x[1];
+}
+__device__ __forceinline__ void wait_stores() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
 
-template <int D, int BITS, int RT, int RG>
-__global__ __launch_bounds__(TPB, attn_occ(D, RT))
+// Four neighbouring dimensions of a row, rounded to nearest even.
+__device__ __forceinline__ void store_out(uint16_t *dst, f32x4 x) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 y;
+    y[0] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[0]) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[1]) << 16;
+    y[1] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2]) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[3]) << 16;
+    *(u32x2 *)dst = y;
+}
+
+// RT row tiles of 16 per wave.
+//
+// The code on a call's path is kept short: with few steps per wave, as for a
+// single token, instructions run about once each and have to be fetched.  So
+// what runs once per segment is rolled up in loops.
+template <int D, int BITS, int RT>
+__global__ __launch_bounds__(TPB, WAVES / 4)
 void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) {
     constexpr int W = BITS == 16 ? 8 : 16;          // elements per 16-byte piece
-    constexpr int TS = 4 * W, TB = TS / 16;         // positions per wave step, in 16-position tiles
-    constexpr int KB = D / (4 * W);                 // k pieces of a tile
+    constexpr int KB = D / (4 * W);                 // k pieces of 16 positions
     constexpr int QB = D / 32;                      // q operands of a row tile
-    constexpr int VB = D / 16;                      // v pieces of a step, and output tiles of a row tile
-    constexpr int PB = TS / 32;                     // probability operands of a step
-    constexpr int TG = kWaves / RG, UNIT = TS * TG, BR = RG * RT * 16;
-    __shared__ float s_ml[kWaves][RT][2][16];
-    __shared__ f32x4 s_o[TG > 1 ? kWaves : 1][TG > 1 ? RT * VB * 64 : 1];
+    constexpr int VB = D / 16;                      // v pieces of a step, output tiles of a row tile
+    constexpr int NT = (RT * VB + WAVES - 1) / WAVES;               // output tiles that a wave joins
+    constexpr int BR = RT * 16;
+    __shared__ float2 s_ml[WAVES][RT][16];
+    __shared__ f32x4 s_o[WAVES][RT * VB * 64];
 
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int rg = w % RG, tg = w / RG, col = lane & 15, g = lane >> 4;
-    int req, rfirst;
-    const int total = scan_units(A, UNIT, BR, -1, req, rfirst);
-    const Ranges R{total / A.grid, total % A.grid};
-    int u = __builtin_amdgcn_readfirstlane(R.begin(blockIdx.x));
-    const int u_end = __builtin_amdgcn_readfirstlane(R.begin(blockIdx.x + 1));
-    if (u >= u_end) return;
-    scan_units(A, UNIT, BR, u, req, rfirst);
-    req = __builtin_amdgcn_readfirstlane(req);
-    rfirst = __builtin_amdgcn_readfirstlane(rfirst);
+    const int col = lane & 15, g = lane >> 4;
+    // neighbours in `at` share an XCD (workgroups go to the eight in turn)
+    const int each = gridDim.x / 8, more = gridDim.x % 8, xcd = blockIdx.x % 8;
+    const int at = xcd * each + min(xcd, more) + blockIdx.x / 8;
+    const int group = A.blocks == 1 ? at : at / A.blocks, rb = A.blocks == 1 ? 0 : at - group * A.blocks;
+    Ranges R;
+    const Start st = find_start(A, group, R);
+    int u = __builtin_amdgcn_readfirstlane(st.u), req = __builtin_amdgcn_readfirstlane(st.req),
+        rfirst = __builtin_amdgcn_readfirstlane(st.first);
+    const int u_end = __builtin_amdgcn_readfirstlane(st.u_end);
     const int page_mask = (1 << A.c.page_shift) - 1;
-    const float c = A.scale;
+    const float c = A.scale, per_rep = 1.f / A.rep;
+    const int row_base = rb * BR;                   // first of the rows (node * rep + q head)
 
     while (u < u_end) {
         kv::Req q = kv::request(A.B, A.c.page_shift, req);
@@ -170,433 +278,429 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
         q.rows = __builtin_amdgcn_readfirstlane(q.rows);
         q.len = __builtin_amdgcn_readfirstlane(q.len);
         q.ok = __builtin_amdgcn_readfirstlane(q.ok);
-        const Units un = units_of(A, q, UNIT, BR);
+        const Units un = units_of(A, q);
         if (u - rfirst >= un.total) {               // also past requests without rows
             rfirst += un.total;
             ++req;
             continue;
         }
-        const int seg = (u - rfirst) / un.per_seg, v0 = u - rfirst - seg * un.per_seg;
+        const int head = (u - rfirst) / un.per_seg, v0 = u - rfirst - head * un.per_seg;
         const int n = min(un.per_seg - v0, u_end - u);
-        const int rb = seg % un.blocks, head = seg / un.blocks;
         const int tokens = q.ok ? q.len + q.rows : 0;
-        const int row_base = rb * BR + rg * RT * 16;                // first of the wave's rows (node * rep + q head)
+        const int rows = q.rows * A.rep;
+        if (row_base >= rows) {                     // a request of fewer row blocks
+            u += n;
+            continue;
+        }
 
-        // q operands and masks of the wave's rows
+        // q operands and masks of the wave's rows; those past the last repeat it and are not written
         bf16x8 qf[RT][QB];
         uint64_t see[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            const int rr = row_base + rt * 16 + col, node = rr / A.rep;
-            const bool in = node < q.rows;
-            const uint16_t *p = A.q + (int64_t)(q.row0 + node) * A.ldq + (head * A.rep + rr - node * A.rep) * D;
+            const int rr = min(row_base + rt * 16 + col, rows - 1), node = (int)((rr + 0.5f) * per_rep);
+            const uint16_t *p = A.q + (int64_t)(q.row0 + node) * A.ldq + (head * A.rep + rr - node * A.rep) * D +
+                                g * (BITS == 16 ? 8 : 16);
 #pragma unroll
-            for (int kb = 0; kb < QB; ++kb) {
-                const int d = BITS == 16 ? kb * 32 + g * 8 : kb / 2 * 64 + g * 16 + kb % 2 * 8;
-                const u32x4 zero = {0u, 0u, 0u, 0u};
-                qf[rt][kb] = as_bf16x8(in ? *(const u32x4 *)(p + d) : zero);
-            }
-            see[rt] = !in ? 0 : A.mask != nullptr ? A.mask[q.row0 + node] : (2ull << node) - 1;
+            for (int kb = 0; kb < QB; ++kb)
+                qf[rt][kb] = as_bf16x8(*(const u32x4 *)(p + (BITS == 16 ? kb * 32 : kb / 2 * 64 + kb % 2 * 8)));
+            see[rt] = (A.mask != nullptr ? A.mask[q.row0 + node] : (2ull << node) - 1) & ((2ull << (q.rows - 1)) - 1);
         }
 
+        // Outputs and sum of each row, in units of 2^m: m is the row's reference,
+        // the maximum (log2) of probability times v scale over the first positions that
+        // it sees.  Later ones may pass it by 2^11 (8 bits) or 2^60 before anything has to
+        // be scaled down; then, which real scores hardly ever ask for, the wave
+        // starts its positions over with the higher reference.  So the loop neither
+        // takes maxima nor rescales.
         f32x4 o[RT][VB];
         float m[RT], l[RT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            m[rt] = NEG_INF;
-            l[rt] = 0.f;
-#pragma unroll
-            for (int vb = 0; vb < VB; ++vb) o[rt][vb] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
+        for (int rt = 0; rt < RT; ++rt) m[rt] = NEG_INF;
 
-        // One step: TS positions from t.  Pages that are none of the cache's
+        // A step takes 32 positions from t.  Pages that are none of the cache's
         // make every row that sees them NaN; page 0 is read in their place.
-        // Page numbers are loaded a step ahead of the k that needs them.
+        // Page numbers are loaded a step ahead of the k that needs them, k a
+        // step ahead of its use, v at the step's start.
         const int32_t *const table = page_table + (int64_t)req * A.B.max_pages;
-        u32x4 kf[TB][KB];
-        f32x4 ksc[TB];
+        u32x4 kf[2][KB];
+        f32x4 ksc[2];
         int64_t chunk = 0;
         bool bad = false;
-        const auto load_k = [&](int t, int32_t page) {
+        const auto find_page = [&](int32_t page) {
             bad = page < 0 || page >= A.c.pages;
-            chunk = (int64_t)(bad ? 0 : page) * A.c.heads + head;
-            const unsigned char *src = (const unsigned char *)A.c.k + ((chunk * D) << A.c.page_shift) * (BITS / 8) +
-                                       (uint32_t)(t & page_mask) * (D * BITS / 8) + lane * 16;
+            chunk = ((int64_t)(bad ? 0 : page) * A.c.heads + head) << A.c.page_shift;
+        };
+        const auto load_k = [&](int t) {
+            const int at = t & page_mask;
+            const unsigned char *src = (const unsigned char *)A.c.k + (chunk + at) * (D * BITS / 8);
 #pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
+            for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) kf[tb][kb] = *(const u32x4 *)(src + (tb * KB + kb) * 1024);
-            if constexpr (BITS == 8) {
-                const float *s = A.c.ks + (chunk << A.c.page_shift) + (t & page_mask) + g * 4;
-#pragma unroll
-                for (int tb = 0; tb < TB; ++tb) ksc[tb] = *(const f32x4 *)(s + tb * 16);
+                for (int kb = 0; kb < KB; ++kb) kf[i][kb] = *(const u32x4 *)(src + (i * KB + kb) * 1024 + (uint32_t)lane * 16);
+                if constexpr (BITS == 8) ksc[i] = *(const f32x4 *)(A.c.ks + chunk + at + i * 16 + (uint32_t)g * 4);
             }
         };
 
-        int t = v0 * UNIT + tg * TS;
-        const int t_end = min((v0 + n) * UNIT, tokens);
-        int32_t page_next = 0;
-        if (t < t_end) {
-            load_k(t, table[t >> A.c.page_shift]);
-            page_next = table[min(t + UNIT, t_end - 1) >> A.c.page_shift];
-        }
-        while (t < t_end) {
-            // v of this step
-            u32x4 vf[VB];
-            f32x4 vsc[TB];
-            {
-                const unsigned char *src = (const unsigned char *)A.c.v + ((chunk * D) << A.c.page_shift) * (BITS / 8) +
-                                           (uint32_t)(t & page_mask) * (D * BITS / 8) + lane * 16;
-#pragma unroll
-                for (int vb = 0; vb < VB; ++vb) vf[vb] = *(const u32x4 *)(src + vb * 1024);
-                if constexpr (BITS == 8) {
-                    const float *s = A.c.vs + (chunk << A.c.page_shift) + (t & page_mask) + g * 4;
-#pragma unroll
-                    for (int tb = 0; tb < TB; ++tb) vsc[tb] = *(const f32x4 *)(s + tb * 16);
-                }
-            }
-            f32x4 s[RT][TB];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int tb = 0; tb < TB; ++tb) s[rt][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    if constexpr (BITS == 16) {
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-                            s[rt][tb] = dec::mfma(as_bf16x8(kf[tb][kb]), qf[rt][kb], s[rt][tb]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const bf16x8 a = codes_bf16(kf[tb][kb][2 * j], kf[tb][kb][2 * j + 1]);
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt) s[rt][tb] = dec::mfma(a, qf[rt][2 * kb + j], s[rt][tb]);
-                        }
-                        // one piece at a time: the scheduler would otherwise decode all of k first and spill
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                }
-            const bool step_bad = bad, tail = t + TS > q.len;
-            const int64_t step_chunk = chunk;
-            if constexpr (BITS == 8) {
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int tb = 0; tb < TB; ++tb) s[rt][tb] *= ksc[tb];
-            }
-            const int t_next = t + UNIT;
-            if (t_next < t_end) {
-                load_k(t_next, page_next);
-                page_next = table[min(t_next + UNIT, t_end - 1) >> A.c.page_shift];
-            }
-
-            bool odd_v = false;
-            if (tail || step_bad) {
-                // masked scores are -inf whatever k held; v past the last position is 0
-#pragma unroll
-                for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int node = t + tb * 16 + g * 4 + i - q.len;
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
-                            const bool vis = node < 0 || (node < q.rows && (see[rt] >> (node & 63) & 1));
-                            const float x = step_bad ? __uint_as_float(0x7fc00000u) : s[rt][tb][i];
-                            s[rt][tb][i] = vis ? x : NEG_INF;
-                        }
-                    }
-                if constexpr (BITS == 16) {
-                    // A row's masked positions must not reach it as 0 * NaN:
-                    // v that is not finite leaves the product and is added
-                    // to the rows that see it.
-                    bool odd = false;
-#pragma unroll
-                    for (int vb = 0; vb < VB; ++vb)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int node = t + e / 2 * 16 + g * 4 + e % 2 * 2 - q.len;
-                            uint32_t x = vf[vb][e];
-                            if (node >= q.rows) x &= 0xffff0000u;
-                            if (node + 1 >= q.rows) x &= 0xffffu;
-                            const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
-                            odd |= lo || hi;
-                            if (lo) x &= 0xffff0000u;
-                            if (hi) x &= 0xffffu;
-                            vf[vb][e] = x;
-                        }
-                    odd_v = __any(odd);
-                }
-            }
-
-            // running maximum and sum; scores become probabilities
-            bf16x8 ph[RT][PB], pl[RT][PB];
+        const int t_first = v0 * kUnit + w * kStep, t_end = min((v0 + n) * kUnit, tokens);
+        bool over, odd_v = false;
+        do {
+            over = false;
+            bool fresh = true;                                      // some row may lack a reference
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                float mx = m[rt];
+                l[rt] = 0.f;
 #pragma unroll
-                for (int tb = 0; tb < TB; ++tb)
-                    mx = fmaxf(fmaxf(fmaxf(mx, s[rt][tb][0]), fmaxf(s[rt][tb][1], s[rt][tb][2])), s[rt][tb][3]);
-                mx = row_max(mx);
-                const float mc = mx == NEG_INF ? 0.f : mx * c;      // nothing seen yet: exp2(-inf) = 0 below
-                if (__any(mx > m[rt])) {
-                    const float f = __builtin_amdgcn_exp2f(m[rt] * c - mc);
-                    l[rt] *= f;
+                for (int vb = 0; vb < VB; ++vb) o[rt][vb] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            int32_t page_next = 0;
+            if (t_first < t_end) {
+                find_page(table[t_first >> A.c.page_shift]);
+                load_k(t_first);
+                page_next = table[min(t_first + kUnit, t_end - 1) >> A.c.page_shift];
+            }
+            for (int t = t_first; t < t_end; t += kUnit) {
+                const bool step_bad = bad, tail = t + kStep > q.len;
+                u32x4 vf[VB];
+                f32x4 vsc[2];
+                {
+                    const int at = t & page_mask;
+                    // an 8-bit piece holds 64 positions: its first or second half
+                    const unsigned char *src = (const unsigned char *)A.c.v + (chunk + (at & -(4 * W))) * (D * BITS / 8) +
+                                               (BITS == 8 ? (at & 32) / 4 : 0);
 #pragma unroll
-                    for (int vb = 0; vb < VB; ++vb) o[rt][vb] *= f;
-                    m[rt] = mx;
-                }
-                float sum = 0.f;
-                uint32_t hw[TB * 2], lw[TB * 2];
-#pragma unroll
-                for (int tb = 0; tb < TB; ++tb) {
-                    float p[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][tb][i], c, -mc));
-                        sum += p[i];
-                        if constexpr (BITS == 8) {
-                            const float x = p[i] * vsc[tb][i];
-                            p[i] = tail && s[rt][tb][i] == NEG_INF ? 0.f : x;
+                    for (int vb = 0; vb < VB; ++vb) {
+                        if constexpr (BITS == 16) {
+                            vf[vb] = *(const u32x4 *)(src + vb * 1024 + (uint32_t)lane * 16);
+                        } else {
+                            const u32x2 x = *(const u32x2 *)(src + vb * 1024 + (uint32_t)lane * 16);
+                            vf[vb][0] = x[0];
+                            vf[vb][1] = x[1];
                         }
                     }
+                    if constexpr (BITS == 8) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float a = p[2 * i], b = p[2 * i + 1];
-                        hw[tb * 2 + i] = dec::pack_hi16(a, b);
-                        lw[tb * 2 + i] = dec::pack_hi16(a - __uint_as_float(__float_as_uint(a) & 0xffff0000u),
-                                                        b - __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+                        for (int i = 0; i < 2; ++i)
+                            vsc[i] = *(const f32x4 *)(A.c.vs + chunk + at + i * 16 + (uint32_t)g * 4);
                     }
                 }
-                l[rt] += sum;
+
+                // scores
+                f32x4 s[RT][2];
 #pragma unroll
-                for (int j = 0; j < PB; ++j) {
-                    ph[rt][j] = as_bf16x8(u32x4{hw[4 * j], hw[4 * j + 1], hw[4 * j + 2], hw[4 * j + 3]});
-                    pl[rt][j] = as_bf16x8(u32x4{lw[4 * j], lw[4 * j + 1], lw[4 * j + 2], lw[4 * j + 3]});
+                for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        const u32x4 k4 = kf[i][kb];
+                        if constexpr (BITS == 16) {
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) s[rt][i] = dec::mfma(as_bf16x8(k4), qf[rt][kb], s[rt][i]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const bf16x8 a = codes_bf16(k4[2 * j], k4[2 * j + 1]);
+#pragma unroll
+                                for (int rt = 0; rt < RT; ++rt) s[rt][i] = dec::mfma(a, qf[rt][2 * kb + j], s[rt][i]);
+                            }
+                        }
+                    }
+                if constexpr (BITS == 8) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        s[rt][0] *= ksc[0];
+                        s[rt][1] *= ksc[1];
+                    }
                 }
-            }
-            if constexpr (BITS == 16) {
-                if (odd_v) {
-                    const uint16_t *vp = (const uint16_t *)A.c.v + ((step_chunk * D) << A.c.page_shift);
-                    const int last = min(TS, tokens - t);
-                    for (int tt = 0; tt < last; ++tt) {
-                        const int node = t + tt - q.len;
+                if (t + kUnit < t_end) {
+                    find_page(page_next);
+                    load_k(t + kUnit);
+                    page_next = table[min(t + 2 * kUnit, t_end - 1) >> A.c.page_shift];
+                }
+
+                if (__builtin_expect(tail || step_bad, 0)) {
+                    const int n0 = t - q.len;                       // node of the step's first position
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        // masked scores are -inf whatever k held
+                        const uint32_t vis = n0 <= -32 ? ~0u :
+                                             n0 <= 0 ? (uint32_t)((see[rt] << -n0) | ((1ull << -n0) - 1)) :
+                                             n0 < 64 ? (uint32_t)(see[rt] >> n0) : 0u;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float x = step_bad ? __uint_as_float(0x7fc00000u) : s[rt][i / 4][i % 4];
+                            s[rt][i / 4][i % 4] = vis >> (g * 4) & (1u << (i / 4 * 16 + i % 4)) ? x : NEG_INF;
+                        }
+                    }
+                    if constexpr (BITS == 16) {
+                        // v past the last position is 0.  A row's masked positions must
+                        // not reach it as 0 * NaN: v that is not finite leaves the
+                        // product and is added afterwards to the rows that see it.
+                        bool odd = false;
+                        const int left = q.rows - n0 - g * 4;
 #pragma unroll
                         for (int vb = 0; vb < VB; ++vb)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float x = kv::bf16_f32(
-                                    vp[kv::v_elem<D, W>((t & page_mask) + tt, vb * 16 + g * 4 + i)]);
-                                if (!(fabsf(x) < __builtin_inff())) {
-#pragma unroll
-                                    for (int rt = 0; rt < RT; ++rt)
-                                        if (node < 0 || (see[rt] >> (node & 63) & 1)) o[rt][vb][i] += x;
-                                }
+                            for (int e = 0; e < 4; ++e) {
+                                const int at = e / 2 * 16 + e % 2 * 2;
+                                uint32_t x = at < left ? at + 1 < left ? vf[vb][e] : vf[vb][e] & 0xffffu : 0u;
+                                const uint32_t keep = ((x & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
+                                                      ((x & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+                                odd |= keep != ~0u;
+                                vf[vb][e] = x & keep;
                             }
+                        odd_v |= __any(odd);
+                    } else {
+                        // no scales past the last position
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (n0 + i / 4 * 16 + g * 4 + i % 4 >= q.rows) vsc[i / 4][i % 4] = 0.f;
                     }
                 }
-            }
+                const auto reference = [&](int rt) {                // of this step alone
+                    float mx = NEG_INF;
 #pragma unroll
-            for (int vb = 0; vb < VB; ++vb)
-#pragma unroll
-                for (int j = 0; j < PB; ++j) {
-                    const bf16x8 a = BITS == 16 ? as_bf16x8(vf[vb]) : codes_bf16(vf[vb][2 * j], vf[vb][2 * j + 1]);
+                    for (int i = 0; i < 8; ++i) {
+                        float z = s[rt][i / 4][i % 4] * c;
+                        // a scale of 0 or NaN still has its sum in range
+                        if constexpr (BITS == 8) z += fmaxf(__builtin_amdgcn_logf(vsc[i / 4][i % 4]), -50.f) - kBase8;
+                        mx = fmaxf(mx, z);
+                    }
+                    return row_max(mx);
+                };
+                if (__builtin_expect(fresh, 0)) {
+                    bool none = false;
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
-                        o[rt][vb] = dec::mfma(a, ph[rt][j], o[rt][vb]);
-                        o[rt][vb] = dec::mfma(a, pl[rt][j], o[rt][vb]);
+                        if (m[rt] == NEG_INF) m[rt] = reference(rt);
+                        none |= m[rt] == NEG_INF;
                     }
-                    if constexpr (BITS == 8) __builtin_amdgcn_sched_barrier(0);
+                    fresh = __any(none);
                 }
-            t = t_next;
-        }
 
-        // ---- the token groups' results become one
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) l[rt] = row_sum(l[rt]);
-        if constexpr (TG > 1) {
-            if (g == 0) {
+                // scores become probabilities
+                u32x4 ph[RT], pl[RT];
+                bool rises[RT];
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    s_ml[w][rt][0][col] = m[rt];
-                    s_ml[w][rt][1][col] = l[rt];
+                    const float mc = zero_if_none(m[rt]);
+                    float p[8], sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][i / 4][i % 4], c, -mc));
+                        sum += p[i];
+                        if constexpr (BITS == 8) p[i] *= vsc[i / 4][i % 4];
+                    }
+                    if constexpr (BITS == 8) {
+                        if (__builtin_expect(tail, 0)) {            // 0 times a scale that is NaN, out of the row's sight
+                            asm volatile("");
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) p[i] = s[rt][i / 4][i % 4] == NEG_INF ? 0.f : p[i];
+                        }
+                    }
+                    rises[rt] = sum > kMostSum;
+                    if constexpr (BITS == 8)
+                        rises[rt] |= max3(max3(p[0], p[1], p[2]), max3(p[3], p[4], p[5]), fmaxf(p[6], p[7])) > kMostF16;
+                    l[rt] += sum;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float a = p[2 * i], b = p[2 * i + 1];
+                        if constexpr (BITS == 8) {
+                            ph[rt][i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+                        } else {
+                            ph[rt][i] = dec::pack_hi16(a, b);
+                            pl[rt][i] = dec::pack_hi16(a - __uint_as_float(__float_as_uint(a) & 0xffff0000u),
+                                                       b - __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+                        }
+                    }
+                }
+                bool any = false;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) any |= rises[rt];
+                if (__builtin_expect(__any(any), 0)) {
+                    // the rows concerned alone: the others' results stay the same to the bit
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        uint64_t of = __ballot(rises[rt]);
+                        of |= of >> 32;
+                        of |= of >> 16;
+                        const float up = fmaxf(m[rt], reference(rt));
+                        m[rt] = of >> col & 1 ? up : m[rt];
+                    }
+                    over = true;
+                    break;
+                }
+#pragma unroll
+                for (int vb = 0; vb < VB; ++vb) {
+                    if constexpr (BITS == 16) {
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) {
+                            o[rt][vb] = dec::mfma(as_bf16x8(vf[vb]), as_bf16x8(ph[rt]), o[rt][vb]);
+                            o[rt][vb] = dec::mfma(as_bf16x8(vf[vb]), as_bf16x8(pl[rt]), o[rt][vb]);
+                        }
+                    } else {
+                        const f16x8 a = codes_f16(vf[vb][0], vf[vb][1]);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            o[rt][vb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(f16x8, ph[rt]), o[rt][vb], 0, 0, 0);
+                    }
                 }
             }
-            __syncthreads();
+        } while (over);
+
+        if (BITS == 16 && __builtin_expect(odd_v, 0)) {
+            // the wave's steps among the request's own rows
+            for (int t = t_first; t < t_end; t += kUnit) {
+                if (t + kStep <= q.len) continue;
+                const int64_t page = table[t >> A.c.page_shift];
+                if (page < 0 || page >= A.c.pages) continue;        // its scores are NaN already
+                const uint16_t *vp = (const uint16_t *)A.c.v + (((page * A.c.heads + head) * D) << A.c.page_shift);
+                const int last = min(kStep, tokens - t);
+                for (int tt = 0; tt < last; ++tt) {
+                    const int node = t + tt - q.len;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                float mx = NEG_INF, sum = 0.f;
+                    for (int vb = 0; vb < VB; ++vb)
 #pragma unroll
-                for (int k = 0; k < TG; ++k) mx = fmaxf(mx, s_ml[k * RG + rg][rt][0][col]);
-                const float mc = mx == NEG_INF ? 0.f : mx * c;
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = kv::bf16_f32(vp[kv::v_elem<D, W>((t & page_mask) + tt, vb * 16 + g * 4 + i)]);
+                            if (!(fabsf(x) < __builtin_inff())) {
 #pragma unroll
-                for (int k = 0; k < TG; ++k)
-                    sum += s_ml[k * RG + rg][rt][1][col] * __builtin_amdgcn_exp2f(s_ml[k * RG + rg][rt][0][col] * c - mc);
-                const float f = __builtin_amdgcn_exp2f(m[rt] * c - mc);
-#pragma unroll
-                for (int vb = 0; vb < VB; ++vb) s_o[w][(rt * VB + vb) * 64 + lane] = o[rt][vb] * f;
-                m[rt] = mx;
-                l[rt] = sum;
+                                for (int rt = 0; rt < RT; ++rt)
+                                    if (node < 0 || (see[rt] >> (node & 63) & 1)) o[rt][vb][i] += x;
+                            }
+                        }
+                }
             }
-            __syncthreads();
         }
 
-        // ---- output rows, or partial sums: wave tg of a row group writes every TG-th tile
-        const bool whole = n == un.per_seg;
-        const int64_t slot = ((int64_t)blockIdx.x * 2 + (v0 == 0 ? 1 : 0)) * RG + rg;
+        // ---- The waves' results become one: through LDS each takes every eighth
+        // output tile, of all waves.
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            const int rr = row_base + rt * 16 + col, node = rr / A.rep;
-            const bool in = node < q.rows;
-            uint16_t *dst = A.out + (int64_t)(q.row0 + node) * A.ldo + (head * A.rep + rr - node * A.rep) * D;
+            l[rt] = row_sum(l[rt]);
+            if (g == 0) s_ml[w][rt][col] = float2{m[rt], l[rt]};
+#pragma unroll
+            for (int vb = 0; vb < VB; ++vb) s_o[w][(rt * VB + vb) * 64 + lane] = o[rt][vb];
+        }
+        __syncthreads();
+        const bool whole = n == un.per_seg;
+        const auto piece = [&](int of, bool starts) {               // of a group's part of the segment
+            return A.part + (((int64_t)of * A.blocks + rb) * 2 + starts) * attn_piece(D, RT);
+        };
+        const auto finish = [&](f32x4 z, float sum, int tile) {
+            const int rr = row_base + tile / VB * 16 + col, node = (int)((rr + 0.5f) * per_rep);
             // a row that sees nothing is 0; one whose length is a fault is NaN
-            const float inv = !q.ok ? __uint_as_float(0x7fc00000u) : l[rt] == 0.f ? 0.f : 1.f / l[rt];
+            const float inv = !q.ok ? __uint_as_float(0x7fc00000u) : sum == 0.f ? 0.f : 1.f / sum;
+            uint16_t *dst = A.out + (int64_t)(q.row0 + node) * A.ldo + (head * A.rep + rr - node * A.rep) * D;
+            if (rr < rows) store_out(dst + tile % VB * 16 + g * 4, z * inv);
+        };
+#pragma unroll 1
+        for (int tile = w; tile < RT * VB; tile += WAVES) {
+            float2 ml[WAVES];
+            float mx = NEG_INF, sum = 0.f;
 #pragma unroll
-            for (int vb = 0; vb < VB; ++vb) {
-                if (TG > 1 && vb % TG != tg) continue;
-                f32x4 x = o[rt][vb];
-                if constexpr (TG > 1) {
-                    x = s_o[rg][(rt * VB + vb) * 64 + lane];
-#pragma unroll
-                    for (int k = 1; k < TG; ++k) x += s_o[k * RG + rg][(rt * VB + vb) * 64 + lane];
-                }
-                if (whole) {
-                    x *= inv;
-                    if (in) {
-                        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                        u32x2 y;
-                        y[0] = (uint32_t)dec::f2bf16(x[0]) | (uint32_t)dec::f2bf16(x[1]) << 16;
-                        y[1] = (uint32_t)dec::f2bf16(x[2]) | (uint32_t)dec::f2bf16(x[3]) << 16;
-                        *(u32x2 *)(dst + vb * 16 + g * 4) = y;
-                    }
-                } else {
-                    *((f32x4 *)(A.part + slot * slot_floats<D, RT>()) + (rt * VB + vb) * 64 + lane) = x;
-                }
+            for (int k = 0; k < WAVES; ++k) {
+                ml[k] = s_ml[k][tile / VB][col];
+                mx = fmaxf(mx, ml[k].x);
             }
-            if (!whole && tg == 0 && g == 0) {
-                float *ml = A.part_ml + (slot * RT + rt) * 32;
-                ml[col] = m[rt];
-                ml[16 + col] = l[rt];
+            const float mc = zero_if_none(mx);
+            f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < WAVES; ++k) {
+                const float f = __builtin_amdgcn_exp2f(ml[k].x - mc);
+                sum += ml[k].y * f;
+                z += s_o[k][tile * 64 + lane] * f;
+            }
+            if (whole) {
+                finish(z, sum, tile);
+            } else {
+                // every tile with its own copy of its rows' statistics, so that
+                // a wave waits for nothing but its own stores
+                float *const p = piece(group, v0 == 0) + tile * kTileFloats;
+                put4(p, lane, z);
+                if (g == 0) put2(p + 256 + col * 2, mx, sum);
             }
         }
-        if constexpr (TG > 1) __syncthreads();                      // the buffers are free for the next segment
+        if (!whole && w < RT * VB) {
+            // Count in; the last to come adds the pieces of the wave's tiles, in
+            // group order.  A group starts at most one shared segment.
+            wait_stores();
+            const int s0 = u - v0, w0 = R.owner(s0), w1 = R.owner(s0 + un.per_seg - 1);
+            uint32_t *const ctr = A.counters + (w0 * A.blocks + rb) * WAVES + w;
+            uint32_t ticket = 0;
+            if (lane == 0) ticket = __hip_atomic_fetch_add(ctr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (__builtin_amdgcn_readfirstlane(ticket) == (uint32_t)(w1 - w0)) {
+                if (lane == 0) __hip_atomic_store(ctr, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                constexpr int XB = 16 / NT;                         // pieces in flight
+                float mx[NT], sum[NT];
+                f32x4 z[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    mx[j] = NEG_INF;
+                    sum[j] = 0.f;
+                    z[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+#pragma unroll 1
+                for (int k0 = w0; k0 <= w1; k0 += XB) {
+                    f32x4 x[XB][NT];
+                    float xm[XB][NT], xl[XB][NT];
+#pragma unroll
+                    for (int i = 0; i < XB; ++i) {
+                        const int k = min(k0 + i, w1);
+                        const float *src = piece(k, k == w0);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const float *p = src + (w + j * WAVES) * kTileFloats;
+                            x[i][j] = get4(p, lane);
+                            get2(p + 256 + col * 2, xm[i][j], xl[i][j]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        float mn = mx[j];
+#pragma unroll
+                        for (int i = 0; i < XB; ++i) mn = fmaxf(mn, xm[i][j]);
+                        const float mc = zero_if_none(mn), f = __builtin_amdgcn_exp2f(mx[j] - mc);
+                        z[j] *= f;
+                        sum[j] *= f;
+                        mx[j] = mn;
+#pragma unroll
+                        for (int i = 0; i < XB; ++i) {
+                            // a repeated last piece is left out
+                            const bool real = k0 + i <= w1;
+                            const float fk = __builtin_amdgcn_exp2f(xm[i][j] - mc);
+                            sum[j] += real ? xl[i][j] * fk : 0.f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) z[j][e] += real ? x[i][j][e] * fk : 0.f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) finish(z[j], sum[j], w + j * WAVES);
+            }
+        }
+        __syncthreads();                                            // the buffers are free for the next segment
         u += n;
     }
 }
 
-// Adds the partial sums of segments that several workgroups share.  A
-// workgroup of this kernel takes 16 rows and 32 dimensions of one segment;
-// its waves take every fourth contributor and are joined through LDS.
-template <int D, int RT, int RG>
-__global__ __launch_bounds__(TPB) void attn_join_kernel(const AttnArgs A, const int unit, const int blocks) {
-    constexpr int VB = D / 16, BR = RG * RT * 16;
-    __shared__ float s_ml[kWaves][2][16];
-    __shared__ f32x4 s_o[kWaves][2][64];
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = lane & 15, g = lane >> 4;
-    int at = blockIdx.x;
-    const int vp = at % (VB / 2);
-    at /= VB / 2;
-    const int rt = at % RT;
-    at /= RT;
-    const int rg = at % RG;
-    at /= RG;
-    const int rb = at % blocks;
-    at /= blocks;
-    const int head = at % A.c.heads, r = at / A.c.heads;
-    const kv::Req q = kv::request(A.B, A.c.page_shift, r);
-    const Units un = units_of(A, q, unit, BR);
-    if (rb >= un.blocks || rb * BR + (rg * RT + rt) * 16 >= q.rows * A.rep) return;
-    int total = 0, first = 0;
-    for (int base = 0; base < A.B.b; base += 64) {
-        int x = 0;
-        if (base + lane < A.B.b) x = units_of(A, kv::request(A.B, A.c.page_shift, base + lane), unit, BR).total;
-        first += wave_sum(base + lane < r ? x : 0);
-        total += wave_sum(x);
-    }
-    const Ranges R{total / A.grid, total % A.grid};
-    first += (head * un.blocks + rb) * un.per_seg;
-    const int w0 = R.owner(first), w1 = R.owner(first + un.per_seg - 1);
-    if (w0 == w1) return;                                           // written by its only workgroup
-    const float c = A.scale;
-    float m = NEG_INF, l = 0.f;
-    f32x4 o[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-    for (int k = w0 + w; k <= w1; k += kWaves) {
-        const int64_t slot = ((int64_t)k * 2 + (k == w0 ? 1 : 0)) * RG + rg;
-        const float *ml = A.part_ml + (slot * RT + rt) * 32;
-        const f32x4 *po = (const f32x4 *)(A.part + slot * slot_floats<D, RT>()) + (rt * VB + vp * 2) * 64 + lane;
-        const float mk = ml[col], lk = ml[16 + col];
-        const f32x4 x0 = po[0], x1 = po[64];
-        const float mx = fmaxf(m, mk), mc = mx == NEG_INF ? 0.f : mx * c;
-        const float f = __builtin_amdgcn_exp2f(m * c - mc), fk = __builtin_amdgcn_exp2f(mk * c - mc);
-        o[0] = o[0] * f + x0 * fk;
-        o[1] = o[1] * f + x1 * fk;
-        l = l * f + lk * fk;
-        m = mx;
-    }
-    if (g == 0) {
-        s_ml[w][0][col] = m;
-        s_ml[w][1][col] = l;
-    }
-    s_o[w][0][lane] = o[0];
-    s_o[w][1][lane] = o[1];
-    __syncthreads();
-    if (w >= 2) return;
-    float mx = NEG_INF;
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) mx = fmaxf(mx, s_ml[k][0][col]);
-    const float mc = mx == NEG_INF ? 0.f : mx * c;
-    float sum = 0.f;
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) {
-        const float f = __builtin_amdgcn_exp2f(s_ml[k][0][col] * c - mc);
-        sum += s_ml[k][1][col] * f;
-        x += s_o[k][w][lane] * f;
-    }
-    const int rr = rb * BR + (rg * RT + rt) * 16 + col, node = rr / A.rep;
-    if (node >= q.rows) return;
-    x *= sum == 0.f ? 0.f : 1.f / sum;
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    u32x2 y;
-    y[0] = (uint32_t)dec::f2bf16(x[0]) | (uint32_t)dec::f2bf16(x[1]) << 16;
-    y[1] = (uint32_t)dec::f2bf16(x[2]) | (uint32_t)dec::f2bf16(x[3]) << 16;
-    *(u32x2 *)(A.out + (int64_t)(q.row0 + node) * A.ldo + (head * A.rep + rr - node * A.rep) * D + (vp * 2 + w) * 16 +
-               g * 4) = y;
-}
-
-template <int D, int BITS, int RT, int RG>
-hipError_t launch(const AttnArgs &A, const AttnPlan &p, hipStream_t s) {
-    hipLaunchKernelGGL((tree_attn_kernel<D, BITS, RT, RG>), dim3(p.grid), dim3(TPB), 0, s, A,
-                       A.B.page_table);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !p.split) return e;
-    const int grid = A.B.b * A.c.heads * p.blocks * RG * RT * (D / 32);
-    hipLaunchKernelGGL((attn_join_kernel<D, RT, RG>), dim3(grid), dim3(TPB), 0, s, A, p.unit, p.blocks);
-    return hipGetLastError();
-}
-
 template <int D, int BITS>
-hipError_t by_rows(const AttnArgs &A, const AttnPlan &p, hipStream_t s) {
-    if constexpr (D == 256) {
-        if (p.rg == 4) return launch<D, BITS, 2, 4>(A, p, s);
-        if (p.rg == 2) return launch<D, BITS, 2, 2>(A, p, s);
-    } else {
-        if (p.rg == 4) return launch<D, BITS, 4, 4>(A, p, s);
-        if (p.rg == 2) return p.rt == 3 ? launch<D, BITS, 3, 2>(A, p, s) : launch<D, BITS, 4, 2>(A, p, s);
-        if (p.rt == 4) return launch<D, BITS, 4, 1>(A, p, s);
-    }
-    return p.rt == 1 ? launch<D, BITS, 1, 1>(A, p, s) : launch<D, BITS, 2, 1>(A, p, s);
+hipError_t launch(const AttnArgs &A, int grid, hipStream_t s) {
+    if (A.tiles == 1)
+        hipLaunchKernelGGL((tree_attn_kernel<D, BITS, 1>), dim3(grid), dim3(TPB), 0, s, A, A.B.page_table);
+    else
+        hipLaunchKernelGGL((tree_attn_kernel<D, BITS, attn_tiles(D)>), dim3(grid), dim3(TPB), 0, s, A, A.B.page_table);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_tree_attention(const AttnArgs &A, const AttnPlan &p, hipStream_t s) {
+hipError_t launch_tree_attention(const AttnArgs &A, hipStream_t s) {
+    const int grid = A.groups * A.blocks;
     if (A.c.bits == 16)
-        return A.c.d == 64 ? by_rows<64, 16>(A, p, s) : A.c.d == 128 ? by_rows<128, 16>(A, p, s) : by_rows<256, 16>(A, p, s);
-    return A.c.d == 64 ? by_rows<64, 8>(A, p, s) : A.c.d == 128 ? by_rows<128, 8>(A, p, s) : by_rows<256, 8>(A, p, s);
+        return A.c.d == 64 ? launch<64, 16>(A, grid, s) : A.c.d == 128 ? launch<128, 16>(A, grid, s) : launch<256, 16>(A, grid, s);
+    return A.c.d == 64 ? launch<64, 8>(A, grid, s) : A.c.d == 128 ? launch<128, 8>(A, grid, s) : launch<256, 8>(A, grid, s);
 }
 
 }  // namespace dspk

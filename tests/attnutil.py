@@ -129,8 +129,7 @@ def run_attention(R: Round, q, hq, masks=None, scale=None, out=None, ws=None):
     if out is None:
         out = torch.full((q.shape[0], hq * R.d), 7.0, dtype=torch.bfloat16, device="cuda")
     if ws is None:
-        ws = torch.full((binding.attn_workspace_bytes(hq, R.heads, R.d, len(R.lens), R.max_rows),), 255,
-                        dtype=torch.uint8, device="cuda")
+        ws = binding.alloc_workspace(binding.attn_workspace_bytes(hq, R.heads, R.d, len(R.lens), R.max_rows))
     binding.tree_attention(R.cache, R.batch, qd, hq, out, ws, scale, None if masks is None else masks_dev(masks))
     torch.cuda.synchronize()
     return out.float().cpu().numpy().reshape(q.shape[0], -1, R.d)

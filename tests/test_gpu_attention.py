@@ -250,3 +250,51 @@ def test_on_another_stream():
     binding.tree_attention(R.cache, R.batch, qd, 8, out, ws, stream=s)
     s.synchronize()
     assert np.array_equal(out.float().cpu().numpy().reshape(want.shape), want)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("m", [1, 17])
+def test_scores_that_rise_along_the_context(bits, m):
+    """Maxima that rise by far more than a reference may lag, by and by and at
+    once, and v scales that grow by orders of magnitude with them."""
+    import torch
+    hkv, d, n = 1, 128, 3000
+    R = Round([n], [m], hkv, d, bits, 64, seed=11)
+    q = _q(R, 4)
+    k, v = R.rng.normal(0, 1, (n + m, hkv, d)), R.rng.normal(0, 1, (n + m, hkv, d))
+    lift = np.linspace(0, 6, n + m) + 4 * (np.arange(n + m) > 2000)
+    k += lift[:, None, None] * bf16(q[0, 0])[None, None] * 0.3           # one head's scores rise by some 300
+    v *= 2.0 ** (lift * 4)[:, None, None]
+    k, v = bf16(k), bf16(v)
+    binding.kv_append(R.cache, binding.AttnBatch(i32([0]), R.table, n + m),
+                      *(dev(x.reshape(n + m, -1), torch.bfloat16) for x in (k, v)))
+    if bits == 8:
+        (ck, sk), (cv, sv) = oa.quantise_rows(k), oa.quantise_rows(v)
+        k, v = ck * sk[..., None].astype(np.float64), cv * sv[..., None].astype(np.float64)
+    got = run_attention(R, q, 4)
+    for i in (0, m - 1):
+        ref, mag = oa.attention(q[i:i + 1], k[:n + i + 1], v[:n + i + 1], n + i, [1], d ** -0.5)
+        # a score's error is 128 * 2^-24 * scale * sum|q k|, some 50 times that of the usual inputs
+        big = np.abs(q[i]) @ np.abs(k[:n + i + 1, 0]).T * d ** -0.5
+        err = np.abs(got[i] - ref[0])
+        tol = 2.0 ** -8 * np.abs(ref[0]) + (2.0 ** -11.5 + 2 * 128 * 2.0 ** -24 * big.max()) * mag[0]
+        assert (err <= tol).all(), (err / tol).max()
+
+
+def test_rows_of_zeros_in_an_8bit_cache():
+    """Scales that are all zero: k of zeros gives even weights, v of zeros a zero."""
+    import torch
+    R = Round([70], [3], 2, 64, 8, 64, seed=12)
+    q = _q(R, 4)
+    z = torch.zeros((73, 128), dtype=torch.bfloat16, device="cuda")
+    every = binding.AttnBatch(i32([0]), R.table, 73)
+    v = dev(R.v[0].reshape(73, -1).astype(np.float32), torch.bfloat16)
+    binding.kv_append(R.cache, every, z, v)
+    vo, ko = torch.empty((73, 128), device="cuda"), torch.empty((73, 128), device="cuda")
+    binding.kv_read(R.cache, every, ko, vo)
+    got = run_attention(R, q, 4)
+    held = vo.cpu().numpy().reshape(73, 2, 64)
+    ref, mag = oa.attention(q, np.zeros((73, 2, 64)), held, 70, chain_masks(3), 0.125)
+    assert_attention(got, ref, mag)
+    binding.kv_append(R.cache, every, z, z)
+    assert (run_attention(R, q, 4) == 0).all()
