@@ -43,6 +43,7 @@ using kv::f32x4;
 using kv::u32x4;
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -140,29 +141,38 @@ struct Ranges {
         return u < cut ? u / (q + 1) : rem + (u - cut) / q;
     }
 };
-// First unit of a group's range and what holds it: the range's bounds,
-// the request and that request's first unit.  Every wave does it by itself;
-// requests are taken 64 at a time, one per lane.
+// A group's range, and where it starts: the request that holds its first unit
+// and that request's first unit.  Every wave does it by itself; requests are
+// taken 64 at a time, one per lane.
 struct Start {
     int u, u_end, req, first;
+    kv::Req q;
 };
+__device__ __forceinline__ int prefix_sum(int x) {                  // inclusive, over the lanes
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
 __device__ __forceinline__ Start find_start(const AttnArgs &A, int group, Ranges &R) {
     const int lane = threadIdx.x & 63;
     int total = 0, x = 0, u = 0;
-    for (int base = 0; base < A.B.b; base += 64) {
+    kv::Req q = {};
+    const auto load = [&](int base) {
         u = 0;
-        if (base + lane < A.B.b) u = units_of(A, kv::request(A.B, A.c.page_shift, base + lane)).total;
-        x = u;                                                      // inclusive prefix sum
-        if (A.B.b > 1) {
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int y = __shfl_up(x, o);
-                if (lane >= o) x += y;
-            }
-            total += __builtin_amdgcn_readlane(x, 63);
-        } else {
-            total = __builtin_amdgcn_readfirstlane(x);
+        if (base + lane < A.B.b) {
+            q = kv::request(A.B, A.c.page_shift, base + lane);
+            u = units_of(A, q).total;
         }
+        x = A.B.b > 1 ? prefix_sum(u) : u;
+    };
+    const int last = A.B.b > 1 ? 63 : 0;
+    for (int base = 0; base < A.B.b; base += 64) {
+        load(base);
+        total += __builtin_amdgcn_readlane(x, last);
     }
     // fewer than two units each: two to some, which is no slower and leaves fewer pieces
     const int groups = total > A.groups && total < 2 * A.groups ? (total + 1) / 2 : A.groups;
@@ -172,28 +182,25 @@ __device__ __forceinline__ Start find_start(const AttnArgs &A, int group, Ranges
     s.u = min(R.begin(group), total);
     s.u_end = min(R.begin(group + 1), total);
     s.req = s.first = 0;
-    if (A.B.b == 1 || s.u >= s.u_end) return s;
-    int sum = 0;
-    for (int base = 0; base < A.B.b; base += 64) {
-        if (A.B.b > 64) {                                           // else x and u are those of the only 64
-            u = 0;
-            if (base + lane < A.B.b) u = units_of(A, kv::request(A.B, A.c.page_shift, base + lane)).total;
-            x = u;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int y = __shfl_up(x, o);
-                if (lane >= o) x += y;
+    int l = 0;
+    if (A.B.b > 1 && s.u < s.u_end) {
+        int sum = 0;
+        for (int base = 0;; base += 64) {                           // ends: the unit is one of total
+            if (A.B.b > 64) load(base);                             // else x, u and q are those of the only 64
+            const uint64_t past = __ballot(sum + x > s.u);
+            if (past || base + 64 >= A.B.b) {
+                l = past ? __ffsll((unsigned long long)past) - 1 : 0;
+                s.req = base + l;
+                s.first = sum + __builtin_amdgcn_readlane(x - u, l);
+                break;
             }
+            sum += __builtin_amdgcn_readlane(x, 63);
         }
-        const uint64_t past = __ballot(sum + x > s.u);
-        if (past) {
-            const int l = __ffsll((unsigned long long)past) - 1;
-            s.req = base + l;
-            s.first = sum + __builtin_amdgcn_readlane(x - u, l);
-            return s;
-        }
-        sum += __builtin_amdgcn_readlane(x, 63);
     }
+    s.q.row0 = __builtin_amdgcn_readlane(q.row0, l);
+    s.q.rows = __builtin_amdgcn_readlane(q.rows, l);
+    s.q.len = __builtin_amdgcn_readlane(q.len, l);
+    s.q.ok = __builtin_amdgcn_readlane(q.ok, l);
     return s;
 }
 
@@ -202,7 +209,6 @@ __device__ __forceinline__ Start find_start(const AttnArgs &A, int group, Ranges
 // accesses, laid out [half][lane].
 __device__ __forceinline__ void put4(float *tile, int lane, f32x4 v) {
     unsigned long long *q = (unsigned long long *)tile;
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
     __hip_atomic_store(q + lane, __builtin_bit_cast(unsigned long long, f32x2{v[0], v[1]}), __ATOMIC_RELAXED,
                        __HIP_MEMORY_SCOPE_AGENT);
     __hip_atomic_store(q + 64 + lane, __builtin_bit_cast(unsigned long long, f32x2{v[2], v[3]}), __ATOMIC_RELAXED,
@@ -210,18 +216,15 @@ __device__ __forceinline__ void put4(float *tile, int lane, f32x4 v) {
 }
 __device__ __forceinline__ f32x4 get4(const float *tile, int lane) {
     const unsigned long long *q = (const unsigned long long *)tile;
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
     const f32x2 a = __builtin_bit_cast(f32x2, __hip_atomic_load(q + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     const f32x2 b = __builtin_bit_cast(f32x2, __hip_atomic_load(q + 64 + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     return f32x4{a[0], a[1], b[0], b[1]};
 }
 __device__ __forceinline__ void put2(float *p, float a, float b) {
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
     __hip_atomic_store((unsigned long long *)p, __builtin_bit_cast(unsigned long long, f32x2{a, b}), __ATOMIC_RELAXED,
                        __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void get2(const float *p, float &a, float &b) {
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
     const f32x2 x = __builtin_bit_cast(f32x2, __hip_atomic_load((const unsigned long long *)p, __ATOMIC_RELAXED,
                                                                 __HIP_MEMORY_SCOPE_AGENT));
     a = x[0];
@@ -254,6 +257,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
     constexpr int VB = D / 16;                      // v pieces of a step, output tiles of a row tile
     constexpr int NT = (RT * VB + WAVES - 1) / WAVES;               // output tiles that a wave joins
     constexpr int BR = RT * 16;
+    constexpr bool AHEAD = D * BITS < 256 * 16;     // else k and v of a step do not fit the registers together
     __shared__ float2 s_ml[WAVES][RT][16];
     __shared__ f32x4 s_o[WAVES][RT * VB * 64];
 
@@ -264,24 +268,25 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
     const int at = xcd * each + min(xcd, more) + blockIdx.x / 8;
     const int group = A.blocks == 1 ? at : at / A.blocks, rb = A.blocks == 1 ? 0 : at - group * A.blocks;
     Ranges R;
-    const Start st = find_start(A, group, R);
+    Start st = find_start(A, group, R);
     int u = __builtin_amdgcn_readfirstlane(st.u), req = __builtin_amdgcn_readfirstlane(st.req),
         rfirst = __builtin_amdgcn_readfirstlane(st.first);
     const int u_end = __builtin_amdgcn_readfirstlane(st.u_end);
+    kv::Req q = st.q;
+    Units un = units_of(A, q);
     const int page_mask = (1 << A.c.page_shift) - 1;
     const float c = A.scale, per_rep = 1.f / A.rep;
     const int row_base = rb * BR;                   // first of the rows (node * rep + q head)
 
     while (u < u_end) {
-        kv::Req q = kv::request(A.B, A.c.page_shift, req);
-        q.row0 = __builtin_amdgcn_readfirstlane(q.row0);
-        q.rows = __builtin_amdgcn_readfirstlane(q.rows);
-        q.len = __builtin_amdgcn_readfirstlane(q.len);
-        q.ok = __builtin_amdgcn_readfirstlane(q.ok);
-        const Units un = units_of(A, q);
-        if (u - rfirst >= un.total) {               // also past requests without rows
+        if (u - rfirst >= un.total) {               // the next request, also past those without rows
             rfirst += un.total;
-            ++req;
+            q = kv::request(A.B, A.c.page_shift, ++req);
+            q.row0 = __builtin_amdgcn_readfirstlane(q.row0);
+            q.rows = __builtin_amdgcn_readfirstlane(q.rows);
+            q.len = __builtin_amdgcn_readfirstlane(q.len);
+            q.ok = __builtin_amdgcn_readfirstlane(q.ok);
+            un = units_of(A, q);
             continue;
         }
         const int head = (u - rfirst) / un.per_seg, v0 = u - rfirst - head * un.per_seg;
@@ -291,20 +296,6 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
         if (row_base >= rows) {                     // a request of fewer row blocks
             u += n;
             continue;
-        }
-
-        // q operands and masks of the wave's rows; those past the last repeat it and are not written
-        bf16x8 qf[RT][QB];
-        uint64_t see[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int rr = min(row_base + rt * 16 + col, rows - 1), node = (int)((rr + 0.5f) * per_rep);
-            const uint16_t *p = A.q + (int64_t)(q.row0 + node) * A.ldq + (head * A.rep + rr - node * A.rep) * D +
-                                g * (BITS == 16 ? 8 : 16);
-#pragma unroll
-            for (int kb = 0; kb < QB; ++kb)
-                qf[rt][kb] = as_bf16x8(*(const u32x4 *)(p + (BITS == 16 ? kb * 32 : kb / 2 * 64 + kb % 2 * 8)));
-            see[rt] = (A.mask != nullptr ? A.mask[q.row0 + node] : (2ull << node) - 1) & ((2ull << (q.rows - 1)) - 1);
         }
 
         // Outputs and sum of each row, in units of 2^m: m is the row's reference,
@@ -321,7 +312,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
         // A step takes 32 positions from t.  Pages that are none of the cache's
         // make every row that sees them NaN; page 0 is read in their place.
         // Page numbers are loaded a step ahead of the k that needs them, k a
-        // step ahead of its use, v at the step's start.
+        // step ahead of its use (AHEAD), v at the step's start.
         const int32_t *const table = page_table + (int64_t)req * A.B.max_pages;
         u32x4 kf[2][KB];
         f32x4 ksc[2];
@@ -343,6 +334,22 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
         };
 
         const int t_first = v0 * kUnit + w * kStep, t_end = min((v0 + n) * kUnit, tokens);
+        const int32_t page_first = t_first < t_end ? table[t_first >> A.c.page_shift] : 0;
+
+        // q operands and masks of the wave's rows; those past the last repeat it and are not written
+        bf16x8 qf[RT][QB];
+        uint64_t see[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int rr = min(row_base + rt * 16 + col, rows - 1), node = (int)((rr + 0.5f) * per_rep);
+            const uint16_t *p = A.q + (int64_t)(q.row0 + node) * A.ldq + (head * A.rep + rr - node * A.rep) * D +
+                                g * (BITS == 16 ? 8 : 16);
+#pragma unroll
+            for (int kb = 0; kb < QB; ++kb)
+                qf[rt][kb] = as_bf16x8(*(const u32x4 *)(p + (BITS == 16 ? kb * 32 : kb / 2 * 64 + kb % 2 * 8)));
+            see[rt] = (A.mask != nullptr ? A.mask[q.row0 + node] : (2ull << node) - 1) & ((2ull << (q.rows - 1)) - 1);
+        }
+
         bool over, odd_v = false;
         do {
             over = false;
@@ -355,15 +362,15 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
             }
             int32_t page_next = 0;
             if (t_first < t_end) {
-                find_page(table[t_first >> A.c.page_shift]);
-                load_k(t_first);
+                find_page(page_first);
+                if constexpr (AHEAD) load_k(t_first);
                 page_next = table[min(t_first + kUnit, t_end - 1) >> A.c.page_shift];
             }
             for (int t = t_first; t < t_end; t += kUnit) {
                 const bool step_bad = bad, tail = t + kStep > q.len;
                 u32x4 vf[VB];
                 f32x4 vsc[2];
-                {
+                const auto load_v = [&] {
                     const int at = t & page_mask;
                     // an 8-bit piece holds 64 positions: its first or second half
                     const unsigned char *src = (const unsigned char *)A.c.v + (chunk + (at & -(4 * W))) * (D * BITS / 8) +
@@ -383,7 +390,8 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                         for (int i = 0; i < 2; ++i)
                             vsc[i] = *(const f32x4 *)(A.c.vs + chunk + at + i * 16 + (uint32_t)g * 4);
                     }
-                }
+                };
+                if constexpr (AHEAD) load_v(); else load_k(t);
 
                 // scores
                 f32x4 s[RT][2];
@@ -406,21 +414,27 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                             }
                         }
                     }
-                if constexpr (BITS == 8) {
+                // to log2: scale times k's scale, or with masks scale alone
+                f32x4 kc[2];
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        s[rt][0] *= ksc[0];
-                        s[rt][1] *= ksc[1];
-                    }
-                }
+                for (int i = 0; i < 2; ++i) kc[i] = BITS == 8 ? ksc[i] * c : f32x4{c, c, c, c};
+                if constexpr (!AHEAD) load_v();
                 if (t + kUnit < t_end) {
                     find_page(page_next);
-                    load_k(t + kUnit);
+                    if constexpr (AHEAD) load_k(t + kUnit);
                     page_next = table[min(t + 2 * kUnit, t_end - 1) >> A.c.page_shift];
                 }
 
                 if (__builtin_expect(tail || step_bad, 0)) {
                     const int n0 = t - q.len;                       // node of the step's first position
+                    if constexpr (BITS == 8) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) s[rt][i] *= kc[i];
+                            kc[i] = f32x4{1.f, 1.f, 1.f, 1.f};
+                        }
+                    }
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
                         // masked scores are -inf whatever k held
@@ -462,7 +476,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                     float mx = NEG_INF;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        float z = s[rt][i / 4][i % 4] * c;
+                        float z = s[rt][i / 4][i % 4] * kc[i / 4][i % 4];
                         // a scale of 0 or NaN still has its sum in range
                         if constexpr (BITS == 8) z += fmaxf(__builtin_amdgcn_logf(vsc[i / 4][i % 4]), -50.f) - kBase8;
                         mx = fmaxf(mx, z);
@@ -488,7 +502,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                     float p[8], sum = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][i / 4][i % 4], c, -mc));
+                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][i / 4][i % 4], kc[i / 4][i % 4], -mc));
                         sum += p[i];
                         if constexpr (BITS == 8) p[i] *= vsc[i / 4][i % 4];
                     }
@@ -507,7 +521,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                     for (int i = 0; i < 4; ++i) {
                         const float a = p[2 * i], b = p[2 * i + 1];
                         if constexpr (BITS == 8) {
-                            ph[rt][i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+                            ph[rt][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), f16x2));
                         } else {
                             ph[rt][i] = dec::pack_hi16(a, b);
                             pl[rt][i] = dec::pack_hi16(a - __uint_as_float(__float_as_uint(a) & 0xffff0000u),
@@ -519,17 +533,21 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) any |= rises[rt];
                 if (__builtin_expect(__any(any), 0)) {
-                    // the rows concerned alone: the others' results stay the same to the bit
+                    // The rows concerned alone: the others' results stay the same to
+                    // the bit.  A reference that this step has raised already does not
+                    // rise again (one so large that log2 of a scale is lost in it still
+                    // lets the limit be passed), so every step restarts at most once per row.
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
                         uint64_t of = __ballot(rises[rt]);
                         of |= of >> 32;
                         of |= of >> 16;
-                        const float up = fmaxf(m[rt], reference(rt));
-                        m[rt] = of >> col & 1 ? up : m[rt];
+                        const float up = reference(rt);
+                        const bool higher = (of >> col & 1) && up > m[rt];
+                        m[rt] = higher ? up : m[rt];
+                        over |= __any(higher) != 0;
                     }
-                    over = true;
-                    break;
+                    if (over) break;
                 }
 #pragma unroll
                 for (int vb = 0; vb < VB; ++vb) {
@@ -632,7 +650,6 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
             if (lane == 0) ticket = __hip_atomic_fetch_add(ctr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             if (__builtin_amdgcn_readfirstlane(ticket) == (uint32_t)(w1 - w0)) {
                 if (lane == 0) __hip_atomic_store(ctr, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                constexpr int XB = 16 / NT;                         // pieces in flight
                 float mx[NT], sum[NT];
                 f32x4 z[NT];
 #pragma unroll
@@ -641,8 +658,8 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                     sum[j] = 0.f;
                     z[j] = f32x4{0.f, 0.f, 0.f, 0.f};
                 }
-#pragma unroll 1
-                for (int k0 = w0; k0 <= w1; k0 += XB) {
+                const auto add = [&](auto most, int k0) {           // pieces k0 .., all in flight
+                    constexpr int XB = most();
                     f32x4 x[XB][NT];
                     float xm[XB][NT], xl[XB][NT];
 #pragma unroll
@@ -675,6 +692,13 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                             for (int e = 0; e < 4; ++e) z[j][e] += real ? x[i][j][e] * fk : 0.f;
                         }
                     }
+                };
+                if (w1 - w0 < 4) {
+                    add(std::integral_constant<int, 4>(), w0);
+                } else {
+                    constexpr int most = NT == 1 ? 16 : 12;
+#pragma unroll 1
+                    for (int k0 = w0; k0 <= w1; k0 += most) add(std::integral_constant<int, most>(), k0);
                 }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) finish(z[j], sum[j], w + j * WAVES);
