@@ -16,18 +16,33 @@ AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t b, int3
     AttnPlan p;
     const int64_t rows = (int64_t)max_rows * (q_heads / kv_heads);    // rows over one k/v head
     const int64_t tiles = (rows + 15) / 16;
-    p.tiles = tiles < attn_tiles(d) ? 1 : attn_tiles(d);
-    p.blocks = (int32_t)((tiles + p.tiles - 1) / p.tiles);
     const int64_t unit = kAttnStep * kAttnWaves, per_seg = capacity < 1 ? 1 : (capacity + unit - 1) / unit;
     const int64_t segs = (int64_t)b * kv_heads;
-    const int32_t most = cus > p.blocks ? cus / p.blocks : 1;         // one workgroup per CU
     p.fits = segs <= INT32_MAX / per_seg;                             // segs * per_seg, without overflowing
-    const int64_t units = p.fits ? segs * per_seg : most;
+    const int64_t units = p.fits ? segs * per_seg : INT32_MAX;
+    // One row tile per wave where a CU gets few units: a launch of two is some 3
+    // us slower before its first unit (twice the registers and LDS), but takes k
+    // and v half as often.  32 q heads over 8, 8 / 16 / 64 rows of one request, one
+    // tile against two: 8.4 / 8.5 / 14.1 us against 12.7 / 12.7 / 19.8 at 1000
+    // positions, 12.5 / 14.9 / 34.4 against 13.5 / 15.0 / 28.1 at 8000 (8 bits).
+    const int most_tiles = attn_tiles(d);
+    p.tiles = units <= 8 * (int64_t)cus / tiles ? 1 : most_tiles < tiles ? most_tiles : (int32_t)tiles;
+    p.blocks = (int32_t)((tiles + p.tiles - 1) / p.tiles);
+    const int32_t most = cus > p.blocks ? cus / p.blocks : 1;         // one workgroup per CU
     p.groups = (int32_t)(units < most ? units : most);
-    const size_t wgs = cus > p.blocks ? cus : p.blocks;               // at least most * blocks
-    p.off_part = (wgs * kAttnWaves * sizeof(uint32_t) + 255) / 256 * 256;
-    // two pieces per workgroup: of the segment it did not start, and of the one it does not end
-    p.ws_bytes = p.off_part + wgs * 2 * attn_piece(d, p.tiles) * sizeof(float);
+    // The last group of a segment adds the pieces of all by itself, at the rate
+    // of one CU; where they are many, a launch of its own is faster (one request
+    // of 8 rows, two tiles, 4 / 8 / 32 pieces: 11.5 / 15 / 26 us in one launch, 12.7
+    // / 12.7 / 13.5 us in two).
+    const int64_t pieces = segs >= p.groups ? 2 : per_seg < p.groups / segs ? per_seg : p.groups / segs + 1;
+    p.join = pieces * p.tiles * 16 * d * (int64_t)sizeof(float) > kAttnJoinBytes;
+    // The workspace is that of the most tiles, which no other choice exceeds: two
+    // pieces per workgroup, of the segment it did not start and of the one it does
+    // not end.
+    const int64_t row_blocks = (tiles + most_tiles - 1) / most_tiles;
+    const size_t wgs = cus > row_blocks ? cus : row_blocks;
+    p.off_part = (2 * wgs * kAttnWaves * kAttnCounter * sizeof(uint32_t) + 255) / 256 * 256;
+    p.ws_bytes = p.off_part + wgs * 2 * attn_piece(d, tiles < most_tiles ? 1 : most_tiles) * sizeof(float);
     p.ws_bytes = (p.ws_bytes + 255) / 256 * 256;
     return p;
 }
@@ -132,12 +147,11 @@ int check_rows(const void *p, int64_t ld, int32_t heads, int32_t d, int32_t dtyp
     return DSPK_OK;
 }
 
-// Workgroups of a launch over (request, 64-position block, head), and one
-// per row besides.
+// Workgroups of a launch over (request, 64-position block, head), and `per_row`
+// for each row a request may have.
 int check_grid(const dspk::AttnBatch &B, int32_t heads, int64_t per_row, const char *who) {
     const int64_t nb = ((int64_t)B.max_rows + dspk::kBlockTokens - 2) / dspk::kBlockTokens + 1;
-    const int64_t per_request = nb * heads;
-    if (per_request > INT32_MAX / B.b || per_request * B.b + B.total_rows * per_row > INT32_MAX)
+    if (nb * heads + B.max_rows * per_row > INT32_MAX / B.b)
         return fail(DSPK_EUNSUPPORTED, "%s: too many rows for one launch", who);
     return DSPK_OK;
 }
@@ -287,7 +301,7 @@ int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch
     if (!aligned(tree_mask, 8)) return fail(DSPK_EINVAL, "%s: tree_mask misaligned", who);
     const dspk::AttnPlan p = dspk::attn_plan(q_heads, A.c.heads, A.c.d, A.B.b, A.B.max_rows,
                                              (int64_t)A.B.max_pages << A.c.page_shift, dspk::device_cus());
-    if (!p.fits) return fail(DSPK_EUNSUPPORTED, "%s: page table too large for one launch", who);
+    if (!p.fits || (int64_t)A.c.heads * p.blocks > 65535) return fail(DSPK_EUNSUPPORTED, "%s: page table too large for one launch", who);
     if (!pointer(workspace, 256) || ws_bytes < p.ws_bytes)
         return fail(DSPK_EINVAL, "%s: workspace of %zu bytes required (256-byte aligned)", who, p.ws_bytes);
     A.q = q;
@@ -300,6 +314,7 @@ int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch
     A.tiles = p.tiles;
     A.blocks = p.blocks;
     A.groups = p.groups;
+    A.join = p.join;
     A.counters = (uint32_t *)workspace;
     A.part = (float *)((char *)workspace + p.off_part);
     return launch_result(dspk::launch_tree_attention(A, (hipStream_t)stream), who);

@@ -74,10 +74,13 @@ hipError_t launch_new_len(const CommitArgs &a, hipStream_t s);
 constexpr int kAttnWaves = 8;
 constexpr int kAttnStep = 32;                       // positions of a wave's step
 constexpr int kAttnTile = 256 + 32;                 // floats of a 16 x 16 tile of partial sums, with m and sum of its rows
+constexpr int kAttnCounter = 16;                   // words from one arrival counter to the next: a memory line each
+constexpr int64_t kAttnJoinBytes = 64 << 10;        // partial sums of a segment above which their addition gets a launch
 constexpr int attn_tiles(int d) { return d == 256 ? 1 : 2; }         // most row tiles of a wave (its registers)
 constexpr int attn_piece(int d, int rt) { return rt * (d / 16) * kAttnTile; }  // floats of a row block's partial sums
 struct AttnPlan {
     int32_t tiles, blocks, groups;
+    int32_t join;                   // shared segments are added by a launch of their own
     bool fits;                      // unit numbers fit 31 bits
     size_t off_part, ws_bytes;      // workspace: counters, then partial sums
 };
@@ -93,8 +96,8 @@ struct AttnArgs {
     int32_t rep;                    // q heads per kv head
     float scale;                    // of the scores, times log2(e)
     const uint64_t *mask;           // [total_rows], or NULL: a chain
-    int32_t tiles, blocks, groups;  // see AttnPlan
-    uint32_t *counters;             // arrivals at shared segments [groups][blocks][waves], zero between calls
+    int32_t tiles, blocks, groups, join;      // see AttnPlan
+    uint32_t *counters;             // arrivals at shared segments [groups][blocks][waves][kAttnCounter], zero between calls
     float *part;                    // partial sums [groups][blocks][2][attn_piece]
 };
 hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t s);

@@ -24,6 +24,8 @@ using kv::f32x4;
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int TPB = 256;
+constexpr int kChunk = 32;          // k/v positions whose cosines are held at a time
+constexpr int kQRows = 4;           // q rows of a workgroup, of many
 
 // Eight lanes' worth of geometry: a head's row is held by D / 8 lanes, eight
 // neighbouring dimensions each.
@@ -33,21 +35,32 @@ struct Geo {
     static constexpr int R = TPB / L;        // rows of a workgroup pass
 };
 
+// Eight neighbouring elements as they lie in memory, and as floats.
 template <bool F32>
-__device__ __forceinline__ void load8(const void *p, int64_t i, float (&x)[8]) {
-    if constexpr (F32) {
-        const f32x4 a = *(const f32x4 *)((const float *)p + i), b = *(const f32x4 *)((const float *)p + i + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = a[e], x[e + 4] = b[e];
-    } else {
-        const u32x4 a = *(const u32x4 *)((const uint16_t *)p + i);
+struct Raw8 {
+    u32x4 v[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        const u32x4 *q = (const u32x4 *)((const char *)p + i * (F32 ? 4 : 2));
+        v[0] = q[0];
+        if constexpr (F32) v[1] = q[1];
+    }
+    __device__ __forceinline__ void clear() {
+        v[0] = u32x4{0u, 0u, 0u, 0u};
+        if constexpr (F32) v[1] = v[0];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            x[2 * e] = __uint_as_float(a[e] << 16);
-            x[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
+            if constexpr (F32) {
+                x[e] = __uint_as_float(v[0][e]);
+                x[e + 4] = __uint_as_float(v[1][e]);
+            } else {
+                x[2 * e] = __uint_as_float(v[0][e] << 16);
+                x[2 * e + 1] = __uint_as_float(v[0][e] & 0xffff0000u);
+            }
         }
     }
-}
+};
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {      // round to nearest even
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
@@ -157,42 +170,45 @@ __device__ __forceinline__ int64_t chunk_elems(const KvCache &c) {
     return (int64_t)D << c.page_shift;
 }
 
+// Rows are taken in chunks whose cosines and sines are worked out first, each
+// once per workgroup; the chunk's elements are on their way meanwhile.
 template <int D, int BITS, bool F32>
 __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const int kv_blocks, const int nb,
-                                                     const int slices) {
+                                                     const int q_blocks, const int q_rows, const int slices) {
     constexpr int L = Geo<D>::L, R = Geo<D>::R, W = BITS == 16 ? 8 : 16;
+    constexpr int CH = kChunk, NP = CH / R > 0 ? CH / R : 1;        // k/v positions of a chunk, passes over them
     typedef typename std::conditional<BITS == 16, uint16_t, uint8_t>::type E;
     constexpr int VS = D + 16 / (int)sizeof(E);                     // padded row of the turned v
-    __shared__ float s_cs[2][R * D / 2];
+    __shared__ float s_cs[2][CH * D / 2];
     __shared__ __attribute__((aligned(16))) E s_v[kBlockTokens * VS];
     const int tid = threadIdx.x, oct = tid % L, slot = tid / L, rot = A.inv_freq != nullptr ? A.rot : 0, h = rot / 2;
 
     if ((int)blockIdx.x >= kv_blocks) {
-        // ---- one row's q heads, or a slice of them
-        const int row = (blockIdx.x - kv_blocks) / slices, sl = (blockIdx.x - kv_blocks) % slices;
-        int r = 0;
-        if (A.B.row_start == nullptr) {
-            r = row / A.B.max_rows;
-        } else {
-            int hi = A.B.b;                                         // last request that starts at or before the row
-            while (hi - r > 1) {
-                const int mid = (r + hi) / 2;
-                if (A.B.row_start[mid] <= row) r = mid; else hi = mid;
-            }
-        }
-        if (r >= A.B.b) return;
+        // ---- q heads of q_rows rows of a request, or a slice of them
+        const int at = blockIdx.x - kv_blocks, sl = at % slices, r = at / slices / q_blocks, i0 = at / slices % q_blocks * q_rows;
         const kv::Req q = kv::request(A.B, A.c.page_shift, r);
-        if (row < q.row0 || row >= q.row0 + q.rows) return;         // a row of no request stays as it is
-        const int pos = A.positions != nullptr ? A.positions[row] : q.len + (row - q.row0);
-        if (tid < h) turn(pos, A.inv_freq[tid], s_cs[0][tid], s_cs[1][tid]);
+        const int n = min(q_rows, q.rows - i0), items = n * A.q_heads;      // (row, head) pairs
+        if (n <= 0) return;
+        Raw8<F32> next;
+        const auto place = [&](int item) { return (int64_t)(q.row0 + i0 + item / A.q_heads); };
+        const auto load = [&](int item) {
+            if (item < items) next.load(A.q, place(item) * A.ldq + item % A.q_heads * D + oct * 8); else next.clear();
+        };
+        int item = sl * R + slot;
+        load(item);
+        for (int i = tid; i < n * h; i += TPB) {
+            const int row = i0 + i / h;
+            turn(A.positions != nullptr ? A.positions[q.row0 + row] : q.len + row, A.inv_freq[i % h], s_cs[0][i], s_cs[1][i]);
+        }
         __syncthreads();
-        for (int hd = sl * R + slot; hd - slot < A.q_heads; hd += slices * R) {
-            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            const bool in = hd < A.q_heads;
-            if (in) load8<F32>(A.q, row * A.ldq + hd * D + oct * 8, x);
+        for (; item - slot < items; item += slices * R) {
+            float x[8];
+            next.get(x);
+            load(item + slices * R);
             if (A.qw != nullptr) norm8<D>(x, A.qw, A.eps, oct);
-            if (rot) rotate8<D>(x, oct, rot, A.interleaved, s_cs[0], s_cs[1]);
-            if (in) *(u32x4 *)(A.q_out + row * A.ldqo + hd * D + oct * 8) = bf16_8(x);
+            const int of = min(item / A.q_heads, n - 1) * h;
+            if (rot) rotate8<D>(x, oct, rot, A.interleaved, s_cs[0] + of, s_cs[1] + of);
+            if (item < items) *(u32x4 *)(A.q_out + place(item) * A.ldqo + item % A.q_heads * D + oct * 8) = bf16_8(x);
         }
         return;
     }
@@ -208,53 +224,67 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
     const int t0 = sp.base & ((1 << A.c.page_shift) - 1);
     const int64_t chunk = page * A.c.heads + head;
     E *const kd = (E *)A.c.k + chunk * chunk_elems<D, BITS>(A.c), *const vd = (E *)A.c.v + chunk * chunk_elems<D, BITS>(A.c);
+    const int row0 = q.row0 + sp.base - q.len;                      // row of the block's position 0
 
-    for (int p0 = sp.lo / R * R; p0 < sp.hi; p0 += R) {
-        const int t = p0 + slot, row = q.row0 + sp.base + t - q.len;
-        const bool in = t >= sp.lo && t < sp.hi;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (in) {
-            load8<F32>(A.k, row * A.ldk + head * D + oct * 8, x);
-            load8<F32>(A.v, row * A.ldv + head * D + oct * 8, y);
+    for (int c0 = sp.lo / CH * CH; c0 < sp.hi; c0 += CH) {
+        Raw8<F32> kr[NP], vr[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int t = c0 + p * R + slot;
+            if (t >= sp.lo && t < sp.hi) {
+                kr[p].load(A.k, (row0 + t) * A.ldk + head * D + oct * 8);
+                vr[p].load(A.v, (row0 + t) * A.ldv + head * D + oct * 8);
+            } else {
+                kr[p].clear();
+                vr[p].clear();
+            }
         }
         if (rot) {
-            __syncthreads();                                        // the previous pass has read its table
-            for (int i = tid; i < R * h; i += TPB) {
-                const int tt = p0 + i / h;
-                if (tt >= sp.lo && tt < sp.hi) {
-                    const int rr = q.row0 + sp.base + tt - q.len;
-                    turn(A.positions != nullptr ? A.positions[rr] : sp.base + tt, A.inv_freq[i % h], s_cs[0][i],
-                         s_cs[1][i]);
-                }
+            __syncthreads();                                        // the previous chunk has read its table
+            const int lo = max(sp.lo, c0), hi = min(sp.hi, c0 + CH);
+            for (int i = tid; i < (hi - lo) * h; i += TPB) {
+                const int t = lo + i / h, o = (lo - c0) * h + i;
+                turn(A.positions != nullptr ? A.positions[row0 + t] : sp.base + t, A.inv_freq[i % h], s_cs[0][o], s_cs[1][o]);
             }
             __syncthreads();
         }
-        if (A.kw != nullptr) norm8<D>(x, A.kw, A.eps, oct);
-        if (rot) rotate8<D>(x, oct, rot, A.interleaved, s_cs[0] + slot * h, s_cs[1] + slot * h);
-        E *const kp = kd + kv::k_piece<D, W>(t0 + t, oct * 8) + (BITS == 8 ? oct % 2 * 8 : 0);
-        if constexpr (BITS == 16) {
-            const u32x4 a = bf16_8(x), b = bf16_8(y);
-            if (in) {
-                *(u32x4 *)kp = a;
-                *(u32x4 *)(s_v + t * VS + oct * 8) = b;
-            }
-        } else {
-            float sk, sv;
-            const u32x2 a = codes8<D>(x, sk), b = codes8<D>(y, sv);
-            if (in) {
-                *(u32x2 *)kp = a;
-                *(u32x2 *)(s_v + t * VS + oct * 8) = b;
-                if (oct == 0) {
-                    const int64_t si = (chunk << A.c.page_shift) + t0 + t;
-                    A.c.ks[si] = sk;
-                    A.c.vs[si] = sv;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int t = c0 + p * R + slot;
+            const bool in = t >= sp.lo && t < sp.hi;
+            if (c0 + p * R >= sp.hi || c0 + p * R + R <= sp.lo) continue;   // no row of the pass: the same for all
+            float x[8], y[8];
+            kr[p].get(x);
+            vr[p].get(y);
+            if (A.kw != nullptr) norm8<D>(x, A.kw, A.eps, oct);
+            const int of = min(t - c0, CH - 1) * h;
+            if (rot) rotate8<D>(x, oct, rot, A.interleaved, s_cs[0] + of, s_cs[1] + of);
+            E *const kp = kd + kv::k_piece<D, W>(t0 + t, oct * 8) + (BITS == 8 ? oct % 2 * 8 : 0);
+            if constexpr (BITS == 16) {
+                if (in) {
+                    *(u32x4 *)kp = bf16_8(x);
+                    *(u32x4 *)(s_v + t * VS + oct * 8) = bf16_8(y);
+                }
+            } else {
+                float sk, sv;
+                const u32x2 a = codes8<D>(x, sk), b = codes8<D>(y, sv);
+                if (in) {
+                    *(u32x2 *)kp = a;
+                    *(u32x2 *)(s_v + t * VS + oct * 8) = b;
+                    if (oct == 0) {
+                        const int64_t si = (chunk << A.c.page_shift) + t0 + t;
+                        A.c.ks[si] = sk;
+                        A.c.vs[si] = sv;
+                    }
                 }
             }
         }
     }
     __syncthreads();
-    for (int i = tid; i < kBlockTokens * D / W; i += TPB) {
-        const int sb = i / (64 * (D / 16)), vb = i / 64 % (D / 16), g = i / 16 % 4, d = vb * 16 + i % 16;
+    // pieces of the turned v, those that hold rows
+    constexpr int per = 64 * (D / 16);                              // pieces of 4W positions
+    for (int i = sp.lo / (4 * W) * per + tid; i < (sp.hi + 4 * W - 1) / (4 * W) * per; i += TPB) {
+        const int sb = i / per, vb = i / 64 % (D / 16), g = i / 16 % 4, d = vb * 16 + i % 16;
         const int first = sb * 4 * W + g * 4;                       // the piece's positions: first + 16 jj + i
         if (first >= sp.hi || first + 4 * W - 16 + 3 < sp.lo) continue;
         E *const dst = vd + kv::v_elem<D, W>(t0 + first, d);
@@ -320,7 +350,9 @@ __global__ __launch_bounds__(TPB) void kv_read_kernel(const ReadArgs A, const in
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(0x7fc00000u);
             } else if constexpr (BITS == 16) {
-                load8<false>(s_x, t * VS + d, x);
+                Raw8<false> raw;
+                raw.load(s_x, t * VS + d);
+                raw.get(x);
             } else {
                 const float s = (which ? A.c.vs : A.c.ks)[(chunk << A.c.page_shift) + t0 + t];
 #pragma unroll
@@ -432,15 +464,16 @@ int touched_blocks(int32_t n) { return (n + kBlockTokens - 2) / kBlockTokens + 1
 
 hipError_t launch_append(const AppendArgs &A, hipStream_t s) {
     const int nb = touched_blocks(A.B.max_rows), kvb = A.B.b * nb * A.c.heads;
-    const int per = TPB * 8 / A.c.d, most = (A.q_heads + per - 1) / per;      // passes of a row's q heads
-    // few rows: a workgroup per pass, for latency; many: all of a row's, which share its cosines
-    const int slices = A.q == nullptr ? 0 : A.B.total_rows < 1024 ? most : 1;
-    const int grid = kvb + A.B.total_rows * slices;
+    // q: few rows go one to a workgroup, sliced further into passes, for latency; many in chunks
+    const bool many = A.B.total_rows >= 1024;
+    const int q_rows = many ? kQRows : 1, q_blocks = (A.B.max_rows + q_rows - 1) / q_rows;
+    const int passes = (A.q_heads * A.c.d + TPB * 8 - 1) / (TPB * 8), slices = many ? 1 : passes;
+    const int grid = kvb + (A.q == nullptr ? 0 : A.B.b * q_blocks * slices);
     with_format(A.c, [&](auto d, auto bits) {
         if (A.f32)
-            hipLaunchKernelGGL((append_kernel<d(), bits(), true>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, slices);
+            hipLaunchKernelGGL((append_kernel<d(), bits(), true>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, q_blocks, q_rows, slices);
         else
-            hipLaunchKernelGGL((append_kernel<d(), bits(), false>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, slices);
+            hipLaunchKernelGGL((append_kernel<d(), bits(), false>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, q_blocks, q_rows, slices);
     });
     return hipGetLastError();
 }

@@ -51,6 +51,7 @@ constexpr int WAVES = kAttnWaves, TPB = 64 * WAVES;
 constexpr int kStep = kAttnStep;        // positions of a wave's step
 constexpr int kTileFloats = kAttnTile;  // a tile of partial sums: 16 x 16 outputs, and m and sum of 16 rows
 constexpr int kUnit = kAttnStep * WAVES;
+constexpr int kJoinWaves = 4;
 
 #define NEG_INF (-__builtin_inff())
 // Limits of what a lane adds at a time, in units of its row's reference, before
@@ -141,6 +142,15 @@ struct Ranges {
         return u < cut ? u / (q + 1) : rem + (u - cut) / q;
     }
 };
+__device__ __forceinline__ Ranges ranges(const AttnArgs &A, int total) {
+    // fewer than two units each: two to some, which is no slower and leaves fewer pieces
+    const int groups = total > A.groups && total < 2 * A.groups ? (total + 1) / 2 : A.groups;
+    Ranges R;
+    R.q = total / groups;
+    R.rem = total - R.q * groups;
+    return R;
+}
+
 // A group's range, and where it starts: the request that holds its first unit
 // and that request's first unit.  Every wave does it by itself; requests are
 // taken 64 at a time, one per lane.
@@ -174,10 +184,7 @@ __device__ __forceinline__ Start find_start(const AttnArgs &A, int group, Ranges
         load(base);
         total += __builtin_amdgcn_readlane(x, last);
     }
-    // fewer than two units each: two to some, which is no slower and leaves fewer pieces
-    const int groups = total > A.groups && total < 2 * A.groups ? (total + 1) / 2 : A.groups;
-    R.q = total / groups;
-    R.rem = total - R.q * groups;
+    R = ranges(A, total);
     Start s;
     s.u = min(R.begin(group), total);
     s.u_end = min(R.begin(group + 1), total);
@@ -241,6 +248,12 @@ __device__ __forceinline__ void store_out(uint16_t *dst, f32x4 x) {
     y[0] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[0]) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[1]) << 16;
     y[1] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2]) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[3]) << 16;
     *(u32x2 *)dst = y;
+}
+
+// A group's part of a segment: the one it starts, or the one it did not.
+template <int D, int RT>
+__device__ __forceinline__ float *piece(const AttnArgs &A, int group, int rb, bool starts) {
+    return A.part + (((int64_t)group * A.blocks + rb) * 2 + starts) * attn_piece(D, RT);
 }
 
 // RT row tiles of 16 per wave.
@@ -312,7 +325,8 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
         // A step takes 32 positions from t.  Pages that are none of the cache's
         // make every row that sees them NaN; page 0 is read in their place.
         // Page numbers are loaded a step ahead of the k that needs them, k a
-        // step ahead of its use (AHEAD), v at the step's start.
+        // step ahead of its use (AHEAD), v at the step's start (k and v both a step
+        // ahead measured the same).
         const int32_t *const table = page_table + (int64_t)req * A.B.max_pages;
         u32x4 kf[2][KB];
         f32x4 ksc[2];
@@ -333,6 +347,26 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
             }
         };
 
+        const auto load_v = [&](int t, u32x4 (&vf)[VB], f32x4 (&vsc)[2]) {
+            const int at = t & page_mask;
+            // an 8-bit piece holds 64 positions: its first or second half
+            const unsigned char *src = (const unsigned char *)A.c.v + (chunk + (at & -(4 * W))) * (D * BITS / 8) +
+                                       (BITS == 8 ? (at & 32) / 4 : 0);
+#pragma unroll
+            for (int vb = 0; vb < VB; ++vb) {
+                if constexpr (BITS == 16) {
+                    vf[vb] = *(const u32x4 *)(src + vb * 1024 + (uint32_t)lane * 16);
+                } else {
+                    const u32x2 x = *(const u32x2 *)(src + vb * 1024 + (uint32_t)lane * 16);
+                    vf[vb][0] = x[0];
+                    vf[vb][1] = x[1];
+                }
+            }
+            if constexpr (BITS == 8) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) vsc[i] = *(const f32x4 *)(A.c.vs + chunk + at + i * 16 + (uint32_t)g * 4);
+            }
+        };
         const int t_first = v0 * kUnit + w * kStep, t_end = min((v0 + n) * kUnit, tokens);
         const int32_t page_first = t_first < t_end ? table[t_first >> A.c.page_shift] : 0;
 
@@ -370,28 +404,8 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                 const bool step_bad = bad, tail = t + kStep > q.len;
                 u32x4 vf[VB];
                 f32x4 vsc[2];
-                const auto load_v = [&] {
-                    const int at = t & page_mask;
-                    // an 8-bit piece holds 64 positions: its first or second half
-                    const unsigned char *src = (const unsigned char *)A.c.v + (chunk + (at & -(4 * W))) * (D * BITS / 8) +
-                                               (BITS == 8 ? (at & 32) / 4 : 0);
-#pragma unroll
-                    for (int vb = 0; vb < VB; ++vb) {
-                        if constexpr (BITS == 16) {
-                            vf[vb] = *(const u32x4 *)(src + vb * 1024 + (uint32_t)lane * 16);
-                        } else {
-                            const u32x2 x = *(const u32x2 *)(src + vb * 1024 + (uint32_t)lane * 16);
-                            vf[vb][0] = x[0];
-                            vf[vb][1] = x[1];
-                        }
-                    }
-                    if constexpr (BITS == 8) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            vsc[i] = *(const f32x4 *)(A.c.vs + chunk + at + i * 16 + (uint32_t)g * 4);
-                    }
-                };
-                if constexpr (AHEAD) load_v(); else load_k(t);
+                if constexpr (!AHEAD) load_k(t);
+                else load_v(t, vf, vsc);
 
                 // scores
                 f32x4 s[RT][2];
@@ -418,7 +432,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                 f32x4 kc[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) kc[i] = BITS == 8 ? ksc[i] * c : f32x4{c, c, c, c};
-                if constexpr (!AHEAD) load_v();
+                if constexpr (!AHEAD) load_v(t, vf, vsc);
                 if (t + kUnit < t_end) {
                     find_page(page_next);
                     if constexpr (AHEAD) load_k(t + kUnit);
@@ -603,9 +617,6 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
         }
         __syncthreads();
         const bool whole = n == un.per_seg;
-        const auto piece = [&](int of, bool starts) {               // of a group's part of the segment
-            return A.part + (((int64_t)of * A.blocks + rb) * 2 + starts) * attn_piece(D, RT);
-        };
         const auto finish = [&](f32x4 z, float sum, int tile) {
             const int rr = row_base + tile / VB * 16 + col, node = (int)((rr + 0.5f) * per_rep);
             // a row that sees nothing is 0; one whose length is a fault is NaN
@@ -635,17 +646,17 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
             } else {
                 // every tile with its own copy of its rows' statistics, so that
                 // a wave waits for nothing but its own stores
-                float *const p = piece(group, v0 == 0) + tile * kTileFloats;
+                float *const p = piece<D, RT>(A, group, rb, v0 == 0) + tile * kTileFloats;
                 put4(p, lane, z);
                 if (g == 0) put2(p + 256 + col * 2, mx, sum);
             }
         }
-        if (!whole && w < RT * VB) {
+        if (!whole && !A.join && w < RT * VB) {
             // Count in; the last to come adds the pieces of the wave's tiles, in
             // group order.  A group starts at most one shared segment.
             wait_stores();
             const int s0 = u - v0, w0 = R.owner(s0), w1 = R.owner(s0 + un.per_seg - 1);
-            uint32_t *const ctr = A.counters + (w0 * A.blocks + rb) * WAVES + w;
+            uint32_t *const ctr = A.counters + ((w0 * A.blocks + rb) * WAVES + w) * kAttnCounter;
             uint32_t ticket = 0;
             if (lane == 0) ticket = __hip_atomic_fetch_add(ctr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             if (__builtin_amdgcn_readfirstlane(ticket) == (uint32_t)(w1 - w0)) {
@@ -665,7 +676,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
 #pragma unroll
                     for (int i = 0; i < XB; ++i) {
                         const int k = min(k0 + i, w1);
-                        const float *src = piece(k, k == w0);
+                        const float *src = piece<D, RT>(A, k, rb, k == w0);
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
                             const float *p = src + (w + j * WAVES) * kTileFloats;
@@ -709,22 +720,117 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
     }
 }
 
-template <int D, int BITS>
-hipError_t launch(const AttnArgs &A, int grid, hipStream_t s) {
-    if (A.tiles == 1)
-        hipLaunchKernelGGL((tree_attn_kernel<D, BITS, 1>), dim3(grid), dim3(TPB), 0, s, A, A.B.page_table);
-    else
-        hipLaunchKernelGGL((tree_attn_kernel<D, BITS, attn_tiles(D)>), dim3(grid), dim3(TPB), 0, s, A, A.B.page_table);
+// The pieces of shared segments, where they are more than the last workgroup of
+// a segment adds in good time (A.join): a workgroup per 16 x 16 output tile, a
+// wave for every fourth piece, in group order.
+template <int D, int RT>
+__global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(const AttnArgs A) {
+    constexpr int VB = D / 16, XB = 8;              // pieces of a wave in flight
+    __shared__ float2 s_ml[kJoinWaves][16];
+    __shared__ f32x4 s_o[kJoinWaves][64];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
+    const int tile = blockIdx.x, rb = blockIdx.y % A.blocks, head = blockIdx.y / A.blocks, r = blockIdx.z;
+    int total = 0, first = 0;
+    Units un = {};
+    kv::Req q = {};
+    for (int base = 0; base < A.B.b; base += 64) {
+        kv::Req ql = {};
+        Units ul = {};
+        if (base + lane < A.B.b) {
+            ql = kv::request(A.B, A.c.page_shift, base + lane);
+            ul = units_of(A, ql);
+        }
+        const int x = A.B.b > 1 ? prefix_sum(ul.total) : ul.total;
+        if (r >= base && r < base + 64) {
+            const int l = r - base;
+            first = total + __builtin_amdgcn_readlane(x - ul.total, l);
+            un.per_seg = __builtin_amdgcn_readlane(ul.per_seg, l);
+            q.row0 = __builtin_amdgcn_readlane(ql.row0, l);
+            q.rows = __builtin_amdgcn_readlane(ql.rows, l);
+        }
+        total += __builtin_amdgcn_readlane(x, A.B.b > 1 ? 63 : 0);
+    }
+    const int rows = q.rows * A.rep, row_base = rb * RT * 16;
+    if (row_base + tile / VB * 16 >= rows) return;
+    const Ranges R = ranges(A, total);
+    first += head * un.per_seg;
+    const int w0 = R.owner(first), w1 = R.owner(first + un.per_seg - 1);
+    if (w0 == w1) return;                                           // written by its only group
+    float mx = NEG_INF, sum = 0.f;
+    f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int k0 = w0 + w; k0 <= w1; k0 += XB * kJoinWaves) {
+        f32x4 x[XB];
+        float2 ml[XB];
+#pragma unroll
+        for (int i = 0; i < XB; ++i) {
+            const int k = k0 + i * kJoinWaves <= w1 ? k0 + i * kJoinWaves : k0;
+            const float *p = piece<D, RT>(A, k, rb, k == w0) + tile * kTileFloats;
+            const f32x2 a = *(const f32x2 *)(p + lane * 2), b = *(const f32x2 *)(p + 128 + lane * 2);
+            x[i] = f32x4{a[0], a[1], b[0], b[1]};
+            ml[i] = *(const float2 *)(p + 256 + col * 2);
+        }
+        float mn = mx;
+#pragma unroll
+        for (int i = 0; i < XB; ++i) mn = fmaxf(mn, ml[i].x);
+        const float mc = zero_if_none(mn), f = __builtin_amdgcn_exp2f(mx - mc);
+        z *= f;
+        sum *= f;
+        mx = mn;
+#pragma unroll
+        for (int i = 0; i < XB; ++i) {
+            const bool real = i == 0 || k0 + i * kJoinWaves <= w1;
+            const float fk = __builtin_amdgcn_exp2f(ml[i].x - mc);
+            sum += real ? ml[i].y * fk : 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] += real ? x[i][e] * fk : 0.f;
+        }
+    }
+    if (g == 0) s_ml[w][col] = float2{mx, sum};
+    s_o[w][lane] = z;
+    __syncthreads();
+    if (w != 0) return;
+    float2 ml[kJoinWaves];
+    mx = NEG_INF;
+#pragma unroll
+    for (int k = 0; k < kJoinWaves; ++k) {
+        ml[k] = s_ml[k][col];
+        mx = fmaxf(mx, ml[k].x);
+    }
+    const float mc = zero_if_none(mx);
+    sum = 0.f;
+    z = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kJoinWaves; ++k) {
+        const float f = __builtin_amdgcn_exp2f(ml[k].x - mc);
+        sum += ml[k].y * f;
+        z += s_o[k][lane] * f;
+    }
+    const int rr = row_base + tile / VB * 16 + col, node = (int)((rr + 0.5f) * (1.f / A.rep));
+    if (rr < rows)
+        store_out(A.out + (int64_t)(q.row0 + node) * A.ldo + (head * A.rep + rr - node * A.rep) * D + tile % VB * 16 + g * 4,
+                  z * (sum == 0.f ? 0.f : 1.f / sum));
+}
+
+template <int D, int BITS, int RT>
+hipError_t launch_tiles(const AttnArgs &A, hipStream_t s) {
+    hipLaunchKernelGGL((tree_attn_kernel<D, BITS, RT>), dim3(A.groups * A.blocks), dim3(TPB), 0, s, A, A.B.page_table);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !A.join) return e;
+    hipLaunchKernelGGL((attn_join_kernel<D, RT>), dim3(RT * D / 16, A.c.heads * A.blocks, A.B.b), dim3(64 * kJoinWaves), 0, s, A);
     return hipGetLastError();
+}
+template <int D, int BITS>
+hipError_t launch(const AttnArgs &A, hipStream_t s) {
+    return A.tiles == 1 ? launch_tiles<D, BITS, 1>(A, s) : launch_tiles<D, BITS, attn_tiles(D)>(A, s);
 }
 
 }  // namespace
 
 hipError_t launch_tree_attention(const AttnArgs &A, hipStream_t s) {
-    const int grid = A.groups * A.blocks;
     if (A.c.bits == 16)
-        return A.c.d == 64 ? launch<64, 16>(A, grid, s) : A.c.d == 128 ? launch<128, 16>(A, grid, s) : launch<256, 16>(A, grid, s);
-    return A.c.d == 64 ? launch<64, 8>(A, grid, s) : A.c.d == 128 ? launch<128, 8>(A, grid, s) : launch<256, 8>(A, grid, s);
+        return A.c.d == 64 ? launch<64, 16>(A, s) : A.c.d == 128 ? launch<128, 16>(A, s) : launch<256, 16>(A, s);
+    return A.c.d == 64 ? launch<64, 8>(A, s) : A.c.d == 128 ? launch<128, 8>(A, s) : launch<256, 8>(A, s);
 }
 
 }  // namespace dspk
