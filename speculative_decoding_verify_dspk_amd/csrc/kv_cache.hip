@@ -24,7 +24,7 @@ using kv::f32x4;
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int TPB = 256;
-constexpr int kChunk = 32;          // k/v positions whose cosines are held at a time
+constexpr int kChunk = 16;          // k/v positions whose cosines are held at a time
 constexpr int kQRows = 4;           // q rows of a workgroup, of many
 
 // Eight lanes' worth of geometry: a head's row is held by D / 8 lanes, eight
@@ -62,64 +62,153 @@ struct Raw8 {
     }
 };
 
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {      // round to nearest even
-    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
-}
-__device__ __forceinline__ u32x4 bf16_8(const float (&x)[8]) {
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x4 bf16_8(const float (&x)[8]) {         // round to nearest even
     u32x4 r;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = bf16_pair(x[2 * e], x[2 * e + 1]);
+    for (int e = 0; e < 4; ++e)
+        r[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x[2 * e], x[2 * e + 1]}), bf16x2));
     return r;
 }
 
-// x * rsqrt(mean(x^2) + eps) * w over a head's row, the sum in fp32.
+// The value of another lane, by a permutation that needs no address: CTRL of
+// the data-parallel primitives, or with M lane ^ M.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+template <int M>
+__device__ __forceinline__ float lane_xor(float x) {
+    return __uint_as_float(__builtin_amdgcn_ds_swizzle(__float_as_uint(x), M << 10 | 0x1f));
+}
+// f over the L lanes of a row, L = 8, 16 or 32: within four lanes, then eight,
+// sixteen (mirrored halves are equal by then) and thirty-two.
+template <int L, typename F>
+__device__ __forceinline__ float over_row(float x, F f) {
+    x = f(x, dpp<0xb1>(x));
+    x = f(x, dpp<0x4e>(x));
+    x = f(x, dpp<0x141>(x));
+    if constexpr (L >= 16) x = f(x, dpp<0x140>(x));
+    if constexpr (L >= 32) x = f(x, lane_xor<16>(x));
+    return x;
+}
+
+// 1 / sqrt(mean(x^2) + eps) of a head's row, the sum in fp32.
 template <int D>
-__device__ __forceinline__ void norm8(float (&x)[8], const float *w, float eps, int oct) {
+__device__ __forceinline__ float norm_factor(const float (&x)[8], float eps) {
     float s = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) s += x[e] * x[e];
-#pragma unroll
-    for (int o = 1; o < Geo<D>::L; o <<= 1) s += __shfl_xor(s, o);
-    const float f = rsqrtf(s * (1.f / D) + eps);
-    const f32x4 a = *(const f32x4 *)(w + oct * 8), b = *(const f32x4 *)(w + oct * 8 + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] *= f * a[e], x[e + 4] *= f * b[e];
+    s = over_row<Geo<D>::L>(s, [](float a, float b) { return a + b; });
+    return rsqrtf(s * (1.f / D) + eps);
 }
 
-// cos and sin of position * freq.  The angle's turns are counted in fp64 and
-// only their fraction is rounded to fp32: at position 10^6 an fp32 product
-// would be off by 0.06 radians.
-__device__ __forceinline__ void turn(int32_t position, float freq, float &c, float &s) {
-    const double rev = (double)position * (double)freq * 0.15915494309189533577;
-    sincospif((float)(2.0 * (rev - rint(rev))), &s, &c);
+__device__ __forceinline__ int next_pow2(int x) { return x <= 1 ? 1 : 1 << (32 - __clz(x - 1)); }
+
+// Turns per position as a fraction of 2^64, and cos and sin of a position's
+// angle.  Counting turns in 64-bit fixed point keeps far positions exact: at
+// position 10^6 an fp32 product would be off by 0.06 radians.
+__device__ __forceinline__ uint64_t turns(float freq) {
+    const double t = (double)freq * 0.15915494309189533577, part = t - floor(t);
+    return part < 1.0 ? (uint64_t)(part * 0x1p64) : 0;
+}
+__device__ __forceinline__ void turn(int32_t position, uint64_t per, float &c, float &s) {
+    const int32_t t = (int32_t)(uint32_t)(((uint64_t)(int64_t)position * per) >> 32);      // of 2^32
+    sincospif((float)t * 0x1p-31f, &s, &c);
 }
 
-// Rotation of a head's row; cs points to the row's cosines, sn to its sines.
-// All lanes of the wave take part (the pair's other half comes from another
-// lane unless pairs are neighbours).
-template <int D>
-__device__ __forceinline__ void rotate8(float (&x)[8], int oct, int rot, int interleaved, const float *cs,
-                                        const float *sn) {
-    const int d0 = oct * 8, h = rot / 2;
-    if (interleaved) {
-        if (d0 >= rot) return;
+// What norm and rotation do to the eight dimensions of a lane, for one row:
+// x -> f (x * cw + partner * sw), f the norm's factor; cosines, sines and
+// weights of the lane and of its partners are folded together.
+struct Turn8 {
+    float cw[8], sw[8];
+};
+// The part that is the same for all rows: weights, and the partners' with the
+// sign of their sines (0 where nothing turns); the lane's place in a table.
+struct Lane8 {
+    float own[8], other[8];
+    int at;                     // first of the lane's frequencies
+    bool in;
+};
+__device__ __forceinline__ void get8(const float *p, float (&x)[8]) {
+    const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float c = cs[d0 / 2 + e], s = sn[d0 / 2 + e], a = x[2 * e], b = x[2 * e + 1];
-            x[2 * e] = a * c - b * s;
-            x[2 * e + 1] = b * c + a * s;
-        }
-        return;
+    for (int e = 0; e < 4; ++e) x[e] = a[e], x[e + 4] = b[e];
+}
+__device__ __forceinline__ Lane8 make_lane(int oct, int rot, int interleaved, const float *w) {
+    Lane8 r;
+    const int d0 = oct * 8, h = rot / 2;            // h is a multiple of 8
+    r.in = d0 < rot;
+    const bool first = d0 < h;
+    r.at = !r.in ? 0 : interleaved ? d0 / 2 : first ? d0 : d0 - h;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.own[e] = r.other[e] = 1.f;
+    if (w != nullptr) {
+        get8(w + d0, r.own);
+        get8(w + (!r.in || interleaved ? d0 : first ? d0 + h : d0 - h), r.other);
     }
-    const bool first = d0 < h, in = d0 < rot;      // h is a multiple of 8
-    const int src = (threadIdx.x & 63) + (!in ? 0 : first ? h / 8 : -h / 8);
+    if (interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const float a = r.other[e];
+            r.other[e] = -r.other[e + 1];
+            r.other[e + 1] = a;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.other[e] = !r.in ? 0.f : !interleaved && first ? -r.other[e] : r.other[e];
+    return r;
+}
+// cs: the row's cosines, sn: its sines.
+__device__ __forceinline__ Turn8 make_turn(const Lane8 &l, int rot, int interleaved, const float *cs, const float *sn) {
+    Turn8 r;
+    float c[8], s[8];
+    if (rot == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.cw[e] = l.own[e], r.sw[e] = 0.f;
+        return r;
+    }
+    if (interleaved) {
+        const f32x4 a = *(const f32x4 *)(cs + l.at), b = *(const f32x4 *)(sn + l.at);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = a[e / 2], s[e] = b[e / 2];
+    } else {
+        get8(cs + l.at, c);
+        get8(sn + l.at, s);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        r.cw[e] = l.in ? c[e] * l.own[e] : l.own[e];
+        r.sw[e] = s[e] * l.other[e];
+    }
+    return r;
+}
+// All lanes of the wave take part.
+template <int D>
+__device__ __forceinline__ void norm_turn(float (&x)[8], bool norm, float eps, int rot, int interleaved, const Turn8 &t) {
+    const float f = norm ? norm_factor<D>(x, eps) : 1.f;
     float p[8];
+    if (rot == 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = __shfl(x[e], src);
-    if (!in) return;
-    const int f = first ? d0 : d0 - h;
+        for (int e = 0; e < 8; ++e) p[e] = 0.f;
+    } else if (interleaved) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * cs[f + e] + (first ? -p[e] : p[e]) * sn[f + e];
+        for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
+    } else if (rot == D) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (D == 128) p[e] = dpp<0x128>(x[e]);        // eight lanes on, of sixteen
+            else p[e] = lane_xor<Geo<D>::L / 2>(x[e]);
+        }
+    } else {
+        const int d0 = threadIdx.x % Geo<D>::L * 8;
+        const int src = (threadIdx.x & 63) + (d0 >= rot ? 0 : d0 < rot / 2 ? rot / 16 : -(rot / 16));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = __shfl(x[e], src);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = f * (x[e] * t.cw[e] + p[e] * t.sw[e]);
 }
 
 // A head's row as 8-bit codes: scale = max|x| / 127, code = round(x * 127 /
@@ -131,8 +220,9 @@ __device__ __forceinline__ u32x2 codes8(const float (&x)[8], float &scale) {
     uint32_t top = 0;                              // bit patterns of magnitudes order like them, NaN on top
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = 1; o < Geo<D>::L; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    top = __float_as_uint(over_row<Geo<D>::L>(__uint_as_float(top), [](float a, float b) {
+        return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+    }));
     const float t = __uint_as_float(top), inv = 127.f / t;
     const bool held = top < 0x7f800000u && inv < __uint_as_float(0x7f800000u);
     scale = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : held ? t / 127.f : 0.f;
@@ -176,10 +266,10 @@ template <int D, int BITS, bool F32>
 __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const int kv_blocks, const int nb,
                                                      const int q_blocks, const int q_rows, const int slices) {
     constexpr int L = Geo<D>::L, R = Geo<D>::R, W = BITS == 16 ? 8 : 16;
-    constexpr int CH = kChunk, NP = CH / R > 0 ? CH / R : 1;        // k/v positions of a chunk, passes over them
+    constexpr int CH = kChunk > R ? kChunk : R, NP = CH / R;        // k/v positions of a chunk, passes over them
     typedef typename std::conditional<BITS == 16, uint16_t, uint8_t>::type E;
     constexpr int VS = D + 16 / (int)sizeof(E);                     // padded row of the turned v
-    __shared__ float s_cs[2][CH * D / 2];
+    __shared__ __attribute__((aligned(16))) float s_cs[2][CH * D / 2];
     __shared__ __attribute__((aligned(16))) E s_v[kBlockTokens * VS];
     const int tid = threadIdx.x, oct = tid % L, slot = tid / L, rot = A.inv_freq != nullptr ? A.rot : 0, h = rot / 2;
 
@@ -187,28 +277,49 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
         // ---- q heads of q_rows rows of a request, or a slice of them
         const int at = blockIdx.x - kv_blocks, sl = at % slices, r = at / slices / q_blocks, i0 = at / slices % q_blocks * q_rows;
         const kv::Req q = kv::request(A.B, A.c.page_shift, r);
-        const int n = min(q_rows, q.rows - i0), items = n * A.q_heads;      // (row, head) pairs
+        const int n = min(q_rows, q.rows - i0);
         if (n <= 0) return;
-        Raw8<F32> next;
-        const auto place = [&](int item) { return (int64_t)(q.row0 + i0 + item / A.q_heads); };
-        const auto load = [&](int item) {
-            if (item < items) next.load(A.q, place(item) * A.ldq + item % A.q_heads * D + oct * 8); else next.clear();
+        const int p2 = next_pow2(h), f = tid & (p2 - 1);            // a frequency per thread
+        const int passes = (A.q_heads + R - 1) / R;                 // of a row's heads
+        constexpr int AT = 4;                                       // passes whose elements are on their way
+        Raw8<F32> next[AT];
+        const auto load = [&](int i, int j, int p) {
+            const int hd = p * R + slot;
+            if (hd < A.q_heads) next[j].load(A.q, (int64_t)(q.row0 + i0 + i) * A.ldq + hd * D + oct * 8);
         };
-        int item = sl * R + slot;
-        load(item);
-        for (int i = tid; i < n * h; i += TPB) {
-            const int row = i0 + i / h;
-            turn(A.positions != nullptr ? A.positions[q.row0 + row] : q.len + row, A.inv_freq[i % h], s_cs[0][i], s_cs[1][i]);
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
+            next[j].clear();
+            load(0, j, sl + j * slices);
+        }
+        const Lane8 ln = make_lane(oct, rot, A.interleaved, A.qw);
+        if (rot && f < h) {
+            const uint64_t per = turns(A.inv_freq[f]);
+            for (int i = tid / p2; i < n; i += TPB / p2) {
+                const int row = i0 + i;
+                turn(A.positions != nullptr ? A.positions[q.row0 + row] : q.len + row, per, s_cs[0][i * h + f], s_cs[1][i * h + f]);
+            }
         }
         __syncthreads();
-        for (; item - slot < items; item += slices * R) {
-            float x[8];
-            next.get(x);
-            load(item + slices * R);
-            if (A.qw != nullptr) norm8<D>(x, A.qw, A.eps, oct);
-            const int of = min(item / A.q_heads, n - 1) * h;
-            if (rot) rotate8<D>(x, oct, rot, A.interleaved, s_cs[0] + of, s_cs[1] + of);
-            if (item < items) *(u32x4 *)(A.q_out + place(item) * A.ldqo + item % A.q_heads * D + oct * 8) = bf16_8(x);
+        for (int pb = sl; pb < passes; pb += AT * slices) {
+            if (pb != sl) {
+#pragma unroll
+                for (int j = 0; j < AT; ++j) load(0, j, pb + j * slices);
+            }
+            for (int i = 0; i < n; ++i) {
+                const Turn8 t = make_turn(ln, rot, A.interleaved, s_cs[0] + i * h, s_cs[1] + i * h);
+#pragma unroll
+                for (int j = 0; j < AT; ++j) {
+                    const int p = pb + j * slices, hd = p * R + slot;
+                    if (p >= passes) break;                         // the same for all
+                    float x[8];
+                    next[j].get(x);
+                    if (i + 1 < n) load(i + 1, j, p);
+                    norm_turn<D>(x, A.qw != nullptr, A.eps, rot, A.interleaved, t);
+                    if (hd < A.q_heads)
+                        *(u32x4 *)(A.q_out + (int64_t)(q.row0 + i0 + i) * A.ldqo + hd * D + oct * 8) = bf16_8(x);
+                }
+            }
         }
         return;
     }
@@ -225,6 +336,9 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
     const int64_t chunk = page * A.c.heads + head;
     E *const kd = (E *)A.c.k + chunk * chunk_elems<D, BITS>(A.c), *const vd = (E *)A.c.v + chunk * chunk_elems<D, BITS>(A.c);
     const int row0 = q.row0 + sp.base - q.len;                      // row of the block's position 0
+    const Lane8 ln = make_lane(oct, rot, A.interleaved, A.kw);
+    uint64_t per_turn = 0;
+    if (rot && (tid & (next_pow2(h) - 1)) < h) per_turn = turns(A.inv_freq[tid & (next_pow2(h) - 1)]);
 
     for (int c0 = sp.lo / CH * CH; c0 < sp.hi; c0 += CH) {
         Raw8<F32> kr[NP], vr[NP];
@@ -241,10 +355,11 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
         }
         if (rot) {
             __syncthreads();                                        // the previous chunk has read its table
-            const int lo = max(sp.lo, c0), hi = min(sp.hi, c0 + CH);
-            for (int i = tid; i < (hi - lo) * h; i += TPB) {
-                const int t = lo + i / h, o = (lo - c0) * h + i;
-                turn(A.positions != nullptr ? A.positions[row0 + t] : sp.base + t, A.inv_freq[i % h], s_cs[0][o], s_cs[1][o]);
+            const int hi = min(sp.hi, c0 + CH), p2 = next_pow2(h), f = tid & (p2 - 1);
+            if (f < h) {
+                for (int t = max(sp.lo, c0) + tid / p2; t < hi; t += TPB / p2)
+                    turn(A.positions != nullptr ? A.positions[row0 + t] : sp.base + t, per_turn, s_cs[0][(t - c0) * h + f],
+                         s_cs[1][(t - c0) * h + f]);
             }
             __syncthreads();
         }
@@ -256,9 +371,11 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
             float x[8], y[8];
             kr[p].get(x);
             vr[p].get(y);
-            if (A.kw != nullptr) norm8<D>(x, A.kw, A.eps, oct);
-            const int of = min(t - c0, CH - 1) * h;
-            if (rot) rotate8<D>(x, oct, rot, A.interleaved, s_cs[0] + of, s_cs[1] + of);
+            if (rot || A.kw != nullptr) {
+                const int of = (t - c0) * h;
+                norm_turn<D>(x, A.kw != nullptr, A.eps, rot, A.interleaved,
+                             make_turn(ln, rot, A.interleaved, s_cs[0] + of, s_cs[1] + of));
+            }
             E *const kp = kd + kv::k_piece<D, W>(t0 + t, oct * 8) + (BITS == 8 ? oct % 2 * 8 : 0);
             if constexpr (BITS == 16) {
                 if (in) {
