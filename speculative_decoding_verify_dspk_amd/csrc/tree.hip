@@ -1,7 +1,7 @@
 // Bookkeeping of a drafted tree: ancestor masks and positions, and greedy
 // acceptance along the tree.  One wave per request, one lane per node (at
-// most 64); a parent's number is below its children's, so every walk over
-// parents or children ends after at most m steps.
+// most 64); a parent's number is below its children's, so a walk down the tree
+// ends after at most m steps.
 //
 // Bound by latency: a few hundred bytes per request, a dozen dependent steps.
 #include <hip/hip_runtime.h>
@@ -25,23 +25,26 @@ __global__ __launch_bounds__(64) void tree_layout_kernel(const int32_t *__restri
                                                          int32_t *__restrict__ positions) {
     const int r = blockIdx.x, j = threadIdx.x;
     bool fault;
-    const int p = load_parent(parents, r, m, j, fault);
-    uint64_t bits = 0;
-    int depth = -1, at = j < m && !fault ? j : -1;
-    bool root = false;
-    while (__any(at >= 0)) {                       // at strictly falls
-        const int up = __shfl(p, at < 0 ? 0 : at);
-        if (at >= 0) {
-            bits |= 1ull << at;
-            ++depth;
-            root = at == 0;
-            at = root ? -1 : up;
+    int p = load_parent(parents, r, m, j, fault);
+    const int32_t len = cache_len[r];
+    // what a node follows, by doubling: after k rounds the bits are those of its
+    // 2^k nearest (itself the first) and p is the one before them
+    uint64_t bits = 1ull << j;
+#pragma unroll
+    for (int k = 1; k < kMaxTree; k <<= 1) {
+        const int at = p < 0 ? 0 : p;
+        const uint64_t b = __shfl((unsigned long long)bits, at);
+        const int up = __shfl(p, at);
+        if (p >= 0) {
+            bits |= b;
+            p = up;
         }
     }
+    const bool there = (bits & 1) && !fault;       // follows the root
     if (j < m) {
         const int64_t i = (int64_t)r * m + j;
-        mask[i] = root ? bits : 0;                 // an absent node sees nothing
-        positions[i] = cache_len[r] + (root ? depth : 0);
+        mask[i] = there ? bits : 0;                // an absent node sees nothing
+        positions[i] = len + (there ? __popcll(bits) - 1 : 0);
     }
 }
 

@@ -11,7 +11,12 @@ Weights and activations are seeded synthetic tensors of the workload's shapes
 (``inputs.LAYER_SHAPES``).  Each decoder layer contributes four launches, as a
 real layer's dependencies allow: q/k/v grouped (they read the same rows), o,
 gate/up grouped, down.  The four inputs of a layer are independent N(0, 1)
-rows; attention, norms and the activation function are outside this path.
+rows; the residual stream's norms and the activation function are outside this
+path.  With ``attach_cache`` a layer's attention is part of it: q and k are
+normed per head and rotated, k and v stored in a paged cache, the rows attend
+over it, and o reads what comes out; ``set_tree`` makes the rows a drafted tree
+instead of a chain, and ``launch_commit`` moves the accepted path's entries
+together after the acceptance.
 
 A round's launches can be captured once into HIP graphs (``capture_round``)
 and replayed every round: the kernels take no host-side work between calls
@@ -31,6 +36,9 @@ class Layer:
     o: binding.DeviceQWeight
     gateup: list
     down: binding.DeviceQWeight
+
+
+HEAD_DIM = 128              # of every workload's layer
 
 
 @dataclass
@@ -84,6 +92,72 @@ class VerifyStack:
         self.ws_down = binding.alloc_workspace(wsb(H, F, M))
         self.ws_head = binding.alloc_workspace(binding.lmhead_workspace_bytes(V, M))
 
+        self.caches = None
+        self.tree_mask = self.positions = None
+
+    # -------------------------------------------------------------- attention
+    def attach_cache(self, context: int, bits: int = 16, page_tokens: int = 64, room: int = 0,
+                     eps: float = 1e-6) -> None:
+        """Gives every layer a k/v cache of one request holding ``context``
+        synthetic entries, with room for max_m rows and ``room`` more positions
+        after them; from then on the layers attend over it."""
+        import torch
+        D = HEAD_DIM
+        self.q_heads, self.kv_heads, self.eps = self.qdim // D, self.kvdim // D, eps
+        pages = -(-(context + self.max_m + room) // page_tokens)
+        g = inputs.device_generator(self.model, self.seed, "cache", context)
+        self.page_table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None].contiguous()
+        self.cache_len = torch.full((1,), context, dtype=torch.int32, device="cuda")
+        f32 = lambda *z: torch.empty(z, dtype=torch.float32, device="cuda")
+        self.caches, self.q_norm, self.k_norm = [], [], []
+        if context:
+            past = binding.AttnBatch(torch.zeros_like(self.cache_len), self.page_table, context)
+        for _ in range(self.n_layers):
+            c = binding.KVCache.alloc(pages, self.kv_heads, D, page_tokens, bits)
+            if context:
+                k, v = (f32(context, self.kvdim).normal_(generator=g) for _ in range(2))
+                binding.kv_append(c, past, k, v)
+            self.caches.append(c)
+            self.q_norm.append(f32(D).uniform_(0.8, 1.2, generator=g))
+            self.k_norm.append(f32(D).uniform_(0.8, 1.2, generator=g))
+        self.inv_freq = (1e6 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().cuda()
+        bf = dict(dtype=torch.bfloat16, device="cuda")
+        self.q_rot = torch.empty((self.max_m, self.qdim), **bf)
+        self.attn_out = torch.empty((self.max_m, self.qdim), **bf)
+        self.mask_buf = torch.empty((1, self.max_m), dtype=torch.int64, device="cuda")
+        self.position_buf = torch.empty((1, self.max_m), dtype=torch.int32, device="cuda")
+        self.ws_attn = binding.alloc_workspace(
+            binding.attn_workspace_bytes(self.q_heads, self.kv_heads, D, 1, self.max_m))
+
+    def set_tree(self, parents, m: int, stream=None) -> None:
+        """The next rounds' rows are the nodes of a tree (parents: int32 [m - 1]
+        on the device, see dspk_tree_layout); None: a chain again."""
+        if parents is None:
+            self.tree_mask = self.positions = None
+            return
+        # the same memory each round, so that captured rounds follow
+        self.tree_mask, self.positions = self.mask_buf[:, :m], self.position_buf[:, :m]
+        binding.tree_layout(parents, 1, m, self.cache_len, self.tree_mask, self.positions, stream)
+
+    def attention_calls(self, li: int, m: int, stream=None) -> list:
+        """Layer li's calls between q/k/v and o, their arguments marshalled."""
+        batch = binding.AttnBatch(self.cache_len, self.page_table, m)
+        c = self.caches[li]
+        pos = None if self.positions is None else self.positions.view(-1)
+        mask = None if self.tree_mask is None else self.tree_mask.view(-1)
+        return [binding.prepare_qkv_norm_rope_append(c, batch, *self.y_qkv, self.q_heads, self.q_rot,
+                                                     q_weight=self.q_norm[li], k_weight=self.k_norm[li], eps=self.eps,
+                                                     inv_freq=self.inv_freq, positions=pos, stream=stream),
+                binding.prepare_tree_attention(c, batch, self.q_rot, self.q_heads, self.attn_out, self.ws_attn,
+                                               tree_mask=mask, stream=stream)]
+
+    def launch_commit(self, path, accept_len, m: int, stream=None) -> None:
+        """After the acceptance of a tree of m nodes: the path's entries of every
+        layer move together and the cached length grows by the accepted nodes.
+        (A chain's entries are in place: its cached length grows by accept_len.)"""
+        binding.kv_commit(self.caches, binding.AttnBatch(self.cache_len, self.page_table, m), path, accept_len,
+                          self.cache_len, stream)
+
     # ------------------------------------------------------------------ sizes
     def layer_weight_bytes(self) -> int:
         L = self.layers[0][0]
@@ -97,9 +171,12 @@ class VerifyStack:
 
     # ---------------------------------------------------------------- launches
     def launch_layers(self, m: int, copy: int = 0, stream=None) -> None:
-        for L in self.layers[copy]:
+        for li, L in enumerate(self.layers[copy]):
             binding.qgemm_verify_grouped(L.qkv, self.x_attn, m, self.y_qkv, self.ws_qkv, stream)
-            binding.qgemm_verify(L.o, self.x_o, m, self.y_o, self.ws_o, stream)
+            if self.caches:
+                for call in self.attention_calls(li, m, stream):
+                    call()
+            binding.qgemm_verify(L.o, self.attn_out if self.caches else self.x_o, m, self.y_o, self.ws_o, stream)
             binding.qgemm_verify_grouped(L.gateup, self.x_mlp, m, self.y_gu, self.ws_gu, stream)
             binding.qgemm_verify(L.down, self.x_down, m, self.y_down, self.ws_down, stream)
 
@@ -111,9 +188,11 @@ class VerifyStack:
         """The round's projection and head calls at width m on weight copy
         ``copy`` with their arguments marshalled once: (layer calls, head call)."""
         layers = []
-        for L in self.layers[copy]:
-            layers += [binding.prepare_qgemm_grouped(L.qkv, self.x_attn, m, self.y_qkv, self.ws_qkv, stream),
-                       binding.prepare_qgemm(L.o, self.x_o, m, self.y_o, self.ws_o, stream),
+        for li, L in enumerate(self.layers[copy]):
+            layers += [binding.prepare_qgemm_grouped(L.qkv, self.x_attn, m, self.y_qkv, self.ws_qkv, stream)]
+            layers += self.attention_calls(li, m, stream) if self.caches else []
+            layers += [binding.prepare_qgemm(L.o, self.attn_out if self.caches else self.x_o, m, self.y_o, self.ws_o,
+                                             stream),
                        binding.prepare_qgemm_grouped(L.gateup, self.x_mlp, m, self.y_gu, self.ws_gu, stream),
                        binding.prepare_qgemm(L.down, self.x_down, m, self.y_down, self.ws_down, stream)]
         head = binding.prepare_lmhead(self.heads[copy], self.h, m, self.argmax, self.logits if want_logits else None,
