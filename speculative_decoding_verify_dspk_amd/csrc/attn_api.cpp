@@ -30,6 +30,7 @@ AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t b, int3
     p.blocks = (int32_t)((tiles + p.tiles - 1) / p.tiles);
     const int32_t most = cus > p.blocks ? cus / p.blocks : 1;         // one workgroup per CU
     p.groups = (int32_t)(units < most ? units : most);
+    p.pairs = per_seg == 2;
     // The last group of a segment adds the pieces of all by itself, at the rate
     // of one CU; where they are many, a launch of its own is faster (one request
     // of 8 rows, two tiles, 4 / 8 / 32 pieces: 11.5 / 15 / 26 us in one launch, 12.7
@@ -315,6 +316,7 @@ int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch
     A.blocks = p.blocks;
     A.groups = p.groups;
     A.join = p.join;
+    A.pairs = p.pairs;
     A.counters = (uint32_t *)workspace;
     A.part = (float *)((char *)workspace + p.off_part);
     return launch_result(dspk::launch_tree_attention(A, (hipStream_t)stream), who);

@@ -81,6 +81,7 @@ constexpr int attn_piece(int d, int rt) { return rt * (d / 16) * kAttnTile; }  /
 struct AttnPlan {
     int32_t tiles, blocks, groups;
     int32_t join;                   // shared segments are added by a launch of their own
+    int32_t pairs;                  // segments are of two units at most
     bool fits;                      // unit numbers fit 31 bits
     size_t off_part, ws_bytes;      // workspace: counters, then partial sums
 };
@@ -96,7 +97,7 @@ struct AttnArgs {
     int32_t rep;                    // q heads per kv head
     float scale;                    // of the scores, times log2(e)
     const uint64_t *mask;           // [total_rows], or NULL: a chain
-    int32_t tiles, blocks, groups, join;      // see AttnPlan
+    int32_t tiles, blocks, groups, join, pairs;      // see AttnPlan
     uint32_t *counters;             // arrivals at shared segments [groups][blocks][waves][kAttnCounter], zero between calls
     float *part;                    // partial sums [groups][blocks][2][attn_piece]
 };

@@ -331,7 +331,6 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
     const Span sp = span(q, tb);
     if (sp.lo >= sp.hi) return;
     const int64_t page = page_of(A.c, A.B, r, sp.base);
-    if (page < 0) return;
     const int t0 = sp.base & ((1 << A.c.page_shift) - 1);
     const int64_t chunk = page * A.c.heads + head;
     E *const kd = (E *)A.c.k + chunk * chunk_elems<D, BITS>(A.c), *const vd = (E *)A.c.v + chunk * chunk_elems<D, BITS>(A.c);
@@ -353,6 +352,7 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
                 vr[p].clear();
             }
         }
+        if (page < 0) return;                                       // asked after the loads have left; nothing is stored
         if (rot) {
             __syncthreads();                                        // the previous chunk has read its table
             const int hi = min(sp.hi, c0 + CH), p2 = next_pow2(h), f = tid & (p2 - 1);
@@ -426,7 +426,8 @@ __global__ __launch_bounds__(TPB) void kv_read_kernel(const ReadArgs A, const in
     constexpr int W = BITS == 16 ? 8 : 16;
     typedef typename std::conditional<BITS == 16, uint16_t, uint8_t>::type E;
     constexpr int VS = D + 16 / (int)sizeof(E);
-    __shared__ __attribute__((aligned(16))) E s_x[kBlockTokens * VS];
+    constexpr int N = kBlockTokens * D / W;         // pieces of a block
+    __shared__ __attribute__((aligned(16))) E s_x[2][kBlockTokens * VS];
     const int tid = threadIdx.x;
     const int head = blockIdx.x % A.c.heads, tb = blockIdx.x / A.c.heads % nb, r = blockIdx.x / A.c.heads / nb;
     kv::Req q = kv::request(A.B, A.c.page_shift, r);
@@ -436,52 +437,51 @@ __global__ __launch_bounds__(TPB) void kv_read_kernel(const ReadArgs A, const in
     const int64_t page = q.ok ? page_of(A.c, A.B, r, sp.base) : -1;
     const int t0 = sp.base & ((1 << A.c.page_shift) - 1);
     const int64_t chunk = page * A.c.heads + head;
-    for (int which = 0; which < 2; ++which) {
-        if (page >= 0) {
-            if (which) __syncthreads();                             // k's rows have left the buffer
-            const E *const src = (const E *)(which ? A.c.v : A.c.k) + chunk * chunk_elems<D, BITS>(A.c);
-            for (int i = tid; i < kBlockTokens * D / W; i += TPB) {
-                if (which == 0) {
-                    const int t = i / (16 * (D / W)) * 16 + i % 16;
-                    const int d = i / 64 % (D / (4 * W)) * 4 * W + i / 16 % 4 * W;
-                    if (t < sp.lo || t >= sp.hi) continue;
-                    *(u32x4 *)(s_x + t * VS + d) = *(const u32x4 *)(src + kv::k_piece<D, W>(t0 + t, d));
-                } else {
-                    const int sb = i / (64 * (D / 16)), vb = i / 64 % (D / 16), g = i / 16 % 4, d = vb * 16 + i % 16;
-                    const int first = sb * 4 * W + g * 4;
-                    if (first >= sp.hi || first + 4 * W - 16 + 3 < sp.lo) continue;
-                    struct { E e[W]; } x = __builtin_bit_cast(decltype(x),
-                                                              *(const u32x4 *)(src + kv::v_elem<D, W>(t0 + first, d)));
+    if (page >= 0) {
+        const E *const ks = (const E *)A.c.k + chunk * chunk_elems<D, BITS>(A.c);
+        const E *const vs = (const E *)A.c.v + chunk * chunk_elems<D, BITS>(A.c);
+#pragma unroll 4
+        for (int i = tid; i < N; i += TPB) {
+            const int t = i / (16 * (D / W)) * 16 + i % 16, d = i / 64 % (D / (4 * W)) * 4 * W + i / 16 % 4 * W;
+            const int sb = i / (64 * (D / 16)), vb = i / 64 % (D / 16), g = i / 16 % 4, dv = vb * 16 + i % 16;
+            const int first = sb * 4 * W + g * 4;                   // v's positions: first + 16 jj + i
+            const bool kin = t >= sp.lo && t < sp.hi, vin = first < sp.hi && first + 4 * W - 16 + 3 >= sp.lo;
+            u32x4 a = {}, b = {};
+            if (kin) a = *(const u32x4 *)(ks + kv::k_piece<D, W>(t0 + t, d));
+            if (vin) b = *(const u32x4 *)(vs + kv::v_elem<D, W>(t0 + first, dv));
+            if (kin) *(u32x4 *)(s_x[0] + t * VS + d) = a;
+            if (vin) {
+                struct { E e[W]; } x = __builtin_bit_cast(decltype(x), b);
 #pragma unroll
-                    for (int j = 0; j < W; ++j) s_x[(first + j / 4 * 16 + j % 4) * VS + d] = x.e[j];
-                }
+                for (int j = 0; j < W; ++j) s_x[1][(first + j / 4 * 16 + j % 4) * VS + dv] = x.e[j];
             }
-            __syncthreads();
         }
-        void *const out = which ? A.v : A.k;
-        const int64_t ld = which ? A.ldv : A.ldk;
-        for (int i = tid; i < (sp.hi - sp.lo) * (D / 8); i += TPB) {
-            const int t = sp.lo + i / (D / 8), d = i % (D / 8) * 8;
-            float x[8];
-            if (page < 0) {
+        __syncthreads();
+    }
+    const int rows = sp.hi - sp.lo;
+    for (int i = tid; i < 2 * rows * (D / 8); i += TPB) {
+        const int which = i >= rows * (D / 8), at = which ? i - rows * (D / 8) : i;
+        const int t = sp.lo + at / (D / 8), d = at % (D / 8) * 8;
+        float x[8];
+        if (page < 0) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(0x7fc00000u);
-            } else if constexpr (BITS == 16) {
-                Raw8<false> raw;
-                raw.load(s_x, t * VS + d);
-                raw.get(x);
-            } else {
-                const float s = (which ? A.c.vs : A.c.ks)[(chunk << A.c.page_shift) + t0 + t];
+            for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(0x7fc00000u);
+        } else if constexpr (BITS == 16) {
+            Raw8<false> raw;
+            raw.load(s_x[which], t * VS + d);
+            raw.get(x);
+        } else {
+            const float s = (which ? A.c.vs : A.c.ks)[(chunk << A.c.page_shift) + t0 + t];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = s * (float)(int8_t)s_x[t * VS + d + e];
-            }
-            const int64_t at = (int64_t)(q.row0 + sp.base + t - q.len) * ld + head * D + d;
-            if constexpr (F32) {
-                *(f32x4 *)((float *)out + at) = f32x4{x[0], x[1], x[2], x[3]};
-                *(f32x4 *)((float *)out + at + 4) = f32x4{x[4], x[5], x[6], x[7]};
-            } else {
-                *(u32x4 *)((uint16_t *)out + at) = bf16_8(x);
-            }
+            for (int e = 0; e < 8; ++e) x[e] = s * (float)(int8_t)s_x[which][t * VS + d + e];
+        }
+        const int64_t to = (int64_t)(q.row0 + sp.base + t - q.len) * (which ? A.ldv : A.ldk) + head * D + d;
+        if constexpr (F32) {
+            float *const out = (float *)(which ? A.v : A.k) + to;
+            *(f32x4 *)out = f32x4{x[0], x[1], x[2], x[3]};
+            *(f32x4 *)(out + 4) = f32x4{x[4], x[5], x[6], x[7]};
+        } else {
+            *(u32x4 *)((uint16_t *)(which ? A.v : A.k) + to) = bf16_8(x);
         }
     }
 }

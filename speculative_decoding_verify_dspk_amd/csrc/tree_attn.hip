@@ -143,8 +143,10 @@ struct Ranges {
     }
 };
 __device__ __forceinline__ Ranges ranges(const AttnArgs &A, int total) {
-    // fewer than two units each: two to some, which is no slower and leaves fewer pieces
-    const int groups = total > A.groups && total < 2 * A.groups ? (total + 1) / 2 : A.groups;
+    // Fewer than two units each: two to some, which is no slower and leaves fewer
+    // pieces.  Segments of two: whole, for a second step costs less than a join.
+    const bool two = total < 2 * A.groups && (total > A.groups || A.pairs);
+    const int groups = two ? (total + 1) / 2 : A.groups;
     Ranges R;
     R.q = total / groups;
     R.rem = total - R.q * groups;
