@@ -5,16 +5,15 @@
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i.k_j - max_j),
 //
 // j over the positions row i sees.  The rows of a request over one kv head are
-// cut into blocks of up to 32 (16 of 256 dimensions: what a wave's registers
-// hold).  A (request, kv head) is a segment, its cache positions are cut into
+// cut into blocks of 16 or 32 (what a wave's registers hold; attn_plan says
+// which).  A (request, kv head) is a segment, its cache positions are cut into
 // units of 256; groups of workgroups, one for each row block, take equal
 // contiguous ranges of all segments' units, so ragged batches load every CU
 // alike.  A group's workgroups sit on one XCD and stream the same k and v at the
-// same time, out of its L2 for all but the first.  A segment shared by groups
-// leaves partial sums in the workspace; the last to arrive adds them in order
-// (deterministic), each wave its own tiles, all pieces in flight at once.  (With
-// row groups as waves of one workgroup instead there were as many times more
-// pieces, and their addition took most of a call.)
+// same time, out of its L2 for all but the first (3 row blocks: 84 MB missed L2
+// of 240 MB asked for).  A segment shared by groups leaves partial sums in the
+// workspace; the last to arrive adds them in order (deterministic), each wave
+// its own tiles, or a launch of its own does where they are many.
 //
 // Within a workgroup each wave takes its own positions, so k and v go from
 // memory to the matrix cores without LDS or barriers: the cache is stored in
@@ -24,11 +23,22 @@
 // lanes, one value each.  The waves' results are joined through LDS when a
 // segment ends.
 //
-// Rounding: scores, maxima, sums and outputs are fp32.  A probability goes
-// into the second product as the sum of two bf16 (16 significant bits): with
-// one bf16 the output's error would be 1.4 times that of the final rounding
-// alone, and the matrix cores have the time.  8-bit codes are exact in bf16;
-// their scales multiply scores and probabilities in fp32.
+// Rounding: scores, statistics, sums and outputs are fp32.  Over a bf16 cache a
+// probability goes into the second product as the sum of two bf16 (16
+// significant bits): with one the output's error would be 1.4 times that of the
+// final rounding alone, and the matrix cores have the time.  8-bit codes are exact in
+// bf16 and fp16; their scales multiply scores and probabilities in fp32, and
+// the scaled probability goes in as one fp16 (11 bits, 2^-12 at most: a
+// hundredth of the output's own rounding in the mean square).
+//
+// What bounds it, measured on MI355X as passes back to back (32 q heads over 8
+// of 128 unless said): one token over 1021 positions 8.2 us, of which 2.2 is the
+// launch, 1.5 the lengths' way to the first page number, 1 the only step, 3.5
+// the way of the results through LDS, memory and the last workgroup; 4 requests
+// of 6 rows over up to 8190 positions 24.4 us (97 MB); 32 of 8 rows over up to
+// 16384 (1.37 GB) 247 us, 5.5 TB/s of the 6.5 this device streams.  Over 8-bit
+// caches of many rows the vector ALUs: decoding takes half of their work (17 rows
+// of 40 heads over 32768 positions, 70 MB: 38 us, ALUs busy for 55% of it).
 #include <hip/hip_runtime.h>
 
 #include "decode.h"
@@ -44,7 +54,6 @@ using kv::u32x4;
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int WAVES = kAttnWaves, TPB = 64 * WAVES;
@@ -245,11 +254,8 @@ __device__ __forceinline__ void wait_stores() {
 
 // Four neighbouring dimensions of a row, rounded to nearest even.
 __device__ __forceinline__ void store_out(uint16_t *dst, f32x4 x) {
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    u32x2 y;
-    y[0] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[0]) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[1]) << 16;
-    y[1] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2]) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[3]) << 16;
-    *(u32x2 *)dst = y;
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    *(u32x2 *)dst = __builtin_bit_cast(u32x2, __builtin_convertvector(x, bf16x4));
 }
 
 // A group's part of a segment: the one it starts, or the one it did not.
@@ -724,7 +730,8 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
 
 // The pieces of shared segments, where they are more than the last workgroup of
 // a segment adds in good time (A.join): a workgroup per 16 x 16 output tile, a
-// wave for every fourth piece, in group order.
+// wave for every fourth piece, in group order.  Latency: 3.4 us for 8 segments
+// of 24 pieces and 16 rows, 4.5 for 24 of 11 pieces and 32 rows.
 template <int D, int RT>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(const AttnArgs A) {
     constexpr int VB = D / 16, XB = 8;              // pieces of a wave in flight
