@@ -536,7 +536,8 @@ size_t dspk_kv_cache_bytes(int64_t pages, int32_t kv_heads, int32_t head_dim, in
  *   b          : requests, 1 .. 65535;
  *   max_rows   : rows of every request, or with row_start the most of one;
  *   total_rows : rows the row arrays hold (>= b * max_rows without row_start);
- *   max_pages  : entries per request of page_table;
+ *   max_pages  : entries per request of page_table, for at most 2^30 positions
+ *                (else DSPK_EUNSUPPORTED);
  *   row_start  : int32 [b + 1], request r owns rows row_start[r] ..
  *                row_start[r + 1] - 1; or NULL: rows r * max_rows ..;
  *   cache_len  : int32 [b], positions cached before the call's rows: row i of

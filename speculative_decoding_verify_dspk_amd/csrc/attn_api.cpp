@@ -122,7 +122,7 @@ int check_cache(const dspk_kv_cache *c, dspk::KvCache &out, const char *who) {
     return DSPK_OK;
 }
 
-int check_batch(const dspk_attn_batch *B, dspk::AttnBatch &out, const char *who) {
+int check_batch(const dspk_attn_batch *B, const dspk::KvCache &c, dspk::AttnBatch &out, const char *who) {
     if (B == nullptr) return fail(DSPK_EINVAL, "%s: batch descriptor is NULL", who);
     if (B->b < 1 || B->b > 65535) return fail(DSPK_EINVAL, "%s: b=%d out of 1..65535", who, B->b);
     if (B->max_rows < 1) return fail(DSPK_EINVAL, "%s: max_rows=%d must be >= 1", who, B->max_rows);
@@ -131,6 +131,10 @@ int check_batch(const dspk_attn_batch *B, dspk::AttnBatch &out, const char *who)
         return fail(DSPK_EINVAL, "%s: total_rows=%d holds fewer than b x max_rows rows", who, B->total_rows);
     if (!pointer(B->cache_len, 4) || !pointer(B->page_table, 4) || !aligned(B->row_start, 4))
         return fail(DSPK_EINVAL, "%s: cache_len or page_table NULL, or an array misaligned", who);
+    // positions, and what the kernels add to them, stay within 31 bits
+    if ((int64_t)B->max_pages << c.page_shift > 1 << 30)
+        return fail(DSPK_EUNSUPPORTED, "%s: max_pages=%d of %d positions (at most 2^30 positions per request)", who,
+                    B->max_pages, 1 << c.page_shift);
     out.b = B->b;
     out.max_rows = B->max_rows;
     out.total_rows = B->total_rows;
@@ -165,7 +169,7 @@ int append_common(const char *who, const dspk_kv_cache *cache, const dspk_attn_b
                   const void *k, int64_t ldk, const void *v, int64_t ldv, int32_t dtype, void *stream) {
     int rc = check_cache(cache, A.c, who);
     if (rc) return rc;
-    rc = check_batch(batch, A.B, who);
+    rc = check_batch(batch, A.c, A.B, who);
     if (rc) return rc;
     rc = check_rows(k, ldk, A.c.heads, A.c.d, dtype, "k", who);
     if (rc) return rc;
@@ -259,7 +263,7 @@ int dspk_kv_read(const dspk_kv_cache *cache, const dspk_attn_batch *batch, void 
     dspk::ReadArgs A{};
     int rc = check_cache(cache, A.c, who);
     if (rc) return rc;
-    rc = check_batch(batch, A.B, who);
+    rc = check_batch(batch, A.c, A.B, who);
     if (rc) return rc;
     rc = check_rows(k, ldk, A.c.heads, A.c.d, dtype, "k", who);
     if (rc) return rc;
@@ -289,7 +293,7 @@ int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch
     dspk::AttnArgs A{};
     int rc = check_cache(cache, A.c, who);
     if (rc) return rc;
-    rc = check_batch(batch, A.B, who);
+    rc = check_batch(batch, A.c, A.B, who);
     if (rc) return rc;
     if (A.B.max_rows > DSPK_MAX_TREE)
         return fail(DSPK_EUNSUPPORTED, "%s: max_rows=%d (at most %d rows of one request)", who, A.B.max_rows,
@@ -364,7 +368,7 @@ int dspk_kv_commit(int32_t count, const dspk_kv_cache *caches, const dspk_attn_b
             c.pages != A.c.pages)
             return fail(DSPK_EINVAL, "%s: caches of one call must have the same shape", who);
     }
-    int rc = check_batch(batch, A.B, who);
+    int rc = check_batch(batch, A.c, A.B, who);
     if (rc) return rc;
     if (A.B.row_start != nullptr || A.B.max_rows > DSPK_MAX_TREE)
         return fail(DSPK_EUNSUPPORTED, "%s: every request has max_rows nodes, at most %d (row_start must be NULL)", who,

@@ -183,3 +183,15 @@ def test_binding_checks_tensors():
     with pytest.raises(ValueError):
         binding.tree_attention(c, b, row(12, 256), 4, row(12, 256), e(256, dtype=torch.uint8),
                                tree_mask=e(12, dtype=torch.int32))
+
+
+def test_page_tables_past_2_to_the_30_positions_are_refused(lib):
+    """A length near 2^31 would pass 32 bits in position arithmetic."""
+    c = _cache(page_tokens=65536)
+    for pages, code in ((16385, EUNSUPPORTED), (32768, EUNSUPPORTED), ((1 << 31) - 1, EUNSUPPORTED)):
+        b = _batch(max_pages=pages)
+        assert _attend(lib, cache=c, batch=b) == code and _append(lib, cache=c, batch=b) == code
+        assert lib.dspk_kv_read(ctypes.byref(c), ctypes.byref(b), P, 1024, P, 1024, 1, None) == code
+        assert lib.dspk_kv_commit(1, ctypes.byref(c), ctypes.byref(b), P, P, None, None) == code
+    b = _batch(max_pages=16384)                                              # the most: refused for what follows it
+    assert _append(lib, cache=c, batch=b, k=None) == EINVAL
