@@ -235,6 +235,8 @@ int dspk_qkv_norm_rope_append(const dspk_kv_cache *cache, const dspk_attn_batch 
             return fail(DSPK_EINVAL, "%s: interleaved=%d (0 or 1)", who, prep->interleaved);
         if (!aligned(prep->positions, 4)) return fail(DSPK_EINVAL, "%s: positions misaligned", who);
     }
+    if ((const void *)q_out == q && (dtype != DSPK_BF16 || ldqo != ldq))
+        return fail(DSPK_EINVAL, "%s: q_out may be q only if q is bf16 with the same leading dimension", who);
     dspk::AppendArgs A{};
     A.q = q;
     A.ldq = ldq;
@@ -313,6 +315,7 @@ int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch
     if (!p.fits || (int64_t)A.c.heads * p.blocks > 65535) return fail(DSPK_EUNSUPPORTED, "%s: page table too large for one launch", who);
     if (!pointer(workspace, 256) || ws_bytes < p.ws_bytes)
         return fail(DSPK_EINVAL, "%s: workspace of %zu bytes required (256-byte aligned)", who, p.ws_bytes);
+    if (q == out) return fail(DSPK_EINVAL, "%s: out must not be q", who);
     A.q = q;
     A.ldq = ldq;
     A.out = out;

@@ -93,10 +93,10 @@ int main() {
                                     const int before = g_launches;
                                     const int64_t ld = (int64_t)hkv * rep * d;
                                     int rc = dspk_tree_attention(&c, &B, (uint16_t *)P, ld, hkv * rep, 0.1f, nullptr,
-                                                                 (uint16_t *)P, ld, (void *)g_ws, g_ws_bytes, nullptr);
+                                                                 (uint16_t *)(P + 4096), ld, (void *)g_ws, g_ws_bytes, nullptr);
                                     CHECK(rc == DSPK_OK && g_launches == before + 1);
                                     rc = dspk_tree_attention(&c, &B, (uint16_t *)P, ld, hkv * rep, 0.1f, nullptr,
-                                                             (uint16_t *)P, ld, (void *)g_ws, g_ws_bytes - 256, nullptr);
+                                                             (uint16_t *)(P + 4096), ld, (void *)g_ws, g_ws_bytes - 256, nullptr);
                                     CHECK(rc == DSPK_EINVAL && g_launches == before + 1 && !g_msg.empty());
                                 }
                             }

@@ -195,3 +195,14 @@ def test_page_tables_past_2_to_the_30_positions_are_refused(lib):
         assert lib.dspk_kv_commit(1, ctypes.byref(c), ctypes.byref(b), P, P, None, None) == code
     b = _batch(max_pages=16384)                                              # the most: refused for what follows it
     assert _append(lib, cache=c, batch=b, k=None) == EINVAL
+
+
+def test_outputs_over_inputs_are_refused(lib):
+    """Workgroups read q rows that others would have overwritten."""
+    assert _attend(lib, q=P, out=P) == EINVAL
+    assert "out must not be q" in lib.dspk_last_error().decode()
+    c, b, d = _cache(), _batch(), binding.QKPrepDesc(1e-6, None, None, None, 0, 0, None)
+    for dt, ldq, ldo in ((0, 4096, 4096), (1, 4096, 4608)):
+        assert lib.dspk_qkv_norm_rope_append(ctypes.byref(c), ctypes.byref(b), ctypes.byref(d), P, ldq, 2 * P, 1024,
+                                             3 * P, 1024, dt, 32, P, ldo, None) == EINVAL
+        assert "q_out may be q only" in lib.dspk_last_error().decode()
