@@ -284,9 +284,10 @@ class KVCache:
                    *((scales(), scales()) if bits == 8 else (None, None)))
 
 
-def _int32(t, name: str):
-    if t is not None and (t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous()):
-        raise ValueError(f"{name}: expected a contiguous int32 tensor")
+def _int32(t, name: str, need: int = 0):
+    if t is not None and (t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous()
+                          or t.numel() < need):
+        raise ValueError(f"{name}: expected a contiguous int32 tensor" + (f" of at least {need} entries" if need else ""))
     return t
 
 
@@ -511,14 +512,20 @@ def prepare_tree_attention(cache: KVCache, batch: AttnBatch, q, q_heads: int, ou
 
 
 def prepare_tree_layout(parents, b: int, m_rows: int, cache_len, tree_mask, positions, stream=None) -> Prepared:
-    return Prepared("dspk_tree_layout", _ptr(_int32(parents, "parents")), b, m_rows,
-                    _int32(cache_len, "cache_len").data_ptr(), tree_mask.data_ptr(),
-                    _int32(positions, "positions").data_ptr(),
+    if tree_mask.element_size() != 8 or not tree_mask.is_contiguous() or tree_mask.numel() < b * m_rows:
+        raise ValueError(f"tree_mask: expected a contiguous 64-bit tensor of at least {b * m_rows} entries")
+    return Prepared("dspk_tree_layout", _ptr(_int32(parents, "parents", b * (m_rows - 1))), b, m_rows,
+                    _int32(cache_len, "cache_len", b).data_ptr(), tree_mask.data_ptr(),
+                    _int32(positions, "positions", b * m_rows).data_ptr(),
                     _stream(stream)).holding(parents, cache_len, tree_mask, positions)
 
 
 def prepare_accept_tree_greedy(target_ids, draft_ids, parents, b: int, m_rows: int, accept_len, committed, path,
                                stream=None) -> Prepared:
+    for t, name, need in ((target_ids, "target_ids", b * m_rows), (draft_ids, "draft_ids", b * (m_rows - 1)),
+                          (parents, "parents", b * (m_rows - 1)), (accept_len, "accept_len", b),
+                          (committed, "committed", b * m_rows), (path, "path", b * m_rows)):
+        _int32(t, name, need)
     return Prepared("dspk_accept_tree_greedy", target_ids.data_ptr(), _ptr(draft_ids), _ptr(parents), b, m_rows,
                     accept_len.data_ptr(), committed.data_ptr(), path.data_ptr(),
                     _stream(stream)).holding(target_ids, draft_ids, parents, accept_len, committed, path)
@@ -526,9 +533,10 @@ def prepare_accept_tree_greedy(target_ids, draft_ids, parents, b: int, m_rows: i
 
 def prepare_kv_commit(caches: list, batch: AttnBatch, path, accept_len, new_len=None, stream=None) -> Prepared:
     descs = (KVCacheDesc * len(caches))(*[c.desc for c in caches])
+    b = batch.desc.b
     return Prepared("dspk_kv_commit", len(caches), descs, ctypes.byref(batch.desc),
-                    _int32(path, "path").data_ptr(), _int32(accept_len, "accept_len").data_ptr(),
-                    _ptr(_int32(new_len, "new_len")),
+                    _int32(path, "path", b * batch.desc.max_rows).data_ptr(),
+                    _int32(accept_len, "accept_len", b).data_ptr(), _ptr(_int32(new_len, "new_len", b)),
                     _stream(stream)).holding(caches, batch, path, accept_len, new_len)
 
 

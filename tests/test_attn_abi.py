@@ -206,3 +206,25 @@ def test_outputs_over_inputs_are_refused(lib):
         assert lib.dspk_qkv_norm_rope_append(ctypes.byref(c), ctypes.byref(b), ctypes.byref(d), P, ldq, 2 * P, 1024,
                                              3 * P, 1024, dt, 32, P, ldo, None) == EINVAL
         assert "q_out may be q only" in lib.dspk_last_error().decode()
+
+
+def test_binding_checks_sizes_of_trees():
+    import torch
+    i = lambda *z: torch.zeros(z, dtype=torch.int32)
+    b, m = 2, 5
+    good = dict(target_ids=i(b, m), draft_ids=i(b, m - 1), parents=i(b, m - 1), accept_len=i(b), committed=i(b, m),
+                path=i(b, m))
+    for name, t in good.items():
+        for bad in (t.view(-1)[:-1], t.long()):
+            with pytest.raises(ValueError, match=name):
+                binding.prepare_accept_tree_greedy(**{**good, name: bad}, b=b, m_rows=m)
+    good = dict(parents=i(b, m - 1), cache_len=i(b), tree_mask=i(b, m).long(), positions=i(b, m))
+    for name, t in good.items():
+        with pytest.raises(ValueError, match=name):
+            binding.prepare_tree_layout(**{**good, name: t.view(-1)[:-1]}, b=b, m_rows=m)
+    c = binding.KVCache.alloc(4, 2, 64, device="cpu")
+    batch = binding.AttnBatch(i(b), i(b, 2), m)
+    good = dict(path=i(b, m), accept_len=i(b), new_len=i(b))
+    for name, t in good.items():
+        with pytest.raises(ValueError, match=name):
+            binding.prepare_kv_commit([c], batch, **{**good, name: t.view(-1)[:-1]})
