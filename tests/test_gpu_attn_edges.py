@@ -42,3 +42,93 @@ def test_batches_without_rows(b, pages):
     torch.cuda.synchronize()
     assert (out == 7).all() and (back == 7).all() and torch.equal(R.cache.k, before)
     assert_attention(run_attention(R, q, 4, ws=ws), *_reference(R, q))
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_calls_on_two_streams_at_once(bits):
+    """Calls that overlap, each with a workspace of its own, over one cache."""
+    import torch
+    R = Round([5000], [6], 2, 128, bits, 64, seed=21)
+    q = _q(R, 8)
+    want = run_attention(R, q, 8)
+    qd = dev(q.reshape(R.total, -1), torch.bfloat16)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(qd) for _ in sides]
+    spaces = [binding.alloc_workspace(binding.attn_workspace_bytes(8, 2, 128, 1, 6)) for _ in sides]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, o, ws in zip(sides, outs, spaces):
+            binding.tree_attention(R.cache, R.batch, qd, 8, o, ws, stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert np.array_equal(o.float().cpu().numpy().reshape(want.shape), want)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_requests_that_share_pages(bits):
+    """Requests over one prefix: full pages in common, the rest their own; and
+    the same request twice gives the same bits."""
+    R = Round([128 + 9], [4], 2, 64, bits, 64, seed=22, pages=16)
+    q = _q(R, 4)
+    alone = run_attention(R, q, 4)
+    table = np.repeat(R.table_np, 3, axis=0)
+    lens = [137, 137, 60]
+    batch = binding.AttnBatch(i32(lens), dev(table), 4)
+    three = np.concatenate([q, q, q])
+    T = Round([0], [1], 2, 64, bits, 64, seed=23)
+    T.cache, T.batch, T.lens, T.max_rows = R.cache, batch, lens, 4
+    got = run_attention(T, three, 4)
+    assert np.array_equal(got[:4], got[4:8])
+    assert_attention(got[:4], *_reference(R, q))
+    # 60 cached positions and the four after them
+    ref, mag = oa.attention(q, R.k[0][:64], R.v[0][:64], 60, chain_masks(4), R.d ** -0.5)
+    assert_attention(got[8:], ref, mag)
+    assert np.array_equal(alone, run_attention(R, q, 4))
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("lens,rows,hq,hkv,d", [
+    ([700, 3, 0, 2500, 260], [9, 0, 1, 33, 4], 12, 2, 128),         # additions by a launch of their own, two row tiles
+    ([8000, 11, 900], [1, 5, 2], 16, 1, 128),                       # few pieces, many groups
+    ([6000, 500], [3, 7], 4, 1, 256),
+    ([257, 511, 255, 300], [1, 1, 1, 0], 8, 2, 128),                # segments of one and two units
+    ([33 * i for i in range(150)], [i % 4 for i in range(150)], 8, 2, 64),
+])
+def test_ragged_batches_split_over_workgroups(lens, rows, hq, hkv, d, bits):
+    R = Round(lens, rows, hkv, d, bits, 64, seed=len(lens), max_rows=max(rows) + 1)
+    q = _q(R, hq)
+    got = run_attention(R, q, hq)
+    for r in range(len(lens)):
+        if rows[r]:
+            assert_attention(got[R.starts[r]:R.starts[r + 1]], *_reference(R, q, r), f"request {r}")
+    assert np.array_equal(got, run_attention(R, q, hq))
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_rows_that_are_not_finite_stay_alone(bits):
+    """NaN and infinities in a row of q reach no other row."""
+    R = Round([300], [12], 2, 128, bits, 64, seed=24)
+    q = _q(R, 8)
+    clean = run_attention(R, q, 8)
+    q[3, 5], q[7, 0, 9] = np.nan, np.inf
+    got = run_attention(R, q, 8)
+    assert np.isnan(got[3, 5]).all()
+    keep = np.ones(got.shape[:2], bool)
+    keep[3, 5] = keep[7, 0] = False
+    assert np.array_equal(got[keep], clean[keep])
+
+
+def test_workspace_of_the_largest_serves_calls_of_every_shape():
+    """One workspace, calls of different heads, dimensions and formats in turn."""
+    import torch
+    shapes = [([900], [1], 32, 8, 128, 16), ([2000], [17], 40, 8, 128, 8), ([3000, 40], [4, 4], 4, 1, 256, 16),
+              ([600], [64], 64, 1, 64, 8)]
+    size = max(binding.attn_workspace_bytes(hq, hkv, d, len(lens), max(rows)) for lens, rows, hq, hkv, d, _ in shapes)
+    ws = binding.alloc_workspace(size)
+    made = [(R, _q(R, hq), hq) for R, hq in ((Round(lens, rows, hkv, d, bits, 64, seed=hq), hq)
+                                             for lens, rows, hq, hkv, d, bits in shapes)]
+    want = [run_attention(R, q, hq) for R, q, hq in made]
+    for i in (0, 2, 1, 3, 3, 0, 1, 2):
+        R, q, hq = made[i]
+        assert np.array_equal(run_attention(R, q, hq, ws=ws), want[i]), i
+    torch.cuda.synchronize()
