@@ -10,7 +10,8 @@
 // (kv_layout.h), so v's positions lie next to each other: a workgroup takes
 // the rows of one 64-position block of one request and head and turns v
 // through LDS, so that whole 16-byte pieces are written wherever the rows
-// fill them.  q's workgroups take rows and keep four loads per lane on their
+// fill them (32 positions, half an 8-bit piece, where there are few blocks).
+// q's workgroups take rows and keep four loads per lane on their
 // way (one: 51 us for the prompts below).
 //
 // Bound by memory traffic for prompts, by the latency of one load-compute-store
@@ -32,6 +33,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int TPB = 256;
 constexpr int kChunk = 16;          // k/v positions whose cosines are held at a time
+constexpr int kBlockShift = 6;      // log2 of a block's positions
+static_assert(1 << kBlockShift == kBlockTokens, "blocks");
 constexpr int kQRows = 4;           // q rows of a workgroup, of many
 
 // Eight lanes' worth of geometry: a head's row is held by D / 8 lanes, eight
@@ -244,16 +247,16 @@ __device__ __forceinline__ u32x2 codes8(const float (&x)[8], float &scale) {
     return r;
 }
 
-// The rows of request q that lie in block tb of its touched blocks: positions
-// base + lo .. base + hi - 1.
+// The rows of request q that lie in block tb of its touched blocks of 2^bs
+// positions: positions base + lo .. base + hi - 1.
 struct Span {
     int32_t base, lo, hi;
 };
-__device__ __forceinline__ Span span(const kv::Req &q, int tb) {
+__device__ __forceinline__ Span span(const kv::Req &q, int tb, int bs = kBlockShift) {
     Span s;
-    s.base = (q.len / kBlockTokens + tb) * kBlockTokens;
+    s.base = ((q.len >> bs) + tb) << bs;
     s.lo = max(q.len - s.base, 0);
-    s.hi = min(q.len + q.rows - s.base, kBlockTokens);
+    s.hi = min(q.len + q.rows - s.base, 1 << bs);
     return s;
 }
 // The page of a position, or -1 where its number is none of the cache's.
@@ -270,7 +273,7 @@ __device__ __forceinline__ int64_t chunk_elems(const KvCache &c) {
 // Rows are taken in chunks whose cosines and sines are worked out first, each
 // once per workgroup; the chunk's elements are on their way meanwhile.
 template <int D, int BITS, bool F32>
-__global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const int kv_blocks, const int nb,
+__global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const int kv_blocks, const int nb, const int bs,
                                                      const int q_blocks, const int q_rows, const int slices) {
     constexpr int L = Geo<D>::L, R = Geo<D>::R, W = BITS == 16 ? 8 : 16;
     constexpr int CH = kChunk > R ? kChunk : R, NP = CH / R;        // k/v positions of a chunk, passes over them
@@ -335,7 +338,7 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
     const int head = blockIdx.x % A.c.heads, tb = blockIdx.x / A.c.heads % nb, r = blockIdx.x / A.c.heads / nb;
     const kv::Req q = kv::request(A.B, A.c.page_shift, r);
     if (!q.ok) return;
-    const Span sp = span(q, tb);
+    const Span sp = span(q, tb, bs);
     if (sp.lo >= sp.hi) return;
     const int64_t page = page_of(A.c, A.B, r, sp.base);
     const int t0 = sp.base & ((1 << A.c.page_shift) - 1);
@@ -405,20 +408,34 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
         }
     }
     __syncthreads();
-    // pieces of the turned v, those that hold rows
+    // the turned v; a whole block of 8-bit pieces 16 bytes at a time (8192 rows
+    // there and back 24.3 us, with halves 25.0)
     constexpr int per = 64 * (D / 16);                              // pieces of 4W positions
-    for (int i = sp.lo / (4 * W) * per + tid; i < (sp.hi + 4 * W - 1) / (4 * W) * per; i += TPB) {
-        const int sb = i / per, vb = i / 64 % (D / 16), g = i / 16 % 4, d = vb * 16 + i % 16;
-        const int first = sb * 4 * W + g * 4;                       // the piece's positions: first + 16 jj + i
-        if (first >= sp.hi || first + 4 * W - 16 + 3 < sp.lo) continue;
-        E *const dst = vd + kv::v_elem<D, W>(t0 + first, d);
-        if (first >= sp.lo && first + 4 * W - 16 + 3 < sp.hi) {
+    if (BITS == 8 && sp.hi - sp.lo == kBlockTokens) {
+        for (int i = tid; i < per; i += TPB) {
+            const int vb = i / 64, g = i / 16 % 4, d = vb * 16 + i % 16;
             E e[W];
 #pragma unroll
-            for (int j = 0; j < W; ++j) e[j] = s_v[(first + j / 4 * 16 + j % 4) * VS + d];
-            *(u32x4 *)dst = __builtin_bit_cast(u32x4, e);
+            for (int j = 0; j < W; ++j) e[j] = s_v[(g * 4 + j / 4 * 16 + j % 4) * VS + d];
+            *(u32x4 *)(vd + kv::v_elem<D, W>(t0 + g * 4, d)) = __builtin_bit_cast(u32x4, e);
+        }
+        return;
+    }
+    // of every piece the 8 elements that lie in 32 positions (all of a bf16
+    // piece, half of an 8-bit one), where they hold rows
+    typedef typename std::conditional<BITS == 16, u32x4, u32x2>::type P8;
+    for (int i = sp.lo / 32 * per + tid; i < (sp.hi + 31) / 32 * per; i += TPB) {
+        const int sb = i / per, vb = i / 64 % (D / 16), g = i / 16 % 4, d = vb * 16 + i % 16;
+        const int first = sb * 32 + g * 4;                          // their positions: first + 16 jj + i
+        if (first >= sp.hi || first + 19 < sp.lo) continue;
+        E *const dst = vd + kv::v_elem<D, W>(t0 + first, d);
+        if (first >= sp.lo && first + 19 < sp.hi) {
+            E e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = s_v[(first + j / 4 * 16 + j % 4) * VS + d];
+            *(P8 *)dst = __builtin_bit_cast(P8, e);
         } else {
-            for (int j = 0; j < W; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const int t = first + j / 4 * 16 + j % 4;
                 if (t >= sp.lo && t < sp.hi) dst[j] = s_v[t * VS + d];
             }
@@ -582,23 +599,33 @@ void with_format(const KvCache &c, F f) {
     else bits(integral_constant<int, 256>());
 }
 
-// Blocks of 64 positions that a request of n rows can touch.
-int touched_blocks(int32_t n) { return (n + kBlockTokens - 2) / kBlockTokens + 1; }
+// Blocks of 2^bs positions that a request of n rows can touch.
+int touched_blocks(int32_t n, int bs = kBlockShift) { return ((n + (1 << bs) - 2) >> bs) + 1; }
 
 }  // namespace
 
 hipError_t launch_append(const AppendArgs &A, hipStream_t s) {
-    const int nb = touched_blocks(A.B.max_rows), kvb = A.B.b * nb * A.c.heads;
-    // q: few rows go one to a workgroup, sliced further into passes, for latency; many in chunks
+    // Few blocks are halved, to double the workgroups at work: norm, rotation and
+    // store of one request of 128 / 512 rows of 32 + 8 + 8 heads 9.9 / 10.7 -> 6.6 /
+    // 7.2 us; more (960 of 64 positions, the prompts above) take 41.5 us whole and
+    // 44.6 halved.
+    int bs = kBlockShift, nb = touched_blocks(A.B.max_rows), kvb = A.B.b * nb * A.c.heads;
+    if (kvb <= 512) {
+        nb = touched_blocks(A.B.max_rows, --bs);
+        kvb = A.B.b * nb * A.c.heads;
+    }
+    // q: few rows go one to a workgroup, sliced further into passes, for latency;
+    // many in chunks (40 heads: 32 requests of 8 rows 7.2 us singly and 8.9 in
+    // chunks, 512 rows 11.1 and 10.8, 2048 rows 17.7 and 14.4)
     const bool many = A.B.total_rows >= 1024;
     const int q_rows = many ? kQRows : 1, q_blocks = (A.B.max_rows + q_rows - 1) / q_rows;
     const int passes = (A.q_heads * A.c.d + TPB * 8 - 1) / (TPB * 8), slices = many ? 1 : passes;
     const int grid = kvb + (A.q == nullptr ? 0 : A.B.b * q_blocks * slices);
     with_format(A.c, [&](auto d, auto bits) {
         if (A.f32)
-            hipLaunchKernelGGL((append_kernel<d(), bits(), true>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, q_blocks, q_rows, slices);
+            hipLaunchKernelGGL((append_kernel<d(), bits(), true>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, bs, q_blocks, q_rows, slices);
         else
-            hipLaunchKernelGGL((append_kernel<d(), bits(), false>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, q_blocks, q_rows, slices);
+            hipLaunchKernelGGL((append_kernel<d(), bits(), false>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, bs, q_blocks, q_rows, slices);
     });
     return hipGetLastError();
 }

@@ -132,3 +132,40 @@ def test_workspace_of_the_largest_serves_calls_of_every_shape():
         R, q, hq = made[i]
         assert np.array_equal(run_attention(R, q, hq, ws=ws), want[i]), i
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("bits,d,f32", [(16, 128, True), (8, 128, False), (8, 64, True), (16, 256, False)])
+def test_many_blocks_at_once_equal_few_at_a_time(bits, d, f32):
+    """Rows of many requests in one call and request by request, in two parts,
+    give the same cache and the same q to the bit."""
+    import torch
+    from attnutil import make_cache, page_table
+    lens, rows, heads, hq = [0, 37, 64, 130, 5], [600, 411, 512, 64, 1], 16, 16
+    assert sum(rows) >= 1024 and 5 * 10 * heads > 512
+    g = torch.Generator(device="cuda").manual_seed(31)
+    dt = torch.float32 if f32 else torch.bfloat16
+    q, k, v = (torch.empty((sum(rows), heads * d), dtype=dt, device="cuda").normal_(generator=g) for _ in range(3))
+    full = [n + m for n, m in zip(lens, rows)]
+    pages = sum(-(-n // 64) for n in full)
+    table = dev(page_table(full, 64, pages, 3))
+    start = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    w = torch.rand((2, d), device="cuda", generator=g) + 0.5
+    freq = 1e4 ** (-torch.arange(0, d, 2, device="cuda") / d)
+    how = dict(q_weight=w[0].contiguous(), k_weight=w[1].contiguous(), inv_freq=freq)
+    got = []
+    for parts in (False, True):
+        c = make_cache(pages, heads, d, 64, bits)
+        out = torch.zeros((sum(rows), hq * d), dtype=torch.bfloat16, device="cuda")
+        if parts:
+            for r, (n, m) in enumerate(zip(lens, rows)):
+                for a, e in ((0, m // 3), (m // 3, m)):
+                    if a < e:
+                        s = slice(int(start[r]) + a, int(start[r]) + e)
+                        batch = binding.AttnBatch(i32([n + a]), table[r:r + 1], e - a)
+                        binding.qkv_norm_rope_append(c, batch, q[s], k[s], v[s], hq, out[s], **how)
+        else:
+            batch = binding.AttnBatch(i32(lens), table, max(rows), sum(rows), dev(start))
+            binding.qkv_norm_rope_append(c, batch, q, k, v, hq, out, **how)
+        got.append([out, c.k, c.v] + ([c.k_scales, c.v_scales] if bits == 8 else []))
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
