@@ -25,12 +25,8 @@ AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t b, int3
     // and v half as often.  32 q heads over 8, 8 / 16 / 64 rows of one request, one
     // tile against two: 8.4 / 8.5 / 14.1 us against 12.7 / 12.7 / 19.8 at 1000
     // positions, 12.5 / 14.9 / 34.4 against 13.5 / 15.0 / 28.1 at 8000 (8 bits).
-    // In units x tiles per CU: 8 (4 requests of 6 rows over 40 heads, 8000
-    // positions, bf16) 24.0 against 26.6 us, 16 (16 rows over 32 heads, one
-    // request of 32000 / four of 8000) 38.0 / 26.6 against 32.3 / 28.8, 32 (four of
-    // 16000) 62 against 54; between 8 and 16 the two cross.
     const int most_tiles = attn_tiles(d);
-    p.tiles = units <= 12 * (int64_t)cus / tiles ? 1 : most_tiles < tiles ? most_tiles : (int32_t)tiles;
+    p.tiles = units <= 8 * (int64_t)cus / tiles ? 1 : most_tiles < tiles ? most_tiles : (int32_t)tiles;
     p.blocks = (int32_t)((tiles + p.tiles - 1) / p.tiles);
     const int32_t most = cus > p.blocks ? cus / p.blocks : 1;         // one workgroup per CU
     p.groups = (int32_t)(units < most ? units : most);
