@@ -20,11 +20,14 @@ AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t b, int3
     const int64_t segs = (int64_t)b * kv_heads;
     p.fits = segs <= INT32_MAX / per_seg;                             // segs * per_seg, without overflowing
     const int64_t units = p.fits ? segs * per_seg : INT32_MAX;
-    // One row tile per wave where a CU gets few units: a launch of two is some 3
+    // One row tile per wave where a CU gets few units: a launch of two is some 2
     // us slower before its first unit (twice the registers and LDS), but takes k
-    // and v half as often.  32 q heads over 8, 8 / 16 / 64 rows of one request, one
-    // tile against two: 8.4 / 8.5 / 14.1 us against 12.7 / 12.7 / 19.8 at 1000
-    // positions, 12.5 / 14.9 / 34.4 against 13.5 / 15.0 / 28.1 at 8000 (8 bits).
+    // and v half as often.  One tile against two, by units x tiles per CU, caches
+    // in memory, 8 k/v heads: 2 (16 rows of 32 heads, one request of 4000
+    // positions, bf16) 13.3 against 14.9 us; 4 (6 rows, four of 4000) 21.6 against
+    // 24.2; 8 (6 rows, four of 8000) 30.2 / 30.6, (16 rows, one of 16000) 30.5 /
+    // 27.8; 12 (17 rows of 40 heads, one of 16000) 36.8 / 31.5; 16 (16 rows, one of
+    // 32000) 47.0 / 38.4.  8 bits alike: 19.5 / 22.7 at 4, 42.9 / 34.0 at 16.
     const int most_tiles = attn_tiles(d);
     p.tiles = units <= 8 * (int64_t)cus / tiles ? 1 : most_tiles < tiles ? most_tiles : (int32_t)tiles;
     p.blocks = (int32_t)((tiles + p.tiles - 1) / p.tiles);

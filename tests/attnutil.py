@@ -80,7 +80,7 @@ def pools_host(c):
 
 
 class Round:
-    """Requests with cached entries and this round's rows: random k/v appended
+    """Requests with cached entries and a call's rows: random k/v appended
     to a poisoned cache, their values as the cache holds them on the host."""
 
     def __init__(self, lens, rows, heads, d, bits=16, page=64, seed=0, std=1.0, max_rows=None, pages=None):
