@@ -35,8 +35,8 @@
 // of 128 unless said): one token over 1021 positions 8.2 us, of which 2.2 is the
 // launch, 1.5 the lengths' way to the first page number, 1 the only step, 3.5
 // the way of the results through LDS, memory and the last workgroup; 4 requests
-// of 6 rows over up to 8190 positions 24.4 us (97 MB); 32 of 8 rows over up to
-// 16384 (1.37 GB) 247 us, 5.5 TB/s of the 6.5 this device streams.  Over 8-bit
+// of 6 rows over up to 8190 positions 25.7 us (97 MB); 32 of 8 rows over up to
+// 16384 (1.37 GB) 248 us, 5.5 TB/s of the 6.5 this device streams.  Over 8-bit
 // caches of many rows the vector ALUs: decoding takes half of their work (17 rows
 // of 40 heads over 32768 positions, 70 MB: 38 us, ALUs busy for 55% of it).
 #include <hip/hip_runtime.h>
