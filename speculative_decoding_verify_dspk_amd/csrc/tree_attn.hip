@@ -66,8 +66,13 @@ constexpr int kJoinWaves = 4;
 // Limits of what a lane adds at a time, in units of its row's reference, before
 // the reference has to rise.  8 bits: a probability times its v scale goes into
 // the product as fp16, at most 2^15, 2^4 at the reference; it keeps its 11 bits
-// down to 2^-18 of the reference.  Sums, and bf16 pairs, have fp32's range.
-constexpr float kMostF16 = 32768.f, kMostSum = 0x1p60f, kBase8 = 4.f;
+// down to 2^-18 of the reference; the sum of probabilities alone, which small v
+// scales let grow to 2^54 at the reference, has fp32's range.  bf16: products with
+// v share that range, of which v has what 2^32 per position leaves, up to 2^78 at
+// 2^17 positions.
+constexpr float kMostF16 = 32768.f, kBase8 = 4.f;
+template <int BITS>
+constexpr float kMostSum = BITS == 8 ? 0x1p60f : 0x1p32f;
 // The reference of a row that has seen nothing yet, for 2^(-inf - ref) = 0.
 __device__ __forceinline__ float zero_if_none(float m) { return m == NEG_INF ? 0.f : m; }
 
@@ -322,7 +327,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
 
         // Outputs and sum of each row, in units of 2^m: m is the row's reference,
         // the maximum (log2) of probability times v scale over the first positions that
-        // it sees.  Later ones may pass it by 2^11 (8 bits) or 2^60 before anything has to
+        // it sees.  Later ones may pass it by 2^11 (8 bits) or 2^32 before anything has to
         // be scaled down; then, which real scores hardly ever ask for, the wave
         // starts its positions over with the higher reference.  So the loop neither
         // takes maxima nor rescales.
@@ -536,7 +541,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                             for (int i = 0; i < 8; ++i) p[i] = s[rt][i / 4][i % 4] == NEG_INF ? 0.f : p[i];
                         }
                     }
-                    rises[rt] = sum > kMostSum;
+                    rises[rt] = sum > kMostSum<BITS>;
                     if constexpr (BITS == 8)
                         rises[rt] |= max3(max3(p[0], p[1], p[2]), max3(p[3], p[4], p[5]), fmaxf(p[6], p[7])) > kMostF16;
                     l[rt] += sum;

@@ -169,3 +169,27 @@ def test_many_blocks_at_once_equal_few_at_a_time(bits, d, f32):
         got.append([out, c.k, c.v] + ([c.k_scales, c.v_scales] if bits == 8 else []))
     for a, b in zip(*got):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("m", [1, 17])
+def test_large_v_under_scores_that_rise(m):
+    """v of 2^75 while a wave's scores rise by up to 2^56 of its first ones: sums
+    of unscaled products stay in fp32's range."""
+    import torch
+    n, d = 3000, 128
+    R = Round([n], [m], 1, d, 16, 64, seed=41)
+    # scores of 3 |k| along one direction that q shares: from 0 to 39 nats
+    q = np.zeros((m, 4, d), np.float32)
+    q[:, :, 0] = 4 * d ** 0.5
+    q = bf16(q)
+    k = np.zeros((n + m, 1, d), np.float32)
+    k[:, 0, 0] = np.linspace(0, 9.75, n + m)
+    v = R.rng.normal(0, 1, (n + m, 1, d)) * 2.0 ** 75
+    k, v = bf16(k), bf16(v)
+    binding.kv_append(R.cache, binding.AttnBatch(i32([0]), R.table, n + m),
+                      *(dev(x.reshape(n + m, -1), torch.bfloat16) for x in (k, v)))
+    got = run_attention(R, q, 4)
+    for i in (0, m - 1):
+        ref, mag = oa.attention(q[i:i + 1], k[:n + i + 1], v[:n + i + 1], n + i, [1], d ** -0.5)
+        # one product per score, of up to 39 nats: off by 2^-24 * 39 * log2(e) in the exponent, below the usual allowance
+        assert_attention(got[i:i + 1], ref, mag, f"row {i}")
