@@ -701,9 +701,10 @@ int dspk_accept_tree_greedy(const int32_t *target_ids, const int32_t *draft_ids,
  *   path, accept_len : of dspk_accept_tree_greedy (device memory);
  *   new_len    : int32 [b] output, cache_len plus the accepted nodes, or NULL;
  *                may be cache_len itself.
- * A request whose path is not one (accept_len < 1, a node out of order) or
- * whose cache_len plus max_rows runs past the page table is left as it is, and
- * its length too.
+ * A request whose path is not one (accept_len < 1, a node out of order), whose
+ * cache_len plus max_rows runs past the page table, or one of whose accepted
+ * nodes lies or would go on a page outside the pools is left as it is, in every
+ * cache, and its length too.
  */
 int dspk_kv_commit(int32_t count, const dspk_kv_cache *caches, const dspk_attn_batch *batch, const int32_t *path,
                    const int32_t *accept_len, int32_t *new_len, void *stream);

@@ -510,24 +510,37 @@ __global__ __launch_bounds__(TPB) void kv_read_kernel(const ReadArgs A, const in
     }
 }
 
-// A request's path is taken if it starts at the root, rises strictly and
-// stays below the nodes of a request; else nothing is moved and nothing kept.
-__device__ __forceinline__ int kept_nodes(const AttnBatch &B, int page_shift, const int32_t *path,
-                                          const int32_t *accept_len, int r) {
+// A request's path is taken, whole, if it starts at the root, rises strictly,
+// stays below the nodes of a request and meets none but the cache's pages; else
+// nothing is moved and nothing kept.  Every wave works it out by itself; `page`:
+// the source's and the destination's of node path[lane].
+__device__ __forceinline__ int kept_nodes(const KvCache &c, const AttnBatch &B, const int32_t *path,
+                                          const int32_t *accept_len, int r, int32_t (&at)[2], int64_t (&page)[2]) {
     const int n = accept_len[r], lane = threadIdx.x & 63;
-    bool bad = n < 1 || n > B.max_rows;
-    if (!bad && lane < n) {
-        const int32_t *p = path + (int64_t)r * B.max_rows;
-        bad = lane == 0 ? p[0] != 0 : p[lane] <= p[lane - 1] || p[lane] >= B.max_rows;
-    }
     const int32_t len = B.cache_len[r];
-    bad |= len < 0 || (int64_t)len + B.max_rows > ((int64_t)B.max_pages << page_shift);
+    bool bad = n < 1 || n > B.max_rows || len < 0 || (int64_t)len + B.max_rows > ((int64_t)B.max_pages << c.page_shift);
+    if (bad) return 0;                                              // the same for all lanes
+    if (lane < n) {
+        const int32_t *p = path + (int64_t)r * B.max_rows;
+        const int32_t node = p[lane];
+        bad = lane == 0 ? node != 0 : node <= p[lane - 1] || node >= B.max_rows;
+        at[0] = len + node;
+        at[1] = len + lane;
+    }
+    if (__any(bad)) return 0;
+    if (lane < n) {
+        page[0] = page_of(c, B, r, at[0]);
+        page[1] = page_of(c, B, r, at[1]);
+        bad = page[0] < 0 || page[1] < 0;
+    }
     return __any(bad) ? 0 : n;
 }
 
-__global__ __launch_bounds__(64) void new_len_kernel(const AttnBatch B, const int page_shift, const int32_t *path,
+__global__ __launch_bounds__(64) void new_len_kernel(const KvCache c, const AttnBatch B, const int32_t *path,
                                                      const int32_t *accept_len, int32_t *new_len) {
-    const int r = blockIdx.x, n = kept_nodes(B, page_shift, path, accept_len, r);
+    int32_t at[2];
+    int64_t page[2];
+    const int r = blockIdx.x, n = kept_nodes(c, B, path, accept_len, r, at, page);
     if (threadIdx.x == 0) new_len[r] = B.cache_len[r] + n;
 }
 
@@ -546,18 +559,17 @@ __global__ __launch_bounds__(TPB) void kv_commit_kernel(const CommitArgs A) {
     __shared__ int32_t s_t[2][kMaxTree];
     const int tid = threadIdx.x, head = blockIdx.x, r = blockIdx.y;
     const CachePtrs C = A.caches[blockIdx.z];
-    const int n = kept_nodes(A.B, A.c.page_shift, A.path, A.accept_len, r);
-    const int len = A.B.cache_len[r];
-    if (A.new_len != nullptr && head == 0 && blockIdx.z == 0 && tid == 0) A.new_len[r] = len + n;
+    int32_t at[2];
+    int64_t page[2];
+    const int n = kept_nodes(A.c, A.B, A.path, A.accept_len, r, at, page);
+    if (A.new_len != nullptr && head == 0 && blockIdx.z == 0 && tid == 0) A.new_len[r] = A.B.cache_len[r] + n;
     if (n <= 1) return;                                             // the root is in place
     if (tid < n) {
-        const int from = len + A.path[(int64_t)r * A.B.max_rows + tid], to = len + tid;
-        const int64_t a = from != to ? page_of(A.c, A.B, r, from) : -1, b = page_of(A.c, A.B, r, to);
-        const bool move = a >= 0 && b >= 0;
-        s_chunk[0][tid] = move ? a * A.c.heads + head : -1;
-        s_chunk[1][tid] = b * A.c.heads + head;
-        s_t[0][tid] = from & ((1 << A.c.page_shift) - 1);
-        s_t[1][tid] = to & ((1 << A.c.page_shift) - 1);
+        const bool move = at[0] != at[1];
+        s_chunk[0][tid] = move ? page[0] * A.c.heads + head : -1;
+        s_chunk[1][tid] = page[1] * A.c.heads + head;
+        s_t[0][tid] = at[0] & ((1 << A.c.page_shift) - 1);
+        s_t[1][tid] = at[1] & ((1 << A.c.page_shift) - 1);
         if (BITS == 8 && move) {
             s_s[0][tid] = C.ks[(s_chunk[0][tid] << A.c.page_shift) + s_t[0][tid]];
             s_s[1][tid] = C.vs[(s_chunk[0][tid] << A.c.page_shift) + s_t[0][tid]];
@@ -649,8 +661,7 @@ hipError_t launch_kv_commit(const CommitArgs &A, hipStream_t s) {
 }
 
 hipError_t launch_new_len(const CommitArgs &A, hipStream_t s) {
-    hipLaunchKernelGGL(new_len_kernel, dim3(A.B.b), dim3(64), 0, s, A.B, A.c.page_shift, A.path, A.accept_len,
-                       A.new_len);
+    hipLaunchKernelGGL(new_len_kernel, dim3(A.B.b), dim3(64), 0, s, A.c, A.B, A.path, A.accept_len, A.new_len);
     return hipGetLastError();
 }
 
