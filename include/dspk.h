@@ -602,7 +602,9 @@ typedef struct dspk_qk_prep {
  * 8-bit: see dspk_kv_append).  Rows of one call must not share a cache
  * position.  Errors: DSPK_EINVAL (pointers, alignment, sizes, leading
  * dimensions, eps, rotary_dim), DSPK_EUNSUPPORTED (cache format, rotary_dim not a
- * multiple of 16, more rows than one launch numbers), DSPK_EDEVICE.
+ * multiple of 16, more rows than one launch numbers: with B = b * min(max_rows,
+ * total_rows), ragged or not, B / 64 * kv_heads and the workgroups of q, at least
+ * B / 4, together below 2^24), DSPK_EDEVICE.
  */
 int dspk_qkv_norm_rope_append(const dspk_kv_cache *cache, const dspk_attn_batch *batch, const dspk_qk_prep *prep,
                               const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
@@ -664,7 +666,8 @@ int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch
  * node 0 is the anchor, node j >= 1 the draft draft_ids[j - 1] that follows
  * node parents[j - 1] < j.  A parent of -1 marks a node that is not there
  * (requests with fewer drafts), and so is what follows it.  Any other parent
- * is a data fault of its request.
+ * is a data fault of its request.  More than 2^26 - 1 requests are
+ * DSPK_EUNSUPPORTED.
  *
  * dspk_tree_layout:
  *   parents   : int32 [b][m_rows - 1];

@@ -8,9 +8,12 @@
 
 namespace dspk {
 
-constexpr int kBlockTokens = 64;    // positions per block of the cache: a page is 2^k blocks
+constexpr int kBlockShift = 6;      // log2 of the positions per block of the cache
+constexpr int kBlockTokens = 1 << kBlockShift;      // a page is 2^k blocks
 constexpr int kMaxTree = 64;        // rows of one request in an attention or tree call (one mask bit each)
 constexpr int kMaxCaches = 64;      // caches (layers) of one commit launch
+constexpr int64_t kLaunchThreads = UINT32_MAX;      // most threads of a launch's dimension
+constexpr int kManyQRows = 4;       // q rows of an append's workgroup, of many
 
 // The paged cache; see the layout at dspk_kv_cache.
 struct KvCache {
@@ -27,9 +30,23 @@ struct AttnBatch {
     const int32_t *row_start, *cache_len, *page_table;
 };
 
+// Shape of an append or read-back launch: workgroups of kRowThreads, one for each
+// block of 2^bs positions that a request of the call can touch and each k/v head,
+// then those of the q rows; see kv_cache.hip.
+constexpr int kRowThreads = 256;
+struct RowsPlan {
+    int32_t bs, nb;                 // log2 of a block's positions, blocks per request
+    int32_t kv_blocks;              // workgroups of the k/v rows
+    int32_t q_rows, q_blocks, slices;   // rows of a q workgroup, workgroups per request, slices of a row's heads
+    int32_t grid;
+    bool fits;                      // the launch's threads fit 32 bits
+};
+RowsPlan rows_plan(const AttnBatch &B, int32_t heads, int32_t d, int32_t q_heads, bool read);
+
 struct AppendArgs {
     KvCache c;
     AttnBatch B;
+    RowsPlan g;
     const void *q, *k, *v;          // rows [total_rows][ld]; q NULL: none
     int64_t ldq, ldk, ldv;
     int32_t q_heads;
@@ -47,6 +64,7 @@ hipError_t launch_append(const AppendArgs &a, hipStream_t s);
 struct ReadArgs {
     KvCache c;
     AttnBatch B;
+    RowsPlan g;
     void *k, *v;                    // rows [total_rows][ld]
     int64_t ldk, ldv;
     int32_t f32;

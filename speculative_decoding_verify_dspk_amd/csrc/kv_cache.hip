@@ -31,11 +31,8 @@ using kv::u32x4;
 using kv::f32x4;
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int TPB = 256;
+constexpr int TPB = kRowThreads;
 constexpr int kChunk = 16;          // k/v positions whose cosines are held at a time
-constexpr int kBlockShift = 6;      // log2 of a block's positions
-static_assert(1 << kBlockShift == kBlockTokens, "blocks");
-constexpr int kQRows = 4;           // q rows of a workgroup, of many
 
 // Eight lanes' worth of geometry: a head's row is held by D / 8 lanes, eight
 // neighbouring dimensions each.
@@ -273,8 +270,7 @@ __device__ __forceinline__ int64_t chunk_elems(const KvCache &c) {
 // Rows are taken in chunks whose cosines and sines are worked out first, each
 // once per workgroup; the chunk's elements are on their way meanwhile.
 template <int D, int BITS, bool F32>
-__global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const int kv_blocks, const int nb, const int bs,
-                                                     const int q_blocks, const int q_rows, const int slices) {
+__global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A) {
     constexpr int L = Geo<D>::L, R = Geo<D>::R, W = BITS == 16 ? 8 : 16;
     constexpr int CH = kChunk > R ? kChunk : R, NP = CH / R;        // k/v positions of a chunk, passes over them
     typedef typename std::conditional<BITS == 16, uint16_t, uint8_t>::type E;
@@ -282,9 +278,11 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
     __shared__ __attribute__((aligned(16))) float s_cs[2][CH * D / 2];
     __shared__ __attribute__((aligned(16))) E s_v[kBlockTokens * VS];
     const int tid = threadIdx.x, oct = tid % L, slot = tid / L, rot = A.inv_freq != nullptr ? A.rot : 0, h = rot / 2;
+    const int kv_blocks = A.g.kv_blocks, nb = A.g.nb, bs = A.g.bs;
 
     if ((int)blockIdx.x >= kv_blocks) {
         // ---- q heads of q_rows rows of a request, or a slice of them
+        const int q_rows = A.g.q_rows, q_blocks = A.g.q_blocks, slices = A.g.slices;
         const int at = blockIdx.x - kv_blocks, sl = at % slices, r = at / slices / q_blocks, i0 = at / slices % q_blocks * q_rows;
         const kv::Req q = kv::request(A.B, A.c.page_shift, r);
         const int n = min(q_rows, q.rows - i0);
@@ -446,13 +444,13 @@ __global__ __launch_bounds__(TPB) void append_kernel(const AppendArgs A, const i
 // Rows q.len .. of the requests, as an append with the same batch wrote them.
 // Rows whose length or page is a fault read back as NaN.
 template <int D, int BITS, bool F32>
-__global__ __launch_bounds__(TPB) void kv_read_kernel(const ReadArgs A, const int nb) {
+__global__ __launch_bounds__(TPB) void kv_read_kernel(const ReadArgs A) {
     constexpr int W = BITS == 16 ? 8 : 16;
     typedef typename std::conditional<BITS == 16, uint16_t, uint8_t>::type E;
     constexpr int VS = D + 16 / (int)sizeof(E);
     constexpr int N = kBlockTokens * D / W;         // pieces of a block
     __shared__ __attribute__((aligned(16))) E s_x[2][kBlockTokens * VS];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, nb = A.g.nb;
     const int head = blockIdx.x % A.c.heads, tb = blockIdx.x / A.c.heads % nb, r = blockIdx.x / A.c.heads / nb;
     kv::Req q = kv::request(A.B, A.c.page_shift, r);
     if (!q.ok) q.len = 0;                                           // only for numbering the rows
@@ -611,44 +609,24 @@ void with_format(const KvCache &c, F f) {
     else bits(integral_constant<int, 256>());
 }
 
-// Blocks of 2^bs positions that a request of n rows can touch.
-int touched_blocks(int32_t n, int bs = kBlockShift) { return ((n + (1 << bs) - 2) >> bs) + 1; }
-
 }  // namespace
 
 hipError_t launch_append(const AppendArgs &A, hipStream_t s) {
-    // Few blocks are halved, to double the workgroups at work: norm, rotation and
-    // store of one request of 128 / 512 rows of 32 + 8 + 8 heads 9.9 / 10.7 -> 6.6 /
-    // 7.2 us; more (960 of 64 positions, the prompts above) take 41.5 us whole and
-    // 44.6 halved.
-    int bs = kBlockShift, nb = touched_blocks(A.B.max_rows), kvb = A.B.b * nb * A.c.heads;
-    if (kvb <= 512) {
-        nb = touched_blocks(A.B.max_rows, --bs);
-        kvb = A.B.b * nb * A.c.heads;
-    }
-    // q: few rows go one to a workgroup, sliced further into passes, for latency;
-    // many in chunks (40 heads: 32 requests of 8 rows 7.2 us singly and 8.9 in
-    // chunks, 512 rows 11.1 and 10.8, 2048 rows 17.7 and 14.4)
-    const bool many = A.B.total_rows >= 1024;
-    const int q_rows = many ? kQRows : 1, q_blocks = (A.B.max_rows + q_rows - 1) / q_rows;
-    const int passes = (A.q_heads * A.c.d + TPB * 8 - 1) / (TPB * 8), slices = many ? 1 : passes;
-    const int grid = kvb + (A.q == nullptr ? 0 : A.B.b * q_blocks * slices);
     with_format(A.c, [&](auto d, auto bits) {
         if (A.f32)
-            hipLaunchKernelGGL((append_kernel<d(), bits(), true>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, bs, q_blocks, q_rows, slices);
+            hipLaunchKernelGGL((append_kernel<d(), bits(), true>), dim3(A.g.grid), dim3(TPB), 0, s, A);
         else
-            hipLaunchKernelGGL((append_kernel<d(), bits(), false>), dim3(grid), dim3(TPB), 0, s, A, kvb, nb, bs, q_blocks, q_rows, slices);
+            hipLaunchKernelGGL((append_kernel<d(), bits(), false>), dim3(A.g.grid), dim3(TPB), 0, s, A);
     });
     return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const ReadArgs &A, hipStream_t s) {
-    const int nb = touched_blocks(A.B.max_rows), grid = A.B.b * nb * A.c.heads;
     with_format(A.c, [&](auto d, auto bits) {
         if (A.f32)
-            hipLaunchKernelGGL((kv_read_kernel<d(), bits(), true>), dim3(grid), dim3(TPB), 0, s, A, nb);
+            hipLaunchKernelGGL((kv_read_kernel<d(), bits(), true>), dim3(A.g.grid), dim3(TPB), 0, s, A);
         else
-            hipLaunchKernelGGL((kv_read_kernel<d(), bits(), false>), dim3(grid), dim3(TPB), 0, s, A, nb);
+            hipLaunchKernelGGL((kv_read_kernel<d(), bits(), false>), dim3(A.g.grid), dim3(TPB), 0, s, A);
     });
     return hipGetLastError();
 }
