@@ -266,6 +266,9 @@ class KVCache:
                               ("v_scales", v_scales, 4 * pages * kv_heads * page_tokens)):
             if t is not None and (not t.is_contiguous() or t.numel() * t.element_size() < size):
                 raise ValueError(f"{name}: expected a contiguous tensor of at least {size} bytes")
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is not None and (t.element_size() != 4 or not t.is_floating_point()):
+                raise ValueError(f"{name}: expected float32, got {t.dtype}")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.pages, self.kv_heads, self.head_dim = pages, kv_heads, head_dim
         self.page_tokens, self.bits = page_tokens, bits
@@ -291,6 +294,12 @@ def _int32(t, name: str, need: int = 0):
     return t
 
 
+def _bits64(t, name: str, need: int) -> None:
+    import torch
+    if t is not None and (t.dtype not in (torch.int64, torch.uint64) or not t.is_contiguous() or t.numel() < need):
+        raise ValueError(f"{name}: expected a contiguous tensor of at least {need} 64-bit integers")
+
+
 class AttnBatch:
     """The requests of an attention or cache call: cached lengths [b], page
     table [b][max_pages], and each request's rows (max_rows each, or by
@@ -313,7 +322,11 @@ class AttnBatch:
 
 
 def _row_array(t, name: str, rows: int):
-    """(address, leading dimension, element type) of rows [>= rows][ld]."""
+    """(address, leading dimension, element type) of rows [>= rows][ld]: float32,
+    or bf16 (bfloat16 or 16-bit integer patterns)."""
+    import torch
+    if t.dtype not in (torch.float32, torch.bfloat16, torch.int16, torch.uint16):
+        raise ValueError(f"{name}: expected float32 or bf16 rows, got {t.dtype}")
     ld = _rows(t, name)
     if t.shape[0] < rows:
         raise ValueError(f"{name}: {t.shape[0]} rows, {rows} needed")
@@ -502,9 +515,7 @@ def prepare_tree_attention(cache: KVCache, batch: AttnBatch, q, q_heads: int, ou
         raise ValueError("q and out: expected bf16 (2-byte elements)")
     for t, name in ((q, "q"), (out, "out")):
         _columns(t, name, q_heads * cache.head_dim)
-    if tree_mask is not None and (tree_mask.element_size() != 8 or not tree_mask.is_contiguous()
-                                  or tree_mask.numel() < batch.total_rows):
-        raise ValueError(f"tree_mask: expected a contiguous 64-bit tensor of at least {batch.total_rows} entries")
+    _bits64(tree_mask, "tree_mask", batch.total_rows)
     return Prepared("dspk_tree_attention", ctypes.byref(cache.desc), ctypes.byref(batch.desc), qp, ldq, q_heads,
                     cache.head_dim ** -0.5 if scale is None else float(scale), _ptr(tree_mask), op, ldo,
                     workspace.data_ptr(), workspace.numel(),
@@ -512,8 +523,7 @@ def prepare_tree_attention(cache: KVCache, batch: AttnBatch, q, q_heads: int, ou
 
 
 def prepare_tree_layout(parents, b: int, m_rows: int, cache_len, tree_mask, positions, stream=None) -> Prepared:
-    if tree_mask.element_size() != 8 or not tree_mask.is_contiguous() or tree_mask.numel() < b * m_rows:
-        raise ValueError(f"tree_mask: expected a contiguous 64-bit tensor of at least {b * m_rows} entries")
+    _bits64(tree_mask, "tree_mask", b * m_rows)
     return Prepared("dspk_tree_layout", _ptr(_int32(parents, "parents", b * (m_rows - 1))), b, m_rows,
                     _int32(cache_len, "cache_len", b).data_ptr(), tree_mask.data_ptr(),
                     _int32(positions, "positions", b * m_rows).data_ptr(),
