@@ -652,8 +652,11 @@ size_t dspk_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head
  *               not overlap q;
  *   workspace : >= dspk_attn_workspace_bytes(...) bytes, 256-byte aligned.
  * A row that sees nothing comes out as zeros.  What a masked position holds
- * does not reach a row, NaN and infinities included.  Scores, statistics and
- * sums are fp32; the result is deterministic.  Errors: DSPK_EINVAL,
+ * does not reach a row, NaN and infinities included.  An infinity of v that a row
+ * sees comes out as that infinity (with the opposite one, or where fp32 has no
+ * probability small enough for it, as NaN).  Scores, statistics and sums are
+ * fp32; a sum may stand at up to 2^32 times its value, so that results are finite
+ * for v up to 2^78 in magnitude.  The result is deterministic.  Errors: DSPK_EINVAL,
  * DSPK_EUNSUPPORTED (cache format, more than DSPK_MAX_TREE rows per request, a
  * page table too large for one launch), DSPK_EDEVICE.
  */

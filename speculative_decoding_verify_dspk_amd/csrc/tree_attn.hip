@@ -286,6 +286,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
     constexpr int BR = RT * 16;
     constexpr bool AHEAD = D * BITS < 256 * 16;     // else k and v of a step do not fit the registers together
     __shared__ float2 s_ml[WAVES][RT][16];
+    __shared__ uint32_t s_odd[WAVES];
     __shared__ f32x4 s_o[WAVES][RT * VB * 64];
 
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -478,7 +479,7 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                     if constexpr (BITS == 16) {
                         // v past the last position is 0.  A row's masked positions must
                         // not reach it as 0 * NaN: v that is not finite leaves the
-                        // product and is added afterwards to the rows that see it.
+                        // product and is added when the waves' results are joined.
                         bool odd = false;
                         const int left = q.rows - n0 - g * 4;
 #pragma unroll
@@ -595,31 +596,6 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
             }
         } while (over);
 
-        if (BITS == 16 && __builtin_expect(odd_v, 0)) {
-            // the wave's steps among the request's own rows
-            for (int t = t_first; t < t_end; t += kUnit) {
-                if (t + kStep <= q.len) continue;
-                const int64_t page = table[t >> A.c.page_shift];
-                if (page < 0 || page >= A.c.pages) continue;        // its scores are NaN already
-                const uint16_t *vp = (const uint16_t *)A.c.v + (((page * A.c.heads + head) * D) << A.c.page_shift);
-                const int last = min(kStep, tokens - t);
-                for (int tt = 0; tt < last; ++tt) {
-                    const int node = t + tt - q.len;
-#pragma unroll
-                    for (int vb = 0; vb < VB; ++vb)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float x = kv::bf16_f32(vp[kv::v_elem<D, W>((t & page_mask) + tt, vb * 16 + g * 4 + i)]);
-                            if (!(fabsf(x) < __builtin_inff())) {
-#pragma unroll
-                                for (int rt = 0; rt < RT; ++rt)
-                                    if (node < 0 || (see[rt] >> (node & 63) & 1)) o[rt][vb][i] += x;
-                            }
-                        }
-                }
-            }
-        }
-
         // ---- The waves' results become one: through LDS each takes every eighth
         // output tile, of all waves.
 #pragma unroll
@@ -629,14 +605,55 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
 #pragma unroll
             for (int vb = 0; vb < VB; ++vb) s_o[w][(rt * VB + vb) * 64 + lane] = o[rt][vb];
         }
+        if (BITS == 16 && lane == 0) s_odd[w] = odd_v;
         __syncthreads();
         const bool whole = n == un.per_seg;
+        bool odd_own = false;                                       // some of the call's own v, of any wave
+        if constexpr (BITS == 16) {
+#pragma unroll
+            for (int k = 0; k < WAVES; ++k) odd_own |= s_odd[k] != 0;
+        }
         const auto finish = [&](f32x4 z, float sum, int tile) {
             const int rr = row_base + tile / VB * 16 + col, node = (int)((rr + 0.5f) * per_rep);
             // a row that sees nothing is 0; one whose length is a fault is NaN
             const float inv = !q.ok ? __uint_as_float(0x7fc00000u) : sum == 0.f ? 0.f : 1.f / sum;
             uint16_t *dst = A.out + (int64_t)(q.row0 + node) * A.ldo + (head * A.rep + rr - node * A.rep) * D;
             if (rr < rows) store_out(dst + tile % VB * 16 + g * 4, z * inv);
+        };
+        // v that are not finite and that a row sees are added alone, without
+        // weights: in the product they would be lost where the low half of a
+        // probability, or all of it, is 0, and reach rows that do not see them.
+        [[maybe_unused]] const auto not_finite = [&](f32x4 &z, float sum, int tile) {
+            const int rr = min(row_base + tile / VB * 16 + col, rows - 1), node = (int)((rr + 0.5f) * per_rep);
+            const uint64_t sees = (A.mask != nullptr ? A.mask[q.row0 + node] : (2ull << node) - 1) & ((2ull << (q.rows - 1)) - 1);
+            const auto odd = [](float x) { return fabsf(x) < __builtin_inff() ? 0.f : x; };
+            float all = 0.f;                                        // cached: dimension `col`, a fourth of the positions
+            f32x4 own = {0.f, 0.f, 0.f, 0.f};                       // among the rows: as z, what the lane's row sees
+            const int end = min((v0 + n) * kUnit, tokens);
+#pragma unroll 1
+            for (int t = v0 * kUnit; t < end; t += kStep) {
+                const int64_t page = table[t >> A.c.page_shift];
+                if (page < 0 || page >= A.c.pages) continue;        // rows that see it are NaN
+                const uint16_t *vp = (const uint16_t *)A.c.v + (((page * A.c.heads + head) * D) << A.c.page_shift);
+                const u32x4 x = *(const u32x4 *)(vp + (t & page_mask) * D + (tile % VB * 64 + lane) * W);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int at = t + e / 4 * 16 + g * 4 + e % 4;
+                    if (at < q.len) all += odd(kv::bf16_f32(x[e / 2] >> (e % 2 * 16) & 0xffffu));
+                }
+#pragma unroll 1
+                for (int at = max(t, q.len); at < min(t + kStep, end); ++at)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (sees >> (at - q.len) & 1)
+                            own[i] += odd(kv::bf16_f32(vp[kv::v_elem<D, W>(at & page_mask, tile % VB * 16 + g * 4 + i)]));
+            }
+            all = row_sum(all);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = __shfl(all, g * 4 + i) + own[i];
+                if (sum == sum && x != 0.f) z[i] = x;
+            }
         };
 #pragma unroll 1
         for (int tile = w; tile < RT * VB; tile += WAVES) {
@@ -654,6 +671,10 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
                 const float f = __builtin_amdgcn_exp2f(ml[k].x - mc);
                 sum += ml[k].y * f;
                 z += s_o[k][tile * 64 + lane] * f;
+            }
+            if constexpr (BITS == 16) {
+                const float x = (z[0] + z[1]) + (z[2] + z[3]);
+                if (__builtin_expect(__any((odd_own || !(x == x)) && sum == sum), 0)) not_finite(z, sum, tile);
             }
             if (whole) {
                 finish(z, sum, tile);

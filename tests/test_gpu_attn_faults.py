@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from attnutil import Round, i32, pools_host
+from attnutil import Round, bf16, dev, i32, pools_host, run_attention
 from speculative_decoding_verify_dspk_amd import binding
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +43,34 @@ def test_commit_keeps_requests_whose_path_meets_a_bad_page(bits, in_place):
                     # both rounds have shuffled pages of their own; the call's are A's
                     want[A.table_np[r, b // 64], b % 64] = x[A.table_np[r, a // 64], a % 64]
             assert np.array_equal(got, want, equal_nan=True)
+
+
+@pytest.mark.parametrize("n,m,hq,hkv,d", [(100, 1, 4, 1, 128), (3000, 17, 8, 1, 128), (700, 6, 8, 2, 64), (500, 3, 2, 1, 256),
+                                          (9000, 40, 16, 2, 128)])
+@pytest.mark.parametrize("even", [True, False])
+def test_cached_v_that_is_not_finite(n, m, hq, hkv, d, even):
+    """Infinities and NaN of cached v, with probabilities of any number of bits
+    (even: all the same, a power of two): an infinity comes out as one, opposite
+    ones and NaN as NaN, and other dimensions keep their bits."""
+    import torch
+    R = Round([n], [m], hkv, d, 16, 64, seed=n + m)
+    q = bf16(R.rng.normal(0, 0 if even else 1, (m, hq, d)))
+    clean, odd = R.v[0].copy(), R.v[0].copy()
+    inf = np.float32("inf")
+    # (position, dimension, value); the last two positions are among the call's rows
+    spots = [(3, 5, inf), (n - 1, 9, -inf), (n // 2, 17, inf), (n // 2 + 1, 17, -inf), (40, 33, np.nan), (7, 40, inf),
+             (n, 40, -inf), (n + m - 1, 41, inf)]
+    for t, i, x in spots:
+        clean[t, 0, i], odd[t, 0, i] = 0, x
+    out = []
+    every = binding.AttnBatch(i32([0]), R.table, n + m)
+    for v in (clean, odd):
+        binding.kv_append(R.cache, every, *(dev(x.reshape(n + m, -1), torch.bfloat16) for x in (R.k[0], v)))
+        out.append(run_attention(R, q, hq))
+    want = out[0].copy()
+    rep = hq // hkv                                       # the first k/v head alone holds them
+    want[:, :rep, 5], want[:, :rep, 9] = inf, -inf
+    want[:, :rep, [17, 33]] = np.nan
+    want[:, :rep, 40] = np.nan                            # every row sees row 0 of the call
+    want[m - 1, :rep, 41] = inf
+    assert np.array_equal(out[1], want, equal_nan=True)
