@@ -100,8 +100,9 @@ class VerifyStack:
                      eps: float = 1e-6) -> None:
         """Gives every layer a k/v cache of one request holding ``context``
         synthetic entries, with room for max_m rows and ``room`` more positions
-        after them; from then on the layers attend over it."""
+        after them; from then on the layers attend over it, the rows a chain."""
         import torch
+        self.tree_mask = self.positions = None
         D = HEAD_DIM
         self.q_heads, self.kv_heads, self.eps = self.qdim // D, self.kvdim // D, eps
         pages = -(-(context + self.max_m + room) // page_tokens)
@@ -125,19 +126,34 @@ class VerifyStack:
         self.q_rot = torch.empty((self.max_m, self.qdim), **bf)
         self.attn_out = torch.empty((self.max_m, self.qdim), **bf)
         self.mask_buf = torch.empty((1, self.max_m), dtype=torch.int64, device="cuda")
-        self.position_buf = torch.empty((1, self.max_m), dtype=torch.int32, device="cuda")
+        i32 = lambda n: torch.zeros((1, n), dtype=torch.int32, device="cuda")
+        self.position_buf, self.parent_buf = i32(self.max_m), i32(self.max_m)
         self.ws_attn = binding.alloc_workspace(
             binding.attn_workspace_bytes(self.q_heads, self.kv_heads, D, 1, self.max_m))
 
     def set_tree(self, parents, m: int, stream=None) -> None:
         """The next rounds' rows are the nodes of a tree (parents: int32 [m - 1]
-        on the device, see dspk_tree_layout); None: a chain again."""
+        on the device, see dspk_tree_layout); None: a chain again.  The parents
+        are copied, into the same memory each time, so that captured rounds of m
+        rows follow."""
+        import torch
         if parents is None:
             self.tree_mask = self.positions = None
             return
-        # the same memory each round, so that captured rounds follow
+        if not self.caches:
+            raise ValueError("set_tree: a tree's rows attend over a cache (attach_cache)")
+        if m < 1 or m > self.max_m:
+            raise ValueError(f"set_tree: a tree of {m} nodes in a stack of {self.max_m} rows")
+        binding._int32(parents, "parents", m - 1)
+        with torch.cuda.stream(stream):
+            self.parent_buf[:, :m - 1].copy_(parents.reshape(1, -1)[:, :m - 1])
         self.tree_mask, self.positions = self.mask_buf[:, :m], self.position_buf[:, :m]
-        binding.tree_layout(parents, 1, m, self.cache_len, self.tree_mask, self.positions, stream)
+        self._lay_out(stream)
+
+    def _lay_out(self, stream=None) -> None:
+        """Masks and positions of the tree at the cached length."""
+        m = self.positions.shape[1]
+        binding.tree_layout(self.parent_buf, 1, m, self.cache_len, self.tree_mask, self.positions, stream)
 
     def attention_calls(self, li: int, m: int, stream=None) -> list:
         """Layer li's calls between q/k/v and o, their arguments marshalled."""
@@ -153,10 +169,13 @@ class VerifyStack:
 
     def launch_commit(self, path, accept_len, m: int, stream=None) -> None:
         """After the acceptance of a tree of m nodes: the path's entries of every
-        layer move together and the cached length grows by the accepted nodes.
+        layer move together, the cached length grows by the accepted nodes, and
+        the tree's positions follow it.
         (A chain's entries are in place: its cached length grows by accept_len.)"""
         binding.kv_commit(self.caches, binding.AttnBatch(self.cache_len, self.page_table, m), path, accept_len,
                           self.cache_len, stream)
+        if self.tree_mask is not None:
+            self._lay_out(stream)
 
     # ------------------------------------------------------------------ sizes
     def layer_weight_bytes(self) -> int:
