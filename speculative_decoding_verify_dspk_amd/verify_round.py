@@ -127,7 +127,7 @@ class VerifyStack:
         self.attn_out = torch.empty((self.max_m, self.qdim), **bf)
         self.mask_buf = torch.empty((1, self.max_m), dtype=torch.int64, device="cuda")
         i32 = lambda n: torch.zeros((1, n), dtype=torch.int32, device="cuda")
-        self.position_buf, self.parent_buf = i32(self.max_m), i32(self.max_m)
+        self.position_buf, self.parent_buf, self.path = i32(self.max_m), i32(self.max_m), i32(self.max_m)
         self.ws_attn = binding.alloc_workspace(
             binding.attn_workspace_bytes(self.q_heads, self.kv_heads, D, 1, self.max_m))
 
@@ -241,7 +241,16 @@ class VerifyStack:
             graphs.append(g)
         return graphs
 
+    def launch_accept(self, m: int, draft_ids, accept_len, committed, stream=None) -> None:
+        """Greedy acceptance of one request of m rows: along the tree that is set
+        (the accepted nodes go to ``path``), or of a chain."""
+        if self.tree_mask is None:
+            binding.accept_greedy(self.argmax, draft_ids, 1, m, accept_len, committed, stream)
+        else:
+            binding.accept_tree_greedy(self.argmax, draft_ids, self.parent_buf, 1, m, accept_len, committed, self.path,
+                                       stream)
+
     def capture_round(self, m: int, copy: int, draft_ids, accept_len, committed):
-        """HIP graphs (layers, head, accept) of one greedy round at width m."""
-        return self.capture_calls(m, copy, lambda: binding.accept_greedy(self.argmax, draft_ids, 1, m, accept_len,
-                                                                          committed))
+        """HIP graphs (layers, head, accept) of one greedy round at width m, of a
+        tree if one is set at the time."""
+        return self.capture_calls(m, copy, lambda: self.launch_accept(m, draft_ids, accept_len, committed))

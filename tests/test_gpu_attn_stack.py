@@ -1,4 +1,5 @@
-"""Stacks whose rounds are trees: rounds that follow one another without a new tree."""
+"""Stacks whose rounds are trees: acceptance of captured rounds, and rounds that
+follow one another without a new tree."""
 import pytest
 
 from attnutil import i32
@@ -12,6 +13,40 @@ def _stack(context, m, room=0):
     st = VerifyStack("qwen3-4b", 1, 8, m, seed="attn-tree")
     st.attach_cache(context, room=room)
     return st
+
+
+def _drafts(target, par, follow):
+    """Drafts that are the target's token after their parent for the nodes of `follow` alone."""
+    return [target[p] if j in follow else target[p] + 1 for j, p in enumerate(par, 1)]
+
+
+def test_captured_tree_rounds_accept_along_the_tree():
+    """A captured round of a tree accepts along that tree, and along the next
+    one that set_tree brings, whatever becomes of the tensors it was given."""
+    import torch
+    m = 7
+    st = _stack(100, m)
+    new = lambda *z: torch.zeros(z, dtype=torch.int32, device="cuda")
+    draft, al, com = new(1, m - 1), new(1), new(1, m)
+    trees = [([0, 0, 1, 2, 2, 5], {2, 5, 6}), ([0, 1, 1, 0, 4, 5], {1, 3}), ([0, 0, 0, 0, 0, 0], {4})]
+    st.set_tree(i32(trees[0][0]), m)
+    graphs = st.capture_round(m, 0, draft, al, com)
+    for par, follow in trees:
+        given = i32(par)
+        st.set_tree(given, m)
+        given.fill_(-9)
+        for g in graphs[:2]:
+            g.replay()
+        torch.cuda.synchronize()
+        t = st.argmax[:m].tolist()
+        d = _drafts(t, par, follow)
+        draft.copy_(i32([d]))
+        graphs[2].replay()
+        torch.cuda.synchronize()
+        n, toks, path = oa.accept_tree_greedy(t, d, par)
+        assert len(path) == len(follow) + 1
+        assert al.tolist() == [n] and com[0].tolist() == toks + [-1] * (m - n)
+        assert st.path[0, :m].tolist() == path + [-1] * (m - n)
 
 
 def test_rounds_of_one_tree_follow_the_cached_length():
