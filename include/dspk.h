@@ -706,7 +706,8 @@ int dspk_accept_tree_greedy(const int32_t *target_ids, const int32_t *draft_ids,
  *   batch      : the round's, without row_start; max_rows = m_rows;
  *   path, accept_len : of dspk_accept_tree_greedy (device memory);
  *   new_len    : int32 [b] output, cache_len plus the accepted nodes, or NULL;
- *                may be cache_len itself.
+ *                may be cache_len itself, but no other array of the call.
+ * No two of the caches may share memory.
  * A request whose path is not one (accept_len < 1, a node out of order), whose
  * cache_len plus max_rows runs past the page table, or one of whose accepted
  * nodes lies or would go on a page outside the pools is left as it is, in every

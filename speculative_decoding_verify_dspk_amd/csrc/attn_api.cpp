@@ -409,14 +409,21 @@ int dspk_kv_commit(int32_t count, const dspk_kv_cache *caches, const dspk_attn_b
                     DSPK_MAX_TREE);
     if (!pointer(path, 4) || !pointer(accept_len, 4) || !aligned(new_len, 4))
         return fail(DSPK_EINVAL, "%s: path or accept_len NULL, or an array misaligned", who);
-    if (new_len != nullptr && new_len != A.B.cache_len && new_len < A.B.cache_len + A.B.b &&
-        A.B.cache_len < new_len + A.B.b)
+    // workgroups read these after others have written new_len
+    const auto over = [&](const int32_t *p, int64_t n) {
+        const uintptr_t a = (uintptr_t)new_len, e = (uintptr_t)p;
+        return new_len != nullptr && a < e + n * sizeof(int32_t) && e < a + A.B.b * sizeof(int32_t);
+    };
+    const bool in_place = new_len == A.B.cache_len;
+    if (!in_place && over(A.B.cache_len, A.B.b))
         return fail(DSPK_EINVAL, "%s: new_len overlaps cache_len without being it", who);
+    if (over(accept_len, A.B.b) || over(path, (int64_t)A.B.b * A.B.max_rows) ||
+        (!in_place && over(A.B.page_table, (int64_t)A.B.b * A.B.max_pages)))
+        return fail(DSPK_EINVAL, "%s: new_len overlaps accept_len, path or the page table", who);
     A.path = path;
     A.accept_len = accept_len;
     // a new_len that is cache_len is written by a launch of its own, after
     // every workgroup has read the old lengths
-    const bool in_place = new_len == A.B.cache_len;
     for (int32_t i = 0; i < count; i += dspk::kMaxCaches) {
         A.count = count - i < dspk::kMaxCaches ? count - i : dspk::kMaxCaches;
         for (int32_t j = 0; j < A.count; ++j)
