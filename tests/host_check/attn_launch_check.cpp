@@ -120,6 +120,31 @@ int main() {
     // rows that the arrays do not hold are not counted
     B.total_rows = 5000;
     CHECK(calls(c, B, 1, rc) == 3);
+    // Attention: a call that is accepted, and calls that differ from it in one thing
+    const dspk_kv_cache kv = {8, 128, 64, 16, 100, P, P, nullptr, nullptr};
+    const dspk_attn_batch two = {2, 4, 8, 9, nullptr, I, I};
+    const size_t need = dspk_attn_workspace_bytes(32, 8, 128, 2, 4);
+    const auto attend = [&](int64_t ldq, int32_t hq, float scale, char *mask, char *out, int64_t ldo, char *ws, size_t bytes) {
+        return dspk_tree_attention(&kv, &two, (uint16_t *)P, ldq, hq, scale, (uint64_t *)mask, (uint16_t *)out, ldo, ws, bytes,
+                                   nullptr);
+    };
+    char *const out = P + (1 << 20), *const ws = P + (1 << 24);
+    int before = g_launches;
+    CHECK(attend(4096, 32, 0.1f, nullptr, out, 4096, ws, need) == DSPK_OK && g_launches == before + 1);
+    CHECK(attend(4096, 32, 0.1f, P + 8, out, 4096, ws, need) == DSPK_OK && g_launches == before + 2);
+    before = g_launches;
+    const auto refused = [&](int rc, const char *text) {
+        CHECK(rc == DSPK_EINVAL && g_launches == before && g_msg.find(text) != std::string::npos);
+    };
+    refused(attend(4090, 32, 0.1f, nullptr, out, 4096, ws, need), "of q");
+    refused(attend(4096, 12, 0.1f, nullptr, out, 4096, ws, need), "q_heads=12");
+    refused(attend(4096, 32, 0.f, nullptr, out, 4096, ws, need), "scale");
+    refused(attend(4096, 32, 0.1f, P + 4, out, 4096, ws, need), "tree_mask");
+    refused(attend(4096, 32, 0.1f, nullptr, P, 4096, ws, need), "out must not be q");
+    refused(attend(4096, 32, 0.1f, nullptr, out, 4088, ws, need), "of out");
+    refused(attend(4096, 32, 0.1f, nullptr, out, 4096, nullptr, need), "workspace");
+    refused(attend(4096, 32, 0.1f, nullptr, out, 4096, ws + 128, need), "workspace");
+    refused(attend(4096, 32, 0.1f, nullptr, out, 4096, ws, need - 1), "workspace");
     // requests of a tree call
     int32_t *const X = (int32_t *)(P + (1 << 20));
     CHECK(dspk_tree_layout(I, (1 << 26) - 1, 4, X, (uint64_t *)P, X, nullptr) == DSPK_OK);
