@@ -1,8 +1,10 @@
-"""Attention-side calls on data that holds faults or values that are not finite."""
+"""Attention-side calls on data that holds faults or values that are not finite,
+and under page tables wider than the lengths."""
 import numpy as np
 import pytest
 
-from attnutil import Round, bf16, dev, i32, pools_host, run_attention
+from attnutil import Round, assert_attention, bf16, chain_masks, dev, i32, pools_host, run_attention
+from oracle import attention as oa
 from speculative_decoding_verify_dspk_amd import binding
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +76,44 @@ def test_cached_v_that_is_not_finite(n, m, hq, hkv, d, even):
     want[:, :rep, 40] = np.nan                            # every row sees row 0 of the call
     want[m - 1, :rep, 41] = inf
     assert np.array_equal(out[1], want, equal_nan=True)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("lens,rows,hq,hkv,d", [([1021], [1], 32, 8, 128), ([1000], [16], 32, 8, 128),
+                                                ([400, 30, 0], [6, 2, 1], 8, 2, 64), ([700], [3], 8, 1, 256)])
+def test_page_tables_wider_than_the_lengths(lens, rows, hq, hkv, d, bits):
+    """A table with room for 1, 8 and 128 times the positions (the plan goes by
+    its width); its unused entries are no pages."""
+    R = Round(lens, rows, hkv, d, bits, 64, seed=61, max_rows=max(rows))
+    q = bf16(R.rng.normal(0, 1, (R.total, hq, d)))
+    tight = R.table_np
+    for wide in (1, 8, 128):
+        table = np.full((len(lens), tight.shape[1] * wide), -1, np.int32)
+        table[:, :tight.shape[1]] = tight
+        R.batch = binding.AttnBatch(R.len_dev, dev(table), R.max_rows, R.total, R.start_dev)
+        got = run_attention(R, q, hq)
+        for r, (n, m) in enumerate(zip(lens, rows)):
+            a, e = R.starts[r], R.starts[r + 1]
+            ref, mag = oa.attention(q[a:e], R.k[r], R.v[r], n, chain_masks(m), d ** -0.5)
+            assert_attention(got[a:e], ref, mag, f"{wide}x, request {r}")
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_a_prompt_in_calls_of_64_rows(bits):
+    """A prompt's rows attend in calls of up to 64, cache_len advanced by each,
+    over entries that one append has stored."""
+    import torch
+    n, m, hq, hkv, d = 37, 150, 8, 2, 64
+    R = Round([n], [m], hkv, d, bits, 64, seed=62)
+    q = bf16(R.rng.normal(0, 1, (m, hq, d)))
+    qd = dev(q.reshape(m, -1), torch.bfloat16)
+    out = torch.zeros_like(qd)
+    ws = binding.alloc_workspace(binding.attn_workspace_bytes(hq, hkv, d, 1, 64))
+    for a in range(0, m, 64):
+        e = min(a + 64, m)
+        binding.tree_attention(R.cache, binding.AttnBatch(i32([n + a]), R.table, e - a), qd[a:e], hq, out[a:e], ws)
+    got = out.float().cpu().numpy().reshape(m, hq, d)
+    for a in range(0, m, 64):
+        e = min(a + 64, m)
+        ref, mag = oa.attention(q[a:e], R.k[0][:n + e], R.v[0][:n + e], n + a, chain_masks(e - a), d ** -0.5)
+        assert_attention(got[a:e], ref, mag, f"rows {a}..")
