@@ -613,7 +613,8 @@ int dspk_qkv_norm_rope_append(const dspk_kv_cache *cache, const dspk_attn_batch 
 /*
  * k and v rows stored as they are ("mlx-dspark 0.7.0", quick start: an 8-bit
  * k/v cache for long contexts).  8-bit caches quantise each head's row by
- * itself: scale = max|x| / 127, code = x * 127 / max|x| rounded half to even.
+ * itself: scale = max|x| / 127, code = x * (127 / max|x|) rounded half to even,
+ * each step in fp32.
  * A row holding a value that is not finite reads back as NaN; one whose
  * largest magnitude is below 4e-37 reads back as zeros.
  */
@@ -636,7 +637,8 @@ size_t dspk_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head
 
 /*
  * Attention of a round's rows over the cache, which already holds their own k
- * and v (an append with the same batch):
+ * and v (an append with the same batch; a prompt's rows attend in calls of up to
+ * DSPK_MAX_TREE, with cache_len advanced from call to call):
  *   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale * q_i . k_j - max),
  * over the positions j row i sees: all cache_len cached ones, and of the
  * request's rows those whose bit is set in the row's mask.  q head h uses k/v
@@ -658,7 +660,9 @@ size_t dspk_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head
  * fp32; a sum may stand at up to 2^32 times its value, so that results are finite
  * for v up to 2^78 in magnitude.  The result is deterministic.  Errors: DSPK_EINVAL,
  * DSPK_EUNSUPPORTED (cache format, more than DSPK_MAX_TREE rows per request, a
- * page table too large for one launch), DSPK_EDEVICE.
+ * page table, or heads times rows, too large for one launch), DSPK_EDEVICE.
+ * The launch is planned for lengths that fill the page table: short contexts are
+ * fastest under a table not much wider than they are.
  */
 int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch, const uint16_t *q, int64_t ldq,
                         int32_t q_heads, float scale, const uint64_t *tree_mask, uint16_t *out, int64_t ldo,

@@ -33,11 +33,15 @@ AttnPlan attn_plan(int32_t q_heads, int32_t kv_heads, int32_t d, int32_t b, int3
     p.blocks = (int32_t)((tiles + p.tiles - 1) / p.tiles);
     const int32_t most = cus > p.blocks ? cus / p.blocks : 1;         // one workgroup per CU
     p.groups = (int32_t)(units < most ? units : most);
-    p.pairs = per_seg == 2;
+    p.pairs = per_seg == 2;                                           // tables of 257 .. 512 positions
     // The last group of a segment adds the pieces of all by itself, at the rate
     // of one CU; where they are many, a launch of its own is faster (one request
     // of 8 rows, two tiles, 4 / 8 / 32 pieces: 11.5 / 15 / 26 us in one launch, 12.7
-    // / 12.7 / 13.5 us in two).
+    // / 12.7 / 13.5 us in two; one tile was not measured).  `pieces` is what lengths
+    // that fill the page table would leave, or one more where ranges do not start with
+    // a segment: shorter contexts pay for the launch without needing it (a tree of 16
+    // over 1000 positions of a bf16 cache 9.0 us under a table of that size, 11.4
+    // under 8 times it, 14.0 under 128 times it, with two tiles then).
     const int64_t pieces = segs >= p.groups ? 2 : per_seg < p.groups / segs ? per_seg : p.groups / segs + 1;
     p.join = pieces * p.tiles * 16 * d * (int64_t)sizeof(float) > kAttnJoinBytes;
     // The workspace is that of the most tiles, which no other choice exceeds: two
@@ -343,7 +347,7 @@ int dspk_tree_attention(const dspk_kv_cache *cache, const dspk_attn_batch *batch
     if (!aligned(tree_mask, 8)) return fail(DSPK_EINVAL, "%s: tree_mask misaligned", who);
     const dspk::AttnPlan p = dspk::attn_plan(q_heads, A.c.heads, A.c.d, A.B.b, A.B.max_rows,
                                              (int64_t)A.B.max_pages << A.c.page_shift, dspk::device_cus());
-    if (!p.fits || (int64_t)A.c.heads * p.blocks > 65535) return fail(DSPK_EUNSUPPORTED, "%s: page table too large for one launch", who);
+    if (!p.fits || (int64_t)A.c.heads * p.blocks > 65535) return fail(DSPK_EUNSUPPORTED, "%s: page table, or heads times rows, too large for one launch", who);
     if (!pointer(workspace, 256) || ws_bytes < p.ws_bytes)
         return fail(DSPK_EINVAL, "%s: workspace of %zu bytes required (256-byte aligned)", who, p.ws_bytes);
     if (q == out) return fail(DSPK_EINVAL, "%s: out must not be q", who);

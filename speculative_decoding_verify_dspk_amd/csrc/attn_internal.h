@@ -93,13 +93,13 @@ constexpr int kAttnWaves = 8;
 constexpr int kAttnStep = 32;                       // positions of a wave's step
 constexpr int kAttnTile = 256 + 32;                 // floats of a 16 x 16 tile of partial sums, with m and sum of its rows
 constexpr int kAttnCounter = 16;                   // words from one arrival counter to the next: a memory line each
-constexpr int64_t kAttnJoinBytes = 64 << 10;        // partial sums of a segment above which their addition gets a launch
+constexpr int64_t kAttnJoinBytes = 64 << 10;        // partial sums of a segment's row block above which their addition gets a launch
 constexpr int attn_tiles(int d) { return d == 256 ? 1 : 2; }         // most row tiles of a wave (its registers)
 constexpr int attn_piece(int d, int rt) { return rt * (d / 16) * kAttnTile; }  // floats of a row block's partial sums
 struct AttnPlan {
     int32_t tiles, blocks, groups;
     int32_t join;                   // shared segments are added by a launch of their own
-    int32_t pairs;                  // segments are of two units at most
+    int32_t pairs;                  // segments are of two units at most, by the page table's width
     bool fits;                      // unit numbers fit 31 bits
     size_t off_part, ws_bytes;      // workspace: counters, then partial sums
 };

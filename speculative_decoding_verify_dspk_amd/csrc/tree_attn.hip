@@ -13,7 +13,10 @@
 // same time, out of its L2 for all but the first (3 row blocks: 84 MB missed L2
 // of 240 MB asked for).  A segment shared by groups leaves partial sums in the
 // workspace; the last to arrive adds them in order (deterministic), each wave
-// its own tiles, or a launch of its own does where they are many.
+// its own tiles, or a launch of its own does where they may be many.  The host,
+// which does not know the lengths, plans for those that the page table has room
+// for: one token over 1021 positions takes 8.3 us under a table of that size, 12.5
+// under one of 8 or 128 times it (a launch of its own that finds little to add).
 //
 // Within a workgroup each wave takes its own positions, so k and v go from
 // memory to the matrix cores without LDS or barriers: the cache is stored in
@@ -38,7 +41,8 @@
 // of 6 rows over up to 8190 positions 25.7 us (97 MB); 32 of 8 rows over up to
 // 16384 (1.37 GB) 248 us, 5.5 TB/s of the 6.5 this device streams.  Over 8-bit
 // caches of many rows the vector ALUs: decoding takes half of their work (17 rows
-// of 40 heads over 32768 positions, 70 MB: 38 us, ALUs busy for 55% of it).
+// of 40 heads over 32768 positions, 70 MB: 39 us, ALUs busy for 55% of it), and
+// the scores' spread: see the references below.
 #include <hip/hip_runtime.h>
 
 #include "decode.h"
@@ -329,9 +333,14 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
         // Outputs and sum of each row, in units of 2^m: m is the row's reference,
         // the maximum (log2) of probability times v scale over the first positions that
         // it sees.  Later ones may pass it by 2^11 (8 bits) or 2^32 before anything has to
-        // be scaled down; then, which real scores hardly ever ask for, the wave
-        // starts its positions over with the higher reference.  So the loop neither
-        // takes maxima nor rescales.
+        // be scaled down; then the wave starts its positions over with the higher
+        // reference.  So the loop neither takes maxima nor rescales, and time depends on
+        // the scores: over 8 bits 17 rows of 40 heads at 32768 positions (caches in
+        // memory) take 45 us with scores of standard deviation 1.5, 84 / 130 / 157 /
+        // 165 with 3 / 4 / 5 / 6, a tree of 16 at 6000 positions 13.9 and 17.5 / 19.7 /
+        // 19.8 / 20.0; at worst, with scores that rise from step to step, every step has
+        // those before it taken again.  Over bf16 nothing changes up to 6 (28.8 us for
+        // 4 requests of 6 rows, 248 for 32 trees of 8).
         f32x4 o[RT][VB];
         float m[RT], l[RT];
 #pragma unroll
@@ -757,8 +766,8 @@ void tree_attn_kernel(const AttnArgs A, const int32_t *__restrict__ page_table) 
 
 // The pieces of shared segments, where they are more than the last workgroup of
 // a segment adds in good time (A.join): a workgroup per 16 x 16 output tile, a
-// wave for every fourth piece, in group order.  Latency: 3.4 us for 8 segments
-// of 24 pieces and 16 rows, 4.5 for 24 of 11 pieces and 32 rows.
+// wave for every fourth piece, in group order.  Latency: 3.5-4.0 us for 32 times
+// 8 pieces of 16 rows, 4.7-5.0 for 24 times 11 pieces of 32 rows.
 template <int D, int RT>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(const AttnArgs A) {
     constexpr int VB = D / 16, XB = 8;              // pieces of a wave in flight
