@@ -26,7 +26,11 @@
  *                         drafts) over that cache;
  *   dspk_tree_layout, dspk_accept_tree_greedy, dspk_kv_commit - a tree's masks
  *                         and positions, greedy acceptance along it, and the
- *                         accepted path's cache entries moved together.
+ *                         accepted path's cache entries moved together;
+ *   dspk_add_rmsnorm, dspk_silu_mul, dspk_i8_quantize, dspk_i8_read, dspk_i8_gemm -
+ *                         a layer's rows between its projections, in 8-bit codes,
+ *                         and products of such rows with 8-bit weights;
+ *   dspk_moe_route, dspk_moe_mlp - a mixture-of-experts layer for a few tokens.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -719,6 +723,191 @@ int dspk_accept_tree_greedy(const int32_t *target_ids, const int32_t *draft_ids,
  */
 int dspk_kv_commit(int32_t count, const dspk_kv_cache *caches, const dspk_attn_batch *batch, const int32_t *path,
                    const int32_t *accept_len, int32_t *new_len, void *stream);
+
+/*
+ * The 8-bit integer side of a layer
+ * ---------------------------------
+ * Rows and weights in signed 8-bit codes with one fp32 scale per row (token) and
+ * per output channel.  Sums of 8-bit products are exact in 32-bit integers, so
+ * a row's result is the same bits whatever rows it is computed with, alone or in
+ * a prompt: verifying drafts gives exactly what one-token decoding gives.  Per
+ * layer: dspk_add_rmsnorm, dspk_i8_gemm over q, k and v, the attention side's
+ * calls, dspk_i8_quantize, dspk_i8_gemm over o, dspk_add_rmsnorm, then either
+ * dspk_i8_gemm over gate and up, dspk_silu_mul and dspk_i8_gemm over down, or
+ * dspk_moe_route and dspk_moe_mlp.
+ *
+ * Rows in 8 bits: codes int8 [m][ld] (ld a multiple of 16, 16-byte aligned: rows
+ * are read in whole 16-byte pieces, whose bytes past a row's length do not
+ * matter) and scales float [m].  A row becomes codes as in an 8-bit cache
+ * (dspk_kv_append): scale = max|x| / 127, code = x * (127 / max|x|) rounded half to
+ * even, each step in fp32; a row holding a value that is not finite gets the scale
+ * NaN and so reads as NaN, one whose largest magnitude is below 4e-37 reads as
+ * zeros.
+ */
+#define DSPK_I8_MAX_K 131071  /* longest sum of 8-bit products that 32 bits hold */
+#define DSPK_MAX_WIDTH 32768  /* longest row of the norm, activation and quantising calls */
+
+/*
+ * Where a row call puts its result (host struct, arrays on the device): bf16
+ * rows, 8-bit rows, or both.
+ *
+ *   rows   : bf16 [m][ld], ld % 8 == 0, 16-byte aligned, or NULL;
+ *   codes  : int8 [m][ldc], ldc % 16 == 0, 16-byte aligned, or NULL;
+ *   scales : float [m], with codes.
+ * Columns past a row's length are left as they are.
+ */
+typedef struct dspk_rows_out {
+    uint16_t *rows;
+    int64_t ld;
+    int8_t *codes;
+    int64_t ldc;
+    float *scales;
+} dspk_rows_out;
+
+/*
+ * The residual stream's step between two parts of a layer, in one launch:
+ *   s = x + residual;  residual_out = s;  y = s * w / sqrt(mean(s^2) + eps).
+ * s is kept in fp32 for y and rounded once, to the residual's type, on storing.
+ *
+ *   x            : rows [m][ldx] of x_dtype (DSPK_F32 | DSPK_BF16): a projection's
+ *                  output; or NULL: nothing is added;
+ *   residual     : rows [m][ldr] of r_dtype, or NULL: zeros (x or residual
+ *                  must be given);
+ *   residual_out : rows [m][ldro] of r_dtype, or NULL: the sum is not stored.  May
+ *                  be residual or x itself (with the same type and leading
+ *                  dimension);
+ *   weight       : float [n], 16-byte aligned, or NULL: ones;
+ *   eps          : finite, >= 0;
+ *   m, n         : rows, >= 0 (0: nothing is done), and their length, 1 ..
+ *                  DSPK_MAX_WIDTH;
+ *   out          : y (rows, codes or both).
+ * Leading dimensions: >= n, multiples of 4 (fp32) or 8 (bf16), rows 16-byte
+ * aligned.  Outputs may not overlap inputs otherwise than as said.  The squares
+ * are summed in fp32: magnitudes up to 1e18.
+ * Errors: DSPK_EINVAL, DSPK_EUNSUPPORTED (n > DSPK_MAX_WIDTH), DSPK_EDEVICE.
+ */
+int dspk_add_rmsnorm(const void *x, int64_t ldx, int32_t x_dtype, const void *residual, int64_t ldr, int32_t r_dtype,
+                     void *residual_out, int64_t ldro, const float *weight, float eps, int32_t m, int32_t n,
+                     const dspk_rows_out *out, void *stream);
+
+/* y = gate / (1 + exp(-gate)) * up in fp32, rounded once into out.  gate, up: rows
+ * [m][ld] of dtype, as above; they may be column ranges of one array. */
+int dspk_silu_mul(const void *gate, int64_t ldg, const void *up, int64_t ldu, int32_t dtype, int32_t m, int32_t n,
+                  const dspk_rows_out *out, void *stream);
+
+/* Rows [m][ldx] of dtype into 8 bits; and the values that 8-bit rows stand for
+ * (scale * code in fp32, rounded once) as rows [m][ldy] of dtype. */
+int dspk_i8_quantize(const void *x, int64_t ldx, int32_t dtype, int32_t m, int32_t n, int8_t *codes, int64_t ldc,
+                     float *scales, void *stream);
+int dspk_i8_read(const int8_t *codes, int64_t ldc, const float *scales, int32_t m, int32_t n, void *y, int64_t ldy,
+                 int32_t dtype, void *stream);
+
+/*
+ * Weights in 8 bits, in the order that the matrix cores take them: `count`
+ * weights [n][k] (1 for a projection, the experts of a mixture layer).
+ *
+ *   tiles  : device memory of dspk_i8_tiled_bytes(n, k, count) bytes, 256-byte
+ *            aligned, written by dspk_i8_pack; weight g's byte of (column c, K r)
+ *            is at [g][c / 16][r / 64][r % 64 / 16][c % 16][r % 16], zero past n and k;
+ *   scales : float [count][n], w = scale * code.
+ */
+typedef struct dspk_i8_weight {
+    int32_t n;
+    int32_t k;
+    int32_t count;
+    const void *tiles;
+    const float *scales;
+} dspk_i8_weight;
+
+/* 0 if the shape is not supported (n, count >= 1, 1 <= k <= DSPK_I8_MAX_K). */
+size_t dspk_i8_tiled_bytes(int32_t n, int32_t k, int32_t count);
+
+/* Codes int8 [count * n][ldc] (weight g's column c is row g * n + c; any ldc >= k,
+ * any alignment) into tiles: once per weight, one launch. */
+int dspk_i8_pack(const int8_t *codes, int64_t ldc, int32_t n, int32_t k, int32_t count, void *tiles, size_t tiles_bytes,
+                 void *stream);
+
+/*
+ * Products of 8-bit rows with an 8-bit weight:
+ *   y[i][c] = float(sum_r x[i][r] * w[c][r]) * x_scales[i] * scales[c],
+ * the sum exact, the two products in fp32, then rounded to y's type: any number of
+ * rows, from one token to a prompt, with the same bits for a row of the same codes.
+ *
+ *   w        : count must be 1;
+ *   x        : codes [m][ldx], ldx >= k, ldx % 16 == 0, 16-byte aligned;
+ *   x_scales : float [m];
+ *   m        : rows, >= 0 (0: nothing is done);
+ *   y        : rows [m][ldy] of y_dtype (DSPK_F32 | DSPK_BF16), ldy >= n, 4-byte
+ *              aligned;
+ *   workspace: NULL, or >= dspk_i8_workspace_bytes(n, k, m) bytes, 256-byte aligned,
+ *              zero-filled before its first use; every call leaves its counters at
+ *              zero, so one buffer of the largest size serves any sequence of these
+ *              calls ordered on one stream.  With it, calls with few columns and
+ *              many rows split their sums over several workgroups (the result is
+ *              the same).
+ * Errors: DSPK_EINVAL, DSPK_EUNSUPPORTED (k > DSPK_I8_MAX_K, more tiles than one
+ * launch numbers), DSPK_EDEVICE.
+ */
+int dspk_i8_gemm(const dspk_i8_weight *w, const int8_t *x, int64_t ldx, const float *x_scales, int32_t m, void *y,
+                 int32_t y_dtype, int64_t ldy, void *workspace, size_t ws_bytes, void *stream);
+size_t dspk_i8_workspace_bytes(int32_t n, int32_t k, int32_t m);
+
+/*
+ * A mixture-of-experts layer for a few tokens
+ * -------------------------------------------
+ * Each token goes through the top_k experts that its router scores highest, and
+ * each expert that any token chose is read once for all of them.
+ */
+#define DSPK_MOE_MAX_ROWS    64
+#define DSPK_MOE_MAX_EXPERTS 1024
+#define DSPK_MOE_MAX_TOP     32
+
+/*
+ * The router: scores z[i][e] = sum_r x[i][r] * router[e][r] in fp32 and of each
+ * row the top_k largest, in descending order (equal scores: the lower expert first).
+ *
+ *   x         : bf16 rows [m][ldx], ldx >= k, ldx % 8 == 0, 16-byte aligned;
+ *   router    : bf16 rows [experts][ldr], alike;
+ *   m, k      : rows, 0 .. DSPK_MOE_MAX_ROWS; their length, >= 1;
+ *   experts   : 1 .. DSPK_MOE_MAX_EXPERTS;  top_k: 1 .. min(experts, DSPK_MOE_MAX_TOP);
+ *   normalize : 0: weights are the softmax over all experts; 1: those divided by the
+ *               sum of the chosen ones;
+ *   ids       : int32 [m][top_k] output;  weights: float [m][top_k] output;
+ *   scores    : float [m][lds] output, or NULL;
+ *   workspace : >= dspk_moe_workspace_bytes(...) bytes, as of dspk_moe_mlp.
+ * A score that is NaN counts as the lowest for ids; a row with such a score, with
+ * one of plus infinity, or with none above minus infinity gets weights of NaN.
+ */
+int dspk_moe_route(const uint16_t *x, int64_t ldx, const uint16_t *router, int64_t ldr, int32_t m, int32_t k,
+                   int32_t experts, int32_t top_k, int32_t normalize, int32_t *ids, float *weights, float *scores,
+                   int64_t lds, void *workspace, size_t ws_bytes, void *stream);
+
+/* Workspace of dspk_moe_route and dspk_moe_mlp (one buffer serves both): zero-fill
+ * it once before its first use; every call leaves its counters at zero, so one
+ * buffer of the largest size serves any sequence of these calls ordered on one
+ * stream.  0 if a size is not supported. */
+size_t dspk_moe_workspace_bytes(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k);
+
+/*
+ * The experts, in two launches:
+ *   h_ij = silu(x_i . gate_e) * (x_i . up_e), e = ids[i][j], in 8 bits with a scale
+ *          per row;
+ *   y_i  = sum_j weights[i][j] * (h_ij . down_e), added in the order of j in fp32.
+ * The products are those of dspk_i8_gemm, kept in fp32.
+ *
+ *   gate, up : weights of n = inter, k = hidden, count = experts;
+ *   down     : n = hidden, k = inter, count = experts;
+ *   x        : codes [m][ldx] with x_scales, as in dspk_i8_gemm; m <= DSPK_MOE_MAX_ROWS;
+ *   ids, weights : [m][top_k], of dspk_moe_route or the caller's own; an id may
+ *              come more than once;
+ *   y        : rows [m][ldy] of y_dtype, ldy >= hidden, 4-byte aligned;
+ *   workspace: >= dspk_moe_workspace_bytes(hidden, inter, experts, m, top_k).
+ * An id of -1 is a slot that is not used: it adds nothing.  Any other id that is no
+ * expert is a data fault: its row of y is NaN.  Deterministic.
+ */
+int dspk_moe_mlp(const dspk_i8_weight *gate, const dspk_i8_weight *up, const dspk_i8_weight *down, const int8_t *x,
+                 int64_t ldx, const float *x_scales, int32_t m, const int32_t *ids, const float *weights, int32_t top_k,
+                 void *y, int32_t y_dtype, int64_t ldy, void *workspace, size_t ws_bytes, void *stream);
 
 /*
  * Draft-cap policy (host code; no GPU, no workspace).

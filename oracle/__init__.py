@@ -11,3 +11,4 @@ from .dspk_oracle import (  # noqa: F401
     penalized_logits, truncate, accept_sample_filtered,
 )
 from . import attention  # noqa: F401,E402
+from . import layer8  # noqa: F401,E402

@@ -24,6 +24,7 @@ DSPK_F32, DSPK_BF16 = 0, 1
 MAX_ROWS = 32
 MAX_GROUPED = 4
 MAX_TREE = 64
+MOE_MAX_ROWS = 64
 
 
 class DspkError(RuntimeError):
@@ -67,6 +68,16 @@ class QKPrepDesc(ctypes.Structure):
     """dspk_qk_prep (host struct)."""
     _fields_ = [("eps", c_float), ("q_weight", c_void_p), ("k_weight", c_void_p), ("inv_freq", c_void_p),
                 ("rotary_dim", c_int32), ("interleaved", c_int32), ("positions", c_void_p)]
+
+
+class RowsOutDesc(ctypes.Structure):
+    """dspk_rows_out (host struct)."""
+    _fields_ = [("rows", c_void_p), ("ld", c_int64), ("codes", c_void_p), ("ldc", c_int64), ("scales", c_void_p)]
+
+
+class Int8WeightDesc(ctypes.Structure):
+    """dspk_i8_weight: weights in 8-bit codes, in the library's tiled layout."""
+    _fields_ = [("n", c_int32), ("k", c_int32), ("count", c_int32), ("tiles", c_void_p), ("scales", c_void_p)]
 
 
 class SampleParamsDesc(ctypes.Structure):
@@ -149,6 +160,25 @@ def lib() -> ctypes.CDLL:
                                               c_void_p, c_void_p]),
         "dspk_kv_commit": (c_int32, [c_int32, P(KVCacheDesc), P(AttnBatchDesc), c_void_p, c_void_p, c_void_p,
                                      c_void_p]),
+        "dspk_add_rmsnorm": (c_int32, [c_void_p, c_int64, c_int32, c_void_p, c_int64, c_int32, c_void_p, c_int64,
+                                       c_void_p, c_float, c_int32, c_int32, P(RowsOutDesc), c_void_p]),
+        "dspk_silu_mul": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32, c_int32, P(RowsOutDesc),
+                                    c_void_p]),
+        "dspk_i8_quantize": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_int32, c_void_p, c_int64, c_void_p,
+                                       c_void_p]),
+        "dspk_i8_read": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_int64, c_int32,
+                                   c_void_p]),
+        "dspk_i8_tiled_bytes": (c_size_t, [c_int32, c_int32, c_int32]),
+        "dspk_i8_pack": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_int32, c_void_p, c_size_t, c_void_p]),
+        "dspk_i8_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32]),
+        "dspk_i8_gemm": (c_int32, [P(Int8WeightDesc), c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_int32, c_int64,
+                                   c_void_p, c_size_t, c_void_p]),
+        "dspk_moe_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32, c_int32, c_int32]),
+        "dspk_moe_route": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32, c_int32,
+                                     c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
+        "dspk_moe_mlp": (c_int32, [P(Int8WeightDesc), P(Int8WeightDesc), P(Int8WeightDesc), c_void_p, c_int64, c_void_p,
+                                   c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_int64, c_void_p, c_size_t,
+                                   c_void_p]),
         "dspk_choose_cap": (c_int32, [P(ctypes.c_double), P(ctypes.c_double), c_int32, ctypes.c_double,
                                       P(ctypes.c_double)]),
         "dspk_cap_init": (c_int32, [P(CapControllerDesc), P(ctypes.c_double), P(ctypes.c_double), c_int32,
@@ -346,6 +376,113 @@ def _kv_rows(cache: KVCache, batch: AttnBatch, k, v):
     for t, name in ((k, "k"), (v, "v")):
         _columns(t, name, cache.kv_heads * cache.head_dim)
     return kp, ldk, vp, ldv, dt
+
+
+# ---------------------------------------------- 8-bit rows, weights, experts
+def _int8(t, name: str):
+    import torch
+    if t.dtype != torch.int8:
+        raise ValueError(f"{name}: expected int8 codes, got {t.dtype}")
+    return t
+
+
+def _floats(t, name: str, need: int):
+    import torch
+    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.numel() < need):
+        raise ValueError(f"{name}: expected a contiguous float32 tensor of at least {need} entries")
+    return t
+
+
+def _sized_rows(t, name: str, m: int, n: int):
+    """(address, leading dimension, element type) of rows [>= m][ld] with n columns at least."""
+    at = _row_array(t, name, m)
+    _columns(t, name, n)
+    return at
+
+
+def _code_rows(codes, scales, m: int, n: int, name: str):
+    """(address, leading dimension, address of the scales) of 8-bit rows."""
+    ld = _rows(_int8(codes, name), name)
+    if codes.shape[0] < m:
+        raise ValueError(f"{name}: {codes.shape[0]} rows, {m} needed")
+    _columns(codes, name, n)
+    if scales is None:
+        raise ValueError(f"{name}: 8-bit rows have scales")
+    return codes.data_ptr(), ld, _floats(scales, f"the scales of {name}", m).data_ptr()
+
+
+def _rows_out(m: int, n: int, out, codes, scales) -> RowsOutDesc:
+    d = RowsOutDesc()
+    if out is not None:
+        d.rows, d.ld, dt = _sized_rows(out, "out", m, n)
+        if dt != DSPK_BF16:
+            raise ValueError("out: expected bf16 rows (2-byte elements)")
+    if codes is not None:
+        d.codes, d.ldc, d.scales = _code_rows(codes, scales, m, n, "codes")
+    elif scales is not None:
+        raise ValueError("scales: there are no codes")
+    return d
+
+
+def i8_tiled_bytes(n: int, k: int, count: int = 1) -> int:
+    return lib().dspk_i8_tiled_bytes(n, k, count)
+
+
+class Int8Weight:
+    """Weights in 8-bit codes with a scale per output channel, packed into the
+    library's tiled layout: codes int8 [n][k] and scales float32 [n], or for
+    the experts of a mixture layer [count][n][k] and [count][n]."""
+
+    def __init__(self, codes, scales, stream=None):
+        import torch
+        _int8(codes, "codes")
+        if codes.dim() not in (2, 3) or codes.stride(-1) != 1:
+            raise ValueError("codes: expected [n][k] or [count][n][k] with unit column stride")
+        self.n, self.k = codes.shape[-2:]
+        self.count = codes.shape[0] if codes.dim() == 3 else 1
+        if codes.dim() == 3 and self.count > 1 and codes.stride(0) != self.n * codes.stride(1):
+            raise ValueError("codes: the weights of one call follow each other")
+        if scales.shape != codes.shape[:-1]:
+            raise ValueError(f"scales: expected {tuple(codes.shape[:-1])}, got {tuple(scales.shape)}")
+        self.scales = _floats(scales, "scales", self.count * self.n)
+        nbytes = i8_tiled_bytes(self.n, self.k, self.count)
+        if nbytes == 0:
+            raise DspkError(-2, lib().dspk_last_error().decode())
+        ldc = codes.stride(-2) if self.n > 1 or self.count > 1 else max(codes.stride(-2), self.k)
+        self.tiles = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        _check(lib().dspk_i8_pack(codes.data_ptr(), ldc, self.n, self.k, self.count, self.tiles.data_ptr(), nbytes,
+                                  _stream(stream)))
+        self.desc = Int8WeightDesc(self.n, self.k, self.count, self.tiles.data_ptr(), scales.data_ptr())
+
+    @classmethod
+    def quantize(cls, w, stream=None) -> "Int8Weight":
+        """From rows of float32 or bf16, [n][k] or [count][n][k]: each output channel in 8 bits."""
+        import torch
+        k = w.shape[-1]
+        rows = w.reshape(-1, k)
+        ld = -(-k // 16) * 16
+        codes = torch.empty((rows.shape[0], ld), dtype=torch.int8, device=w.device)[:, :k]
+        scales = torch.empty(rows.shape[0], dtype=torch.float32, device=w.device)
+        i8_quantize(rows, rows.shape[0], k, codes, scales, stream)
+        return cls(codes.view(w.shape) if ld == k else codes.unflatten(0, w.shape[:-1]), scales.view(w.shape[:-1]), stream)
+
+    @property
+    def nbytes(self) -> int:
+        """Bytes of the codes and scales."""
+        return self.count * self.n * (self.k + 4)
+
+
+class MoEWeights:
+    """The experts of a mixture layer: gate and up [experts][inter][hidden],
+    down [experts][hidden][inter]."""
+
+    def __init__(self, gate: Int8Weight, up: Int8Weight, down: Int8Weight):
+        self.gate, self.up, self.down = gate, up, down
+        self.hidden, self.inter, self.experts = gate.k, gate.n, gate.count
+
+    @property
+    def nbytes(self) -> int:
+        return self.gate.nbytes + self.up.nbytes + self.down.nbytes
 
 
 # ------------------------------------------------------------ cap policy
@@ -550,6 +687,89 @@ def prepare_kv_commit(caches: list, batch: AttnBatch, path, accept_len, new_len=
                     _stream(stream)).holding(caches, batch, path, accept_len, new_len)
 
 
+def prepare_add_rmsnorm(x, residual, residual_out, weight, m: int, n: int, eps: float = 1e-6, out=None, codes=None,
+                        scales=None, stream=None) -> Prepared:
+    """s = x + residual -> residual_out, its RMS norm times weight -> out (bf16
+    rows) and / or codes with scales; x, residual, residual_out and weight may be
+    None."""
+    xp, ldx, dx = (None, 0, DSPK_F32) if x is None else _sized_rows(x, "x", m, n)
+    rp, ldr, dr = (None, 0, None) if residual is None else _sized_rows(residual, "residual", m, n)
+    op, ldo, do = (None, 0, None) if residual_out is None else _sized_rows(residual_out, "residual_out", m, n)
+    if None not in (dr, do) and dr != do:
+        raise ValueError("residual and residual_out: expected one element type")
+    dr = next((d for d in (dr, do) if d is not None), DSPK_F32)
+    desc = _rows_out(m, n, out, codes, scales)
+    return Prepared("dspk_add_rmsnorm", xp, ldx, dx, rp, ldr, dr, op, ldo, _ptr(_floats(weight, "weight", n)),
+                    float(eps), m, n, ctypes.byref(desc),
+                    _stream(stream)).holding(x, residual, residual_out, weight, out, codes, scales)
+
+
+def prepare_silu_mul(gate, up, m: int, n: int, out=None, codes=None, scales=None, stream=None) -> Prepared:
+    gp, ldg, dg = _sized_rows(gate, "gate", m, n)
+    up_, ldu, du = _sized_rows(up, "up", m, n)
+    if dg != du:
+        raise ValueError("gate and up: expected one element type")
+    desc = _rows_out(m, n, out, codes, scales)
+    return Prepared("dspk_silu_mul", gp, ldg, up_, ldu, dg, m, n, ctypes.byref(desc),
+                    _stream(stream)).holding(gate, up, out, codes, scales)
+
+
+def prepare_i8_quantize(x, m: int, n: int, codes, scales, stream=None) -> Prepared:
+    xp, ldx, dx = _sized_rows(x, "x", m, n)
+    cp, ldc, sp = _code_rows(codes, scales, m, n, "codes")
+    return Prepared("dspk_i8_quantize", xp, ldx, dx, m, n, cp, ldc, sp, _stream(stream)).holding(x, codes, scales)
+
+
+def prepare_i8_read(codes, scales, m: int, n: int, y, stream=None) -> Prepared:
+    cp, ldc, sp = _code_rows(codes, scales, m, n, "codes")
+    yp, ldy, dy = _sized_rows(y, "y", m, n)
+    return Prepared("dspk_i8_read", cp, ldc, sp, m, n, yp, ldy, dy, _stream(stream)).holding(codes, scales, y)
+
+
+def prepare_i8_gemm(w: Int8Weight, x, x_scales, m: int, y, workspace=None, stream=None) -> Prepared:
+    """x: int8 rows [>= m][ldx] with x_scales; workspace: None, or a zero-filled
+    buffer of i8_workspace_bytes."""
+    xp, ldx, sp = _code_rows(x, x_scales, m, w.k, "x")
+    yp, ldy, dy = _sized_rows(y, "y", m, w.n)
+    return Prepared("dspk_i8_gemm", ctypes.byref(w.desc), xp, ldx, sp, m, yp, dy, ldy, _ptr(workspace),
+                    0 if workspace is None else workspace.numel(),
+                    _stream(stream)).holding(w, x, x_scales, y, workspace)
+
+
+def prepare_moe_route(x, router, m: int, ids, weights, workspace, normalize: bool = True, scores=None,
+                      stream=None) -> Prepared:
+    """x: bf16 rows [>= m][k]; router: bf16 [experts][k]; ids int32 and weights float32 [m][top_k]."""
+    experts, k = router.shape
+    rp, ldr, dr = _sized_rows(router, "router", experts, k)
+    xp, ldx, dx = _sized_rows(x, "x", m, k)
+    if dx != DSPK_BF16 or dr != DSPK_BF16:
+        raise ValueError("x and router: expected bf16 rows (2-byte elements)")
+    if ids.dim() != 2 or ids.shape[0] < m:
+        raise ValueError(f"ids: expected [{m}][top_k]")
+    top_k, zp, ldz = ids.shape[1], None, 0
+    if scores is not None:
+        zp, ldz, dz = _sized_rows(scores, "scores", m, experts)
+        if dz != DSPK_F32:
+            raise ValueError("scores: expected float32 rows")
+    return Prepared("dspk_moe_route", xp, ldx, rp, ldr, m, k, experts, top_k, int(normalize),
+                    _int32(ids, "ids", m * top_k).data_ptr(), _floats(weights, "weights", m * top_k).data_ptr(), zp, ldz,
+                    workspace.data_ptr(), workspace.numel(),
+                    _stream(stream)).holding(x, router, ids, weights, scores, workspace)
+
+
+def prepare_moe_mlp(moe: MoEWeights, x, x_scales, m: int, ids, weights, y, workspace, stream=None) -> Prepared:
+    """x: int8 rows [>= m][hidden] with x_scales; ids and weights [m][top_k], as moe_route gives them."""
+    xp, ldx, sp = _code_rows(x, x_scales, m, moe.hidden, "x")
+    yp, ldy, dy = _sized_rows(y, "y", m, moe.hidden)
+    if ids.dim() != 2 or ids.shape[0] < m:
+        raise ValueError(f"ids: expected [{m}][top_k]")
+    top_k = ids.shape[1]
+    return Prepared("dspk_moe_mlp", ctypes.byref(moe.gate.desc), ctypes.byref(moe.up.desc), ctypes.byref(moe.down.desc),
+                    xp, ldx, sp, m, _int32(ids, "ids", m * top_k).data_ptr(),
+                    _floats(weights, "weights", m * top_k).data_ptr(), top_k, yp, dy, ldy, workspace.data_ptr(),
+                    workspace.numel(), _stream(stream)).holding(moe, x, x_scales, ids, weights, y, workspace)
+
+
 # ------------------------------------------------------------ entry points
 def version() -> int:
     return lib().dspk_version()
@@ -717,3 +937,40 @@ def accept_tree_greedy(target_ids, draft_ids, parents, b: int, m_rows: int, acce
 
 def kv_commit(caches: list, batch: AttnBatch, path, accept_len, new_len=None, stream=None) -> None:
     prepare_kv_commit(caches, batch, path, accept_len, new_len, stream)()
+
+
+def add_rmsnorm(x, residual, residual_out, weight, m: int, n: int, **options) -> None:
+    """options as in prepare_add_rmsnorm."""
+    prepare_add_rmsnorm(x, residual, residual_out, weight, m, n, **options)()
+
+
+def silu_mul(gate, up, m: int, n: int, out=None, codes=None, scales=None, stream=None) -> None:
+    prepare_silu_mul(gate, up, m, n, out, codes, scales, stream)()
+
+
+def i8_quantize(x, m: int, n: int, codes, scales, stream=None) -> None:
+    prepare_i8_quantize(x, m, n, codes, scales, stream)()
+
+
+def i8_read(codes, scales, m: int, n: int, y, stream=None) -> None:
+    prepare_i8_read(codes, scales, m, n, y, stream)()
+
+
+def i8_workspace_bytes(n: int, k: int, m: int) -> int:
+    return lib().dspk_i8_workspace_bytes(n, k, m)
+
+
+def i8_gemm(w: Int8Weight, x, x_scales, m: int, y, workspace=None, stream=None) -> None:
+    prepare_i8_gemm(w, x, x_scales, m, y, workspace, stream)()
+
+
+def moe_workspace_bytes(hidden: int, inter: int, experts: int, m: int, top_k: int) -> int:
+    return lib().dspk_moe_workspace_bytes(hidden, inter, experts, m, top_k)
+
+
+def moe_route(x, router, m: int, ids, weights, workspace, normalize: bool = True, scores=None, stream=None) -> None:
+    prepare_moe_route(x, router, m, ids, weights, workspace, normalize, scores, stream)()
+
+
+def moe_mlp(moe: MoEWeights, x, x_scales, m: int, ids, weights, y, workspace, stream=None) -> None:
+    prepare_moe_mlp(moe, x, x_scales, m, ids, weights, y, workspace, stream)()

@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdspk.so")
 PROBE_LIB = os.path.join(PKG, "libdspk_probe.so")      # measurement only: the streaming-read probe
 SOURCES = ["qgemm.hip", "slab.hip", "prefill.hip", "pack.hip", "accept.hip", "noalloc.hip", "api.cpp", "plan.cpp", "policy.cpp",
-           "kv_cache.hip", "tree_attn.hip", "tree.hip", "attn_api.cpp"]
+           "kv_cache.hip", "tree_attn.hip", "tree.hip", "attn_api.cpp",
+           "rows8.hip", "i8_gemm.hip", "moe.hip", "i8_api.cpp"]
 
 # Packed fp32 instructions are kept out of every HIP object (the compiler
 # would otherwise form them from ordinary float code).

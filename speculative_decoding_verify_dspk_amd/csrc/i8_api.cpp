@@ -1,0 +1,402 @@
+// C ABI of the 8-bit integer side: argument checks, launch plans and launches.  As
+// in the rest of the ABI, everything the host can see is checked before anything
+// is enqueued; nothing here allocates, frees or synchronises.
+#include <math.h>
+#include <stdarg.h>
+#include <stdio.h>
+
+#include "../../include/dspk.h"
+#include "i8_internal.h"
+
+namespace dspk {
+
+I8Plan i8_plan(int32_t n, int32_t k, int32_t m, int cus) {
+    (void)cus;
+    I8Plan p{};
+    const int64_t steps = ((int64_t)k + kI8K - 1) / kI8K;
+    p.row_tiles = m <= 16 ? 1 : m <= 32 ? 2 : 4;
+    const int64_t waves = (steps + 7) / 8;
+    p.waves = (int32_t)(waves > 16 ? 16 : waves);
+    p.grid_x = ((int64_t)n + kI8Cols - 1) / kI8Cols;
+    p.grid_y = ((int64_t)m + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
+    // threads of the grid's first dimension in 32 bits, workgroups of its second in 16
+    p.fits = p.grid_x * 64 * p.waves <= UINT32_MAX && p.grid_y <= 65535;
+    p.ws_bytes = 0;
+    return p;
+}
+
+MoePlan moe_plan(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k) {
+    MoePlan p{};
+    const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    const size_t slots = (size_t)m * top_k;
+    p.ldh = ((int64_t)inter + kI8Cols - 1) / kI8Cols * kI8Cols;
+    p.ldp = ((int64_t)hidden + kI8Cols - 1) / kI8Cols * kI8Cols;
+    p.off_scores = up(kMoeHead);
+    p.off_h = up(p.off_scores + (size_t)m * experts * sizeof(float));
+    p.off_part = up(p.off_h + slots * p.ldh * sizeof(float));
+    p.ws_bytes = up(p.off_part + slots * p.ldp * sizeof(float));
+    return p;
+}
+
+}  // namespace dspk
+
+namespace {
+
+int fail(int code, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return dspk::set_error(code, buf);
+}
+
+int ok() { return dspk::set_error(DSPK_OK, ""); }
+
+int launch_result(hipError_t e, const char *who) {
+    if (e != hipSuccess) return fail(DSPK_EDEVICE, "%s: launch failed: %s", who, hipGetErrorString(e));
+    return ok();
+}
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+bool pointer(const void *p, size_t a) { return p != nullptr && aligned(p, a); }
+
+int check_dtype(int32_t dtype, const char *name, const char *who) {
+    if (dtype != DSPK_F32 && dtype != DSPK_BF16)
+        return fail(DSPK_EINVAL, "%s: element type %d of %s (DSPK_F32 or DSPK_BF16)", who, dtype, name);
+    return DSPK_OK;
+}
+
+// Rows [m][ld] of n elements, in whole 16-byte pieces.
+int check_rows(const void *p, int64_t ld, int32_t n, int32_t dtype, const char *name, const char *who) {
+    const int64_t per = dtype == DSPK_F32 ? 4 : 8;
+    if (!pointer(p, 16)) return fail(DSPK_EINVAL, "%s: %s must be a non-NULL 16-byte aligned device pointer", who, name);
+    if (ld < n || ld % per)
+        return fail(DSPK_EINVAL, "%s: leading dimension %lld of %s must be >= %d and a multiple of %lld", who,
+                    (long long)ld, name, n, (long long)per);
+    return DSPK_OK;
+}
+
+int check_codes(const void *p, int64_t ld, int32_t n, const float *scales, const char *name, const char *who) {
+    if (!pointer(p, 16)) return fail(DSPK_EINVAL, "%s: %s must be a non-NULL 16-byte aligned device pointer", who, name);
+    if (ld < n || ld % 16)
+        return fail(DSPK_EINVAL, "%s: leading dimension %lld of %s must be >= %d and a multiple of 16", who,
+                    (long long)ld, name, n);
+    if (!pointer(scales, 4)) return fail(DSPK_EINVAL, "%s: the scales of %s are NULL or misaligned", who, name);
+    return DSPK_OK;
+}
+
+int check_width(int32_t m, int32_t n, const char *who) {
+    if (m < 0) return fail(DSPK_EINVAL, "%s: m=%d must be >= 0", who, m);
+    if (n < 1) return fail(DSPK_EINVAL, "%s: n=%d must be >= 1", who, n);
+    if (n > DSPK_MAX_WIDTH) return fail(DSPK_EUNSUPPORTED, "%s: n=%d (at most %d)", who, n, DSPK_MAX_WIDTH);
+    return DSPK_OK;
+}
+
+// y of the products: rows [m][ldy], elements alone aligned.
+int check_y(const void *y, int64_t ldy, int32_t n, const char *who) {
+    if (!pointer(y, 4)) return fail(DSPK_EINVAL, "%s: y NULL or misaligned", who);
+    if (ldy < n) return fail(DSPK_EINVAL, "%s: ldy=%lld < n=%d", who, (long long)ldy, n);
+    return DSPK_OK;
+}
+
+int check_out(const dspk_rows_out *out, dspk::RowArgs &A, const char *who) {
+    if (out->rows != nullptr) {
+        int rc = check_rows(out->rows, out->ld, A.n, DSPK_BF16, "out.rows", who);
+        if (rc) return rc;
+    }
+    if (out->codes != nullptr) {
+        int rc = check_codes(out->codes, out->ldc, A.n, out->scales, "out.codes", who);
+        if (rc) return rc;
+    }
+    A.rows = out->rows;
+    A.ld = out->ld;
+    A.codes = out->codes;
+    A.ldc = out->ldc;
+    A.scales = out->scales;
+    return DSPK_OK;
+}
+
+int check_some_out(const dspk_rows_out *out, const char *who) {
+    if (out == nullptr || (out->rows == nullptr && out->codes == nullptr))
+        return fail(DSPK_EINVAL, "%s: out is NULL, or has neither rows nor codes", who);
+    if (out->codes == nullptr && out->scales != nullptr) return fail(DSPK_EINVAL, "%s: out.scales without out.codes", who);
+    return DSPK_OK;
+}
+
+int check_i8_shape(int32_t n, int32_t k, int32_t count, const char *who) {
+    if (n < 1 || k < 1 || count < 1)
+        return fail(DSPK_EINVAL, "%s: n=%d, k=%d and count=%d must be >= 1", who, n, k, count);
+    if (k > DSPK_I8_MAX_K) return fail(DSPK_EUNSUPPORTED, "%s: k=%d (at most %d)", who, k, DSPK_I8_MAX_K);
+    return DSPK_OK;
+}
+
+int64_t tiles_of(int32_t n) { return ((int64_t)n + dspk::kI8Cols - 1) / dspk::kI8Cols; }
+int64_t steps_of(int32_t k) { return ((int64_t)k + dspk::kI8K - 1) / dspk::kI8K; }
+
+int check_i8_weight(const dspk_i8_weight *w, const char *name, const char *who) {
+    if (w == nullptr) return fail(DSPK_EINVAL, "%s: %s is NULL", who, name);
+    int rc = check_i8_shape(w->n, w->k, w->count, who);
+    if (rc) return rc;
+    if (!pointer(w->tiles, 256) || !pointer(w->scales, 4))
+        return fail(DSPK_EINVAL, "%s: tiles of %s must be 256-byte aligned, its scales 4-byte aligned, neither NULL", who,
+                    name);
+    return DSPK_OK;
+}
+
+// The sizes of an expert layer; 0: fine.
+int check_moe(int32_t m, int32_t experts, int32_t top_k, const char *who) {
+    if (m < 0 || m > DSPK_MOE_MAX_ROWS) return fail(DSPK_EINVAL, "%s: m=%d out of 0..%d", who, m, DSPK_MOE_MAX_ROWS);
+    if (experts < 1 || experts > DSPK_MOE_MAX_EXPERTS)
+        return fail(DSPK_EINVAL, "%s: experts=%d out of 1..%d", who, experts, DSPK_MOE_MAX_EXPERTS);
+    if (top_k < 1 || top_k > DSPK_MOE_MAX_TOP)
+        return fail(DSPK_EINVAL, "%s: top_k=%d out of 1..%d", who, top_k, DSPK_MOE_MAX_TOP);
+    return DSPK_OK;
+}
+
+int check_workspace(const void *ws, size_t bytes, size_t need, const char *who) {
+    if (!pointer(ws, 256) || bytes < need)
+        return fail(DSPK_EINVAL, "%s: workspace of %zu bytes required (256-byte aligned)", who, need);
+    return DSPK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int dspk_add_rmsnorm(const void *x, int64_t ldx, int32_t x_dtype, const void *residual, int64_t ldr, int32_t r_dtype,
+                     void *residual_out, int64_t ldro, const float *weight, float eps, int32_t m, int32_t n,
+                     const dspk_rows_out *out, void *stream) {
+    const char *who = "dspk_add_rmsnorm";
+    dspk::RowArgs A{};
+    int rc = check_width(m, n, who);
+    if (rc || (rc = check_dtype(x_dtype, "x", who)) || (rc = check_dtype(r_dtype, "residual", who))) return rc;
+    if (!(eps >= 0.f) || !isfinite(eps)) return fail(DSPK_EINVAL, "%s: eps must be finite and >= 0", who);
+    if (!aligned(weight, 16)) return fail(DSPK_EINVAL, "%s: weight must be 16-byte aligned", who);
+    if (m == 0) return ok();
+    if ((rc = check_some_out(out, who))) return rc;
+    if (x == nullptr && residual == nullptr) return fail(DSPK_EINVAL, "%s: x and residual are both NULL", who);
+    A.m = m;
+    A.n = n;
+    if ((x != nullptr && (rc = check_rows(x, ldx, n, x_dtype, "x", who))) ||
+        (residual != nullptr && (rc = check_rows(residual, ldr, n, r_dtype, "residual", who))) ||
+        (residual_out != nullptr && (rc = check_rows(residual_out, ldro, n, r_dtype, "residual_out", who))) ||
+        (rc = check_out(out, A, who)))
+        return rc;
+    if (residual_out != nullptr && ((residual_out == residual && ldro != ldr) ||
+                                    (residual_out == x && (r_dtype != x_dtype || ldro != ldx))))
+        return fail(DSPK_EINVAL, "%s: residual_out may be residual or x only with its type and leading dimension", who);
+    A.x = x;
+    A.ldx = ldx;
+    A.x_f32 = x_dtype == DSPK_F32;
+    A.r = residual;
+    A.ldr = ldr;
+    A.r_f32 = r_dtype == DSPK_F32;
+    A.r_out = residual_out;
+    A.ldro = ldro;
+    A.w = weight;
+    A.eps = eps;
+    return launch_result(dspk::launch_rows(dspk::kRowNorm, A, dspk::device_cus(), (hipStream_t)stream), who);
+}
+
+int dspk_silu_mul(const void *gate, int64_t ldg, const void *up, int64_t ldu, int32_t dtype, int32_t m, int32_t n,
+                  const dspk_rows_out *out, void *stream) {
+    const char *who = "dspk_silu_mul";
+    dspk::RowArgs A{};
+    int rc = check_width(m, n, who);
+    if (rc || (rc = check_dtype(dtype, "gate and up", who))) return rc;
+    if (m == 0) return ok();
+    if ((rc = check_some_out(out, who))) return rc;
+    A.m = m;
+    A.n = n;
+    if ((rc = check_rows(gate, ldg, n, dtype, "gate", who)) || (rc = check_rows(up, ldu, n, dtype, "up", who)) ||
+        (rc = check_out(out, A, who)))
+        return rc;
+    A.x = gate;
+    A.ldx = ldg;
+    A.r = up;
+    A.ldr = ldu;
+    A.x_f32 = A.r_f32 = dtype == DSPK_F32;
+    return launch_result(dspk::launch_rows(dspk::kRowSilu, A, dspk::device_cus(), (hipStream_t)stream), who);
+}
+
+int dspk_i8_quantize(const void *x, int64_t ldx, int32_t dtype, int32_t m, int32_t n, int8_t *codes, int64_t ldc,
+                     float *scales, void *stream) {
+    const char *who = "dspk_i8_quantize";
+    dspk::RowArgs A{};
+    int rc = check_width(m, n, who);
+    if (rc || (rc = check_dtype(dtype, "x", who))) return rc;
+    if (m == 0) return ok();
+    if ((rc = check_rows(x, ldx, n, dtype, "x", who)) || (rc = check_codes(codes, ldc, n, scales, "codes", who))) return rc;
+    A.m = m;
+    A.n = n;
+    A.x = x;
+    A.ldx = ldx;
+    A.x_f32 = dtype == DSPK_F32;
+    A.codes = codes;
+    A.ldc = ldc;
+    A.scales = scales;
+    return launch_result(dspk::launch_rows(dspk::kRowPlain, A, dspk::device_cus(), (hipStream_t)stream), who);
+}
+
+int dspk_i8_read(const int8_t *codes, int64_t ldc, const float *scales, int32_t m, int32_t n, void *y, int64_t ldy,
+                 int32_t dtype, void *stream) {
+    const char *who = "dspk_i8_read";
+    int rc = check_width(m, n, who);
+    if (rc || (rc = check_dtype(dtype, "y", who))) return rc;
+    if (m == 0) return ok();
+    if ((rc = check_codes(codes, ldc, n, scales, "codes", who)) || (rc = check_rows(y, ldy, n, dtype, "y", who))) return rc;
+    const dspk::I8ReadArgs A = {codes, ldc, scales, m, n, y, ldy, dtype == DSPK_F32};
+    return launch_result(dspk::launch_i8_read(A, (hipStream_t)stream), who);
+}
+
+size_t dspk_i8_tiled_bytes(int32_t n, int32_t k, int32_t count) {
+    if (check_i8_shape(n, k, count, "dspk_i8_tiled_bytes")) return 0;
+    const size_t one = (size_t)tiles_of(n) * steps_of(k) * dspk::kI8Frag;      // < 2^49
+    return one > (size_t)(SIZE_MAX / count) ? 0 : one * count;
+}
+
+int dspk_i8_pack(const int8_t *codes, int64_t ldc, int32_t n, int32_t k, int32_t count, void *tiles, size_t tiles_bytes,
+                 void *stream) {
+    const char *who = "dspk_i8_pack";
+    int rc = check_i8_shape(n, k, count, who);
+    if (rc) return rc;
+    if (codes == nullptr || ldc < k) return fail(DSPK_EINVAL, "%s: codes NULL, or ldc=%lld < k=%d", who, (long long)ldc, k);
+    const size_t need = dspk_i8_tiled_bytes(n, k, count);
+    if (!pointer(tiles, 256) || need == 0 || tiles_bytes < need)
+        return fail(DSPK_EINVAL, "%s: tiles of %zu bytes required (256-byte aligned)", who, need);
+    const dspk::I8PackArgs A = {codes, ldc, n, k, (int32_t)tiles_of(n), (int32_t)steps_of(k), tiles_of(n) * count, tiles};
+    return launch_result(dspk::launch_i8_pack(A, (hipStream_t)stream), who);
+}
+
+size_t dspk_i8_workspace_bytes(int32_t n, int32_t k, int32_t m) {
+    if (check_i8_shape(n, k, 1, "dspk_i8_workspace_bytes") || m < 1) return 0;
+    return dspk::i8_plan(n, k, m, dspk::device_cus()).ws_bytes;
+}
+
+int dspk_i8_gemm(const dspk_i8_weight *w, const int8_t *x, int64_t ldx, const float *x_scales, int32_t m, void *y,
+                 int32_t y_dtype, int64_t ldy, void *workspace, size_t ws_bytes, void *stream) {
+    const char *who = "dspk_i8_gemm";
+    int rc = check_i8_weight(w, "w", who);
+    if (rc) return rc;
+    if (w->count != 1) return fail(DSPK_EINVAL, "%s: a weight of count=%d (must be 1)", who, w->count);
+    if (m < 0) return fail(DSPK_EINVAL, "%s: m=%d must be >= 0", who, m);
+    if ((rc = check_dtype(y_dtype, "y", who))) return rc;
+    if (m == 0) return ok();
+    if ((rc = check_codes(x, ldx, w->k, x_scales, "x", who)) || (rc = check_y(y, ldy, w->n, who))) return rc;
+    const dspk::I8Plan p = dspk::i8_plan(w->n, w->k, m, dspk::device_cus());
+    if (!p.fits) return fail(DSPK_EUNSUPPORTED, "%s: n=%d, m=%d: too many tiles for one launch", who, w->n, m);
+    if (workspace != nullptr && (rc = check_workspace(workspace, ws_bytes, p.ws_bytes, who))) return rc;
+    dspk::I8GemmArgs A{};
+    A.tiles = (const char *)w->tiles;
+    A.w_scales = w->scales;
+    A.x = x;
+    A.x_scales = x_scales;
+    A.y = y;
+    A.ldx = ldx;
+    A.ldy = ldy;
+    A.m = m;
+    A.n = w->n;
+    A.k = w->k;
+    A.tiles_n = (int32_t)tiles_of(w->n);
+    A.steps = (int32_t)steps_of(w->k);
+    A.y_bf16 = y_dtype == DSPK_BF16;
+    A.vec = ldy % 4 == 0 && aligned(y, A.y_bf16 ? 8 : 16);
+    return launch_result(dspk::launch_i8_gemm(A, p, (hipStream_t)stream), who);
+}
+
+size_t dspk_moe_workspace_bytes(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k) {
+    const char *who = "dspk_moe_workspace_bytes";
+    if (check_moe(m, experts, top_k, who) || m < 1 || check_i8_shape(inter, hidden, experts, who) ||
+        check_i8_shape(hidden, inter, experts, who) || hidden > dspk::kMoeMaxHidden)
+        return 0;
+    return dspk::moe_plan(hidden, inter, experts, m, top_k).ws_bytes;
+}
+
+int dspk_moe_route(const uint16_t *x, int64_t ldx, const uint16_t *router, int64_t ldr, int32_t m, int32_t k,
+                   int32_t experts, int32_t top_k, int32_t normalize, int32_t *ids, float *weights, float *scores,
+                   int64_t lds, void *workspace, size_t ws_bytes, void *stream) {
+    const char *who = "dspk_moe_route";
+    int rc = check_moe(m, experts, top_k, who);
+    if (rc) return rc;
+    if (top_k > experts) return fail(DSPK_EINVAL, "%s: top_k=%d of %d experts", who, top_k, experts);
+    if (k < 1) return fail(DSPK_EINVAL, "%s: k=%d must be >= 1", who, k);
+    if (normalize != 0 && normalize != 1) return fail(DSPK_EINVAL, "%s: normalize=%d (0 or 1)", who, normalize);
+    if (m == 0) return ok();
+    if ((rc = check_rows(x, ldx, k, DSPK_BF16, "x", who)) || (rc = check_rows(router, ldr, k, DSPK_BF16, "router", who)))
+        return rc;
+    if (!pointer(ids, 4) || !pointer(weights, 4)) return fail(DSPK_EINVAL, "%s: ids or weights NULL or misaligned", who);
+    if (!aligned(scores, 4) || (scores != nullptr && lds < experts))
+        return fail(DSPK_EINVAL, "%s: scores misaligned, or lds=%lld < experts=%d", who, (long long)lds, experts);
+    const size_t at = dspk::moe_plan(1, 1, experts, m, top_k).off_scores, need = at + (size_t)m * experts * sizeof(float);
+    if ((rc = check_workspace(workspace, ws_bytes, need, who))) return rc;
+    dspk::RouteArgs A{};
+    A.x = x;
+    A.ldx = ldx;
+    A.router = router;
+    A.ldr = ldr;
+    A.m = m;
+    A.k = k;
+    A.experts = experts;
+    A.top_k = top_k;
+    A.normalize = normalize;
+    A.ids = ids;
+    A.weights = weights;
+    A.scores = scores;
+    A.lds = lds;
+    A.part = (float *)((char *)workspace + at);
+    A.counter = (uint32_t *)workspace;
+    return launch_result(dspk::launch_moe_route(A, (hipStream_t)stream), who);
+}
+
+int dspk_moe_mlp(const dspk_i8_weight *gate, const dspk_i8_weight *up, const dspk_i8_weight *down, const int8_t *x,
+                 int64_t ldx, const float *x_scales, int32_t m, const int32_t *ids, const float *weights, int32_t top_k,
+                 void *y, int32_t y_dtype, int64_t ldy, void *workspace, size_t ws_bytes, void *stream) {
+    const char *who = "dspk_moe_mlp";
+    int rc = check_i8_weight(gate, "gate", who);
+    if (rc || (rc = check_i8_weight(up, "up", who)) || (rc = check_i8_weight(down, "down", who))) return rc;
+    const int32_t hidden = gate->k, inter = gate->n, experts = gate->count;
+    if ((rc = check_moe(m, experts, top_k, who))) return rc;
+    if (up->n != inter || up->k != hidden || up->count != experts || down->n != hidden || down->k != inter ||
+        down->count != experts)
+        return fail(DSPK_EINVAL, "%s: gate, up and down of different sizes", who);
+    if (hidden > dspk::kMoeMaxHidden)
+        return fail(DSPK_EUNSUPPORTED, "%s: hidden=%d (at most %d)", who, hidden, dspk::kMoeMaxHidden);
+    if ((rc = check_dtype(y_dtype, "y", who))) return rc;
+    if (m == 0) return ok();
+    if ((rc = check_codes(x, ldx, hidden, x_scales, "x", who)) || (rc = check_y(y, ldy, hidden, who))) return rc;
+    if (!pointer(ids, 4) || !pointer(weights, 4)) return fail(DSPK_EINVAL, "%s: ids or weights NULL or misaligned", who);
+    const dspk::MoePlan p = dspk::moe_plan(hidden, inter, experts, m, top_k);
+    if ((rc = check_workspace(workspace, ws_bytes, p.ws_bytes, who))) return rc;
+    dspk::MoeArgs A{};
+    A.gate = (const char *)gate->tiles;
+    A.up = (const char *)up->tiles;
+    A.down = (const char *)down->tiles;
+    A.gate_scales = gate->scales;
+    A.up_scales = up->scales;
+    A.down_scales = down->scales;
+    A.x = x;
+    A.ldx = ldx;
+    A.x_scales = x_scales;
+    A.m = m;
+    A.hidden = hidden;
+    A.inter = inter;
+    A.experts = experts;
+    A.top_k = top_k;
+    A.ids = ids;
+    A.weights = weights;
+    A.y = y;
+    A.ldy = ldy;
+    A.y_bf16 = y_dtype == DSPK_BF16;
+    char *ws = (char *)workspace;
+    A.ldh = p.ldh;
+    A.ldp = p.ldp;
+    A.h = (float *)(ws + p.off_h);
+    A.part = (float *)(ws + p.off_part);
+    A.top = (uint32_t *)(ws + dspk::kMoeTop);
+    A.ctr = (uint32_t *)(ws + dspk::kMoeCtr);
+    A.done = (uint32_t *)ws + 1;
+    return launch_result(dspk::launch_moe_mlp(A, (hipStream_t)stream), who);
+}
+
+}  // extern "C"

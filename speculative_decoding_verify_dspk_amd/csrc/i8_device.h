@@ -1,0 +1,106 @@
+// Device helpers of the 8-bit integer side.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "i8_internal.h"
+
+namespace dspk {
+namespace i8 {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ uint16_t to_bf16(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+__device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
+    return (uint32_t)to_bf16(lo) | ((uint32_t)to_bf16(hi) << 16);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// A row's scale and the factor of its codes, from its largest magnitude (as
+// bits, NaN on top): scale = top / 127, code = x * (127 / top) rounded half to even.
+// held: false for a row that reads as NaN (scale NaN) or as zeros (below 4e-37,
+// where 127 / top is no number), whose codes are zeros.
+struct Step8 {
+    float scale, inv;
+    bool held;
+};
+__device__ __forceinline__ Step8 step8(uint32_t top) {
+    Step8 s;
+    const float t = __uint_as_float(top);
+    s.inv = 127.f / t;
+    s.held = top < 0x7f800000u && s.inv < __uint_as_float(0x7f800000u);
+    s.scale = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : s.held ? t / 127.f : 0.f;
+    return s;
+}
+__device__ __forceinline__ uint32_t code8(float x, const Step8 &s) {
+    return s.held ? (uint32_t)(int)rintf(x * s.inv) & 0xffu : 0u;
+}
+__device__ __forceinline__ uint32_t codes8(float a, float b, float c, float d, const Step8 &s) {
+    return code8(a, s) | code8(b, s) << 8 | code8(c, s) << 16 | code8(d, s) << 24;
+}
+
+// x / (1 + exp(-x)); exp overflows to infinity far below zero, which leaves -0.
+__device__ __forceinline__ float silu(float x) { return x / (1.f + expf(-x)); }
+
+// Data that other workgroups of the same launch read goes by device-scope accesses,
+// which reach them without a cache flush; the writer waits for them before it counts
+// itself in.
+__device__ __forceinline__ void share(float *p, float a, float b) {
+    __hip_atomic_store((unsigned long long *)p,
+                       (unsigned long long)__float_as_uint(a) | (unsigned long long)__float_as_uint(b) << 32,
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 shared2(const float *p) {
+    const unsigned long long v =
+        __hip_atomic_load((unsigned long long *)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+// Counts a workgroup in after what its threads shared; true in the last of `of`.
+// Every thread of the workgroup calls it.  The counter is left at zero by the last.
+__device__ __forceinline__ bool last_to_arrive(uint32_t *counter, uint32_t of) {
+    __shared__ uint32_t ticket;
+    __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));          // vmcnt(0): this wave's data is performed
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        ticket = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (ticket == of - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    return ticket == of - 1;
+}
+
+__device__ __forceinline__ i32x4 mfma64(i32x4 a, i32x4 b, i32x4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+// Four neighbouring columns of a row of y.
+template <bool BF16>
+__device__ __forceinline__ void store4(void *y, int64_t at, int32_t col, int32_t n, bool vec, const float (&v)[4]) {
+    if (vec && col + 4 <= n) {
+        if constexpr (BF16)
+            *(u32x2 *)((uint16_t *)y + at) = u32x2{to_bf16_pair(v[0], v[1]), to_bf16_pair(v[2], v[3])};
+        else
+            *(f32x4 *)((float *)y + at) = f32x4{v[0], v[1], v[2], v[3]};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (col + e >= n) break;
+        if constexpr (BF16)
+            ((uint16_t *)y)[at + e] = to_bf16(v[e]);
+        else
+            ((float *)y)[at + e] = v[e];
+    }
+}
+
+}  // namespace i8
+}  // namespace dspk

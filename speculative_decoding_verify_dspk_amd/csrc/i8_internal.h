@@ -1,0 +1,132 @@
+// Internal declarations of the 8-bit integer side of a layer (row kernels,
+// products of 8-bit rows with 8-bit weights, expert layers), shared by its C-ABI
+// layer and kernels.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace dspk {
+
+// ---- rows: norm, activation, quantising -------------------------------------
+enum RowOp : int { kRowNorm = 0, kRowSilu = 1, kRowPlain = 2 };
+struct RowArgs {
+    const void *x;                  // [m][ldx]; norm: or NULL; silu: gate
+    const void *r;                  // norm: residual, or NULL; silu: up
+    void *r_out;                    // norm: [m][ldro] of r's type, or NULL
+    int64_t ldx, ldr, ldro;
+    int32_t x_f32, r_f32;           // element types: fp32, else bf16
+    const float *w;                 // norm: [n], or NULL
+    float eps;
+    int32_t m, n;
+    uint16_t *rows;                 // outputs; see dspk_rows_out
+    int64_t ld;
+    int8_t *codes;
+    int64_t ldc;
+    float *scales;
+};
+constexpr int kRowPiece = 8;        // columns of a lane's piece
+constexpr int kRowMostThreads = 1024;
+hipError_t launch_rows(RowOp op, const RowArgs &a, int cus, hipStream_t s);
+
+struct I8ReadArgs {
+    const int8_t *codes;
+    int64_t ldc;
+    const float *scales;
+    int32_t m, n;
+    void *y;
+    int64_t ldy;
+    int32_t y_f32;
+};
+hipError_t launch_i8_read(const I8ReadArgs &a, hipStream_t s);
+
+// ---- weights and products ----------------------------------------------------
+// A weight is fragments of 16 columns x 64 K, 1 KiB each, K fastest: lane l of a
+// wave holds column l % 16, K 16 (l / 16) .. + 15, its operand of a 16x16x64
+// matrix instruction.
+constexpr int kI8Cols = 16, kI8K = 64, kI8Frag = kI8Cols * kI8K;
+struct I8PackArgs {
+    const int8_t *codes;
+    int64_t ldc;
+    int32_t n, k, tiles_n, steps;   // tiles of 16 columns of one weight, fragments of a tile
+    int64_t tiles;                  // of all weights
+    void *out;
+};
+hipError_t launch_i8_pack(const I8PackArgs &a, hipStream_t s);
+
+struct I8GemmArgs {
+    const char *tiles;
+    const float *w_scales;
+    const int8_t *x;
+    const float *x_scales;
+    void *y;
+    int64_t ldx, ldy;
+    int32_t m, n, k;
+    int32_t tiles_n, steps;         // tiles of 16 columns, fragments of a tile: ceil(k / 64)
+    int32_t y_bf16;
+    int32_t vec;                    // four neighbouring columns of y are stored at once
+};
+// Shape of a launch; see i8_gemm.hip.
+struct I8Plan {
+    int32_t row_tiles;              // 16-row tiles of a workgroup
+    int32_t waves;
+    int64_t grid_x, grid_y;
+    bool fits;
+    size_t ws_bytes;
+};
+I8Plan i8_plan(int32_t n, int32_t k, int32_t m, int cus);
+hipError_t launch_i8_gemm(const I8GemmArgs &a, const I8Plan &p, hipStream_t s);
+
+// ---- expert layers -----------------------------------------------------------
+constexpr int kMoeMaxRows = 64, kMoeMaxExperts = 1024, kMoeMaxTop = 32;
+constexpr int kMoeMaxSlots = kMoeMaxRows * kMoeMaxTop;
+constexpr int kMoeMaxHidden = 65536;
+constexpr int kMoeCols = 64;        // columns of a down workgroup
+// Workspace: what has to be zero between calls lies at fixed places in front, so
+// that calls of any sizes share one buffer:
+//   [0, 256)   arrivals of the router's workgroups, of the down columns
+//   kMoeTop    largest magnitudes of h's rows, as bits [kMoeMaxSlots]
+//   kMoeCtr    arrivals at each block of kMoeCols columns
+// then the router's scores, h and the down products, each written before it is read.
+constexpr size_t kMoeTop = 256, kMoeCtr = kMoeTop + 4 * kMoeMaxSlots,
+                 kMoeHead = kMoeCtr + 4 * (kMoeMaxHidden / kMoeCols);
+struct MoePlan {
+    int64_t ldh, ldp;               // floats of a row of h, of a down product
+    size_t off_scores, off_h, off_part, ws_bytes;
+};
+MoePlan moe_plan(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k);
+
+struct RouteArgs {
+    const uint16_t *x, *router;
+    int64_t ldx, ldr, lds;
+    int32_t m, k, experts, top_k, normalize;
+    int32_t *ids;
+    float *weights, *scores;        // scores: or NULL
+    float *part;                    // [m][experts] in the workspace
+    uint32_t *counter;
+};
+hipError_t launch_moe_route(const RouteArgs &a, hipStream_t s);
+
+struct MoeArgs {
+    const char *gate, *up, *down;
+    const float *gate_scales, *up_scales, *down_scales;
+    const int8_t *x;
+    const float *x_scales;
+    int64_t ldx, ldy, ldh, ldp;
+    int32_t m, hidden, inter, experts, top_k;
+    const int32_t *ids;
+    const float *weights;
+    void *y;
+    int32_t y_bf16;
+    float *h, *part;                // [m * top_k][ldh], [m * top_k][ldp]
+    uint32_t *top;                  // [m * top_k]
+    uint32_t *ctr, *done;           // arrivals per column block, of column blocks
+};
+hipError_t launch_moe_mlp(const MoeArgs &a, hipStream_t s);
+
+int device_cus();
+// Stores the thread's error message (dspk_last_error) and returns `code`.
+int set_error(int code, const char *msg);
+
+}  // namespace dspk
