@@ -808,7 +808,8 @@ int dspk_i8_read(const int8_t *codes, int64_t ldc, const float *scales, int32_t 
  *
  *   tiles  : device memory of dspk_i8_tiled_bytes(n, k, count) bytes, 256-byte
  *            aligned, written by dspk_i8_pack; weight g's byte of (column c, K r)
- *            is at [g][c / 16][r / 64][r % 64 / 16][c % 16][r % 16], zero past n and k;
+ *            is at [g][c / 16][r / 64][r % 64 / 16][c % 16][r % 16], with k and n filled up
+ *            by zeros to multiples of 128 and 16;
  *   scales : float [count][n], w = scale * code.
  */
 typedef struct dspk_i8_weight {
@@ -845,8 +846,8 @@ int dspk_i8_pack(const int8_t *codes, int64_t ldc, int32_t n, int32_t k, int32_t
  *              calls ordered on one stream.  With it, calls with few columns and
  *              many rows split their sums over several workgroups (the result is
  *              the same).
- * Errors: DSPK_EINVAL, DSPK_EUNSUPPORTED (k > DSPK_I8_MAX_K, more tiles than one
- * launch numbers), DSPK_EDEVICE.
+ * Errors: DSPK_EINVAL, DSPK_EUNSUPPORTED (k > DSPK_I8_MAX_K, ldx > 2^24, more tiles
+ * than one launch numbers), DSPK_EDEVICE.
  */
 int dspk_i8_gemm(const dspk_i8_weight *w, const int8_t *x, int64_t ldx, const float *x_scales, int32_t m, void *y,
                  int32_t y_dtype, int64_t ldy, void *workspace, size_t ws_bytes, void *stream);

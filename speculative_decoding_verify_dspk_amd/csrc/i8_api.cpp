@@ -10,18 +10,100 @@
 
 namespace dspk {
 
-I8Plan i8_plan(int32_t n, int32_t k, int32_t m, int cus) {
-    (void)cus;
+// Which kernel a product takes.
+//
+// Streams read each weight fragment once into registers and all of x for every 16 or
+// 32 columns: best while x is small beside the weight.  Tiles stage both through
+// LDS, so x is read once per 64 to 256 columns.  Measured (us, weights in memory;
+// tile splits in brackets), n x k:
+//            19456x2560       2560x9728        34816x5120       5120x17408
+//   rows   stream  tile     stream  tile     stream  tile     stream  tile
+//      1    10.0  13.0        6.9   9.6 [4]   29.8  40.7       15.9  20.4 [6]
+//     16    11.9  13.9       10.0   9.8 [4]   34.6  41.2       20.6  20.9 [6]
+//     17    12.3  14.2       10.2  10.0 [4]   34.9  41.7       22.5  21.2 [6]
+//     32    15.7  15.1       13.8  10.1 [4]   46.7  42.4       30.3  21.3 [6]
+//     33    16.5  21.8       15.1  12.1 [6]   50.2  52.8       30.7  24.2 [3]
+//     64    23.6  24.1       22.6  12.5 [4]   67.9  58.5       45.7  25.8 [3]
+// Two column tiles per stream workgroup where there are more tiles than CUs (16
+// rows, 384 tiles: 6.4 -> 5.8 us), one where there are not (160 tiles: 6.2 / 5.3).
+//
+// Tiles and their K splits are chosen by an estimate fitted to measured launches: a
+// workgroup's start and end take 4 us, a stage of 128 K takes the longer of the time
+// that all resident workgroups' loads need of the caches (16.5 TB/s) and the stage's
+// own time (1.4 times that for two on a CU), a split costs 2 us and .3 us per MB of
+// sums that change hands.  E.g. 301 rows of 6144x4096: 64x128 18.4 us (estimated 18.4),
+// split in two 19.7 (22.2), 128x128 in three 24.3 (26.6); 512 rows of 2560x9728: 64x128
+// in three 24.2 (28.8), 128x128 in three 29.7 (31.0); 1024 rows of 19456x2560: 256x256
+// 69.2 (64), 128x128 83.2 (79).
+I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
     I8Plan p{};
-    const int64_t steps = ((int64_t)k + kI8K - 1) / kI8K;
-    p.row_tiles = m <= 16 ? 1 : m <= 32 ? 2 : 4;
-    const int64_t waves = (steps + 7) / 8;
-    p.waves = (int32_t)(waves > 16 ? 16 : waves);
-    p.grid_x = ((int64_t)n + kI8Cols - 1) / kI8Cols;
-    p.grid_y = ((int64_t)m + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
-    // threads of the grid's first dimension in 32 bits, workgroups of its second in 16
-    p.fits = p.grid_x * 64 * p.waves <= UINT32_MAX && p.grid_y <= 65535;
-    p.ws_bytes = 0;
+    const int64_t steps = i8_steps(k), stages = steps / 2, tiles = i8_tiles(n);
+    const auto over = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const int64_t weight = (int64_t)n * k;
+    const bool wide = tiles > cus, few = tiles <= cus + cus / 4 && weight >= 24 << 20;
+    p.splits = 1;
+    // few: long sums over few columns, which streams read x too often for
+    const bool stream = m <= 16 || (m <= 32 && !few && (m <= 24 || weight < 24 << 20)) ||
+                        (m > 32 && m <= 48 && !few) || (m <= 64 && weight < 2 << 20);
+    if (stream) {
+        p.kind = m <= 16 ? (wide ? kI8Stream16x2 : kI8Stream16x1)
+                 : m <= 32 ? (wide ? kI8Stream32x2 : kI8Stream32x1) : (wide ? kI8Stream64x2 : kI8Stream64x1);
+        // 4 to 8 waves, so that their rings' last turns are full (40 fragments, rings
+        // of 4: 5 waves 11.9 us, 4 12.7)
+        const int ring = p.kind == kI8Stream16x1 ? 8 : p.kind == kI8Stream64x2 ? 2 : 4;
+        int64_t least = INT64_MAX;
+        for (int w = 4; w <= 8; ++w) {
+            const int64_t turns = over(steps, (int64_t)w * ring) * w * ring;
+            if (turns < least) least = turns, p.waves = w;
+        }
+        p.groups = over(tiles, wide ? 2 : 1);
+        p.fits = p.groups * 64 * p.waves <= UINT32_MAX;
+        return p;
+    }
+    struct Shape {
+        I8Kind kind;
+        int rows, cols;
+        double kb, own;             // of a stage: KB loaded, us alone on a CU
+    };
+    static const Shape shapes[] = {{kI8Tile32x64, 32, 64, 12, .25}, {kI8Tile64x64, 64, 64, 16, .26},
+                                   {kI8Tile64x128, 64, 128, 24, .45}, {kI8Tile128x128, 128, 128, 32, .8}};
+    double best = 1e300;
+    for (const Shape &c : shapes) {
+        if (m <= 32 ? c.rows != 32 : c.rows == 32) continue;
+        const int64_t of = over(m, c.rows) * over(n, c.cols);
+        for (int s = 1; s <= 8; ++s) {
+            if (s > 1 && (!split || stages < 4 * s || of * s > 4 * cus || of > kI8MaxSplitTiles)) break;
+            const int64_t all = of * s, at_once = all < 2 * cus ? all : 2 * cus;
+            const double loads = at_once * c.kb * 1.024e-3 / 16.5 * (256. / cus);
+            const double stage = at_once > cus ? 1.4 * c.own : c.own;
+            const double us = (double)over(all, 2 * cus) * (4 + (double)stages / s * (loads > stage ? loads : stage)) +
+                              (s > 1 ? 2 + .3e-6 * 4 * all * c.rows * c.cols : 0);
+            if (us >= best) continue;
+            best = us;
+            p.kind = c.kind;
+            p.splits = s;
+            p.groups = of;
+            p.off_part = p.ws_bytes = 0;
+            if (s > 1) {
+                p.off_part = kI8MaxSplitTiles * sizeof(uint32_t);
+                p.ws_bytes = p.off_part + (size_t)all * c.rows * c.cols * sizeof(int32_t);
+            }
+        }
+    }
+    // 256 x 256: whole rounds of one workgroup per CU, then the rest in quarters, if that
+    // is the shorter
+    const int64_t big = over(m, 256) * over(n, 256), rest = big % cus;
+    const double whole = 5 + 2.1 * stages, quarters = (double)over(4 * rest, cus) * (4 + .65 * stages);
+    const bool cut = rest != 0 && quarters < whole;
+    const double us = (double)(cut ? big / cus : over(big, cus)) * whole + (cut ? quarters : 0);
+    if (m > 64 && us < best) {
+        p = I8Plan{};
+        p.kind = kI8Tile256x256;
+        p.splits = 1;
+        p.whole = cut ? big - rest : big;
+        p.groups = p.whole + 4 * (big - p.whole);
+    }
+    p.fits = p.groups * 512 <= UINT32_MAX;
     return p;
 }
 
@@ -130,9 +212,6 @@ int check_i8_shape(int32_t n, int32_t k, int32_t count, const char *who) {
     if (k > DSPK_I8_MAX_K) return fail(DSPK_EUNSUPPORTED, "%s: k=%d (at most %d)", who, k, DSPK_I8_MAX_K);
     return DSPK_OK;
 }
-
-int64_t tiles_of(int32_t n) { return ((int64_t)n + dspk::kI8Cols - 1) / dspk::kI8Cols; }
-int64_t steps_of(int32_t k) { return ((int64_t)k + dspk::kI8K - 1) / dspk::kI8K; }
 
 int check_i8_weight(const dspk_i8_weight *w, const char *name, const char *who) {
     if (w == nullptr) return fail(DSPK_EINVAL, "%s: %s is NULL", who, name);
@@ -252,7 +331,7 @@ int dspk_i8_read(const int8_t *codes, int64_t ldc, const float *scales, int32_t 
 
 size_t dspk_i8_tiled_bytes(int32_t n, int32_t k, int32_t count) {
     if (check_i8_shape(n, k, count, "dspk_i8_tiled_bytes")) return 0;
-    const size_t one = (size_t)tiles_of(n) * steps_of(k) * dspk::kI8Frag;      // < 2^49
+    const size_t one = (size_t)dspk::i8_tiles(n) * dspk::i8_steps(k) * dspk::kI8Frag;      // < 2^49
     return one > (size_t)(SIZE_MAX / count) ? 0 : one * count;
 }
 
@@ -265,13 +344,13 @@ int dspk_i8_pack(const int8_t *codes, int64_t ldc, int32_t n, int32_t k, int32_t
     const size_t need = dspk_i8_tiled_bytes(n, k, count);
     if (!pointer(tiles, 256) || need == 0 || tiles_bytes < need)
         return fail(DSPK_EINVAL, "%s: tiles of %zu bytes required (256-byte aligned)", who, need);
-    const dspk::I8PackArgs A = {codes, ldc, n, k, (int32_t)tiles_of(n), (int32_t)steps_of(k), tiles_of(n) * count, tiles};
+    const dspk::I8PackArgs A = {codes, ldc, n, k, (int32_t)dspk::i8_tiles(n), (int32_t)dspk::i8_steps(k), dspk::i8_tiles(n) * count, tiles};
     return launch_result(dspk::launch_i8_pack(A, (hipStream_t)stream), who);
 }
 
 size_t dspk_i8_workspace_bytes(int32_t n, int32_t k, int32_t m) {
     if (check_i8_shape(n, k, 1, "dspk_i8_workspace_bytes") || m < 1) return 0;
-    return dspk::i8_plan(n, k, m, dspk::device_cus()).ws_bytes;
+    return dspk::i8_plan(n, k, m, true, dspk::device_cus()).ws_bytes;
 }
 
 int dspk_i8_gemm(const dspk_i8_weight *w, const int8_t *x, int64_t ldx, const float *x_scales, int32_t m, void *y,
@@ -284,7 +363,9 @@ int dspk_i8_gemm(const dspk_i8_weight *w, const int8_t *x, int64_t ldx, const fl
     if ((rc = check_dtype(y_dtype, "y", who))) return rc;
     if (m == 0) return ok();
     if ((rc = check_codes(x, ldx, w->k, x_scales, "x", who)) || (rc = check_y(y, ldy, w->n, who))) return rc;
-    const dspk::I8Plan p = dspk::i8_plan(w->n, w->k, m, dspk::device_cus());
+    // the rows of a tile are numbered in 32 bits
+    if (ldx > 1 << 24) return fail(DSPK_EUNSUPPORTED, "%s: ldx=%lld (at most 2^24)", who, (long long)ldx);
+    const dspk::I8Plan p = dspk::i8_plan(w->n, w->k, m, workspace != nullptr, dspk::device_cus());
     if (!p.fits) return fail(DSPK_EUNSUPPORTED, "%s: n=%d, m=%d: too many tiles for one launch", who, w->n, m);
     if (workspace != nullptr && (rc = check_workspace(workspace, ws_bytes, p.ws_bytes, who))) return rc;
     dspk::I8GemmArgs A{};
@@ -298,10 +379,14 @@ int dspk_i8_gemm(const dspk_i8_weight *w, const int8_t *x, int64_t ldx, const fl
     A.m = m;
     A.n = w->n;
     A.k = w->k;
-    A.tiles_n = (int32_t)tiles_of(w->n);
-    A.steps = (int32_t)steps_of(w->k);
+    A.tiles_n = (int32_t)dspk::i8_tiles(w->n);
+    A.steps = (int32_t)dspk::i8_steps(w->k);
     A.y_bf16 = y_dtype == DSPK_BF16;
     A.vec = ldy % 4 == 0 && aligned(y, A.y_bf16 ? 8 : 16);
+    A.whole = (int32_t)p.whole;
+    A.splits = p.splits;
+    A.ctr = (uint32_t *)workspace;
+    A.part = (int32_t *)((char *)workspace + p.off_part);
     return launch_result(dspk::launch_i8_gemm(A, p, (hipStream_t)stream), who);
 }
 

@@ -59,6 +59,15 @@ __device__ __forceinline__ void share(float *p, float a, float b) {
                        (unsigned long long)__float_as_uint(a) | (unsigned long long)__float_as_uint(b) << 32,
                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ void share(int32_t *p, int32_t a, int32_t b) {
+    __hip_atomic_store((unsigned long long *)p, (unsigned long long)(uint32_t)a | (unsigned long long)(uint32_t)b << 32,
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ int2 shared2(const int32_t *p) {
+    const unsigned long long v =
+        __hip_atomic_load((unsigned long long *)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return make_int2((int32_t)(uint32_t)v, (int32_t)(uint32_t)(v >> 32));
+}
 __device__ __forceinline__ float2 shared2(const float *p) {
     const unsigned long long v =
         __hip_atomic_load((unsigned long long *)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

@@ -42,10 +42,12 @@ struct I8ReadArgs {
 hipError_t launch_i8_read(const I8ReadArgs &a, hipStream_t s);
 
 // ---- weights and products ----------------------------------------------------
-// A weight is fragments of 16 columns x 64 K, 1 KiB each, K fastest: lane l of a
-// wave holds column l % 16, K 16 (l / 16) .. + 15, its operand of a 16x16x64
-// matrix instruction.
+// A weight is fragments of 16 columns x 64 K, 1 KiB each, K fastest, an even number
+// of them (K is filled up with zeros): lane l of a wave holds column l % 16, K
+// 16 (l / 16) .. + 15, its operand of a 16x16x64 matrix instruction.
 constexpr int kI8Cols = 16, kI8K = 64, kI8Frag = kI8Cols * kI8K;
+constexpr int64_t i8_tiles(int64_t n) { return (n + kI8Cols - 1) / kI8Cols; }
+constexpr int64_t i8_steps(int64_t k) { return (k + 2 * kI8K - 1) / (2 * kI8K) * 2; }
 struct I8PackArgs {
     const int8_t *codes;
     int64_t ldc;
@@ -63,19 +65,30 @@ struct I8GemmArgs {
     void *y;
     int64_t ldx, ldy;
     int32_t m, n, k;
-    int32_t tiles_n, steps;         // tiles of 16 columns, fragments of a tile: ceil(k / 64)
+    int32_t tiles_n, steps;         // tiles of 16 columns, fragments of a tile
     int32_t y_bf16;
     int32_t vec;                    // four neighbouring columns of y are stored at once
+    int32_t whole;                  // 256 x 256 tiles that are not cut into four
+    int32_t splits;                 // of K; > 1 needs the two regions below
+    int32_t *part;                  // sums [tile][split][wave][..]
+    uint32_t *ctr;                  // arrivals [tile], zero between calls
 };
-// Shape of a launch; see i8_gemm.hip.
+// Shape of a launch; see i8_gemm.hip.  Stream: rows x 16-column tiles of a workgroup;
+// tile: rows x columns.
+enum I8Kind : int {
+    kI8Stream16x1, kI8Stream16x2, kI8Stream32x1, kI8Stream32x2, kI8Stream64x1, kI8Stream64x2,
+    kI8Tile32x64, kI8Tile64x64, kI8Tile64x128, kI8Tile128x128, kI8Tile256x256
+};
 struct I8Plan {
-    int32_t row_tiles;              // 16-row tiles of a workgroup
-    int32_t waves;
-    int64_t grid_x, grid_y;
+    I8Kind kind;
+    int32_t waves;                  // stream: of a workgroup
+    int32_t splits;                 // tile: of K
+    int64_t whole, groups;          // 256 x 256 tiles that are not cut, workgroups
     bool fits;
-    size_t ws_bytes;
+    size_t off_part, ws_bytes;      // workspace: arrivals, then sums
 };
-I8Plan i8_plan(int32_t n, int32_t k, int32_t m, int cus);
+constexpr int kI8MaxSplitTiles = 1024;
+I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus);
 hipError_t launch_i8_gemm(const I8GemmArgs &a, const I8Plan &p, hipStream_t s);
 
 // ---- expert layers -----------------------------------------------------------

@@ -255,7 +255,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(const MoeArgs A) {
     int active;
     const int e = find(S, A, blockIdx.y, active);
     if (e < 0) return;
-    const int steps = (A.hidden + kI8K - 1) / kI8K, tiles = gridDim.x;
+    const int steps = (int)i8_steps(A.hidden), tiles = gridDim.x;
     const int64_t tile = ((int64_t)e * tiles + blockIdx.x) * steps * kI8Frag + 16 * (threadIdx.x & 63);
     const float *gs = A.gate_scales + (int64_t)e * A.inter, *us = A.up_scales + (int64_t)e * A.inter;
     for (int base = 0; base < S.count; base += 32) {
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(const MoeArgs A) 
     const int e = find(S, A, blockIdx.y, active);
     // with no expert chosen at all the first row of workgroups still writes y
     if (e < 0 && !(active == 0 && blockIdx.y == 0)) return;
-    const int steps = (A.inter + kI8K - 1) / kI8K, tiles = (A.hidden + kI8Cols - 1) / kI8Cols;
+    const int steps = (int)i8_steps(A.inter), tiles = (int)i8_tiles(A.hidden);
     if (e >= 0) {
         const int tile = blockIdx.x * (kMoeCols / kI8Cols) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const char *dt = A.down + ((int64_t)e * tiles + min(tile, tiles - 1)) * steps * kI8Frag + 16 * (threadIdx.x & 63);

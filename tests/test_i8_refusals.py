@@ -116,10 +116,10 @@ WEIGHT = [
 @pytest.mark.parametrize("bad,code,text", WEIGHT + [
     (dict(w="none"), EINVAL, "w is NULL"), (dict(count=2), EINVAL, "count=2"), (dict(m=-1), EINVAL, "m=-1"),
     (dict(x=None), EINVAL, "x must be"), (dict(x=P + 8), EINVAL, "x must be"), (dict(ldx=128), EINVAL, "of x"),
-    (dict(ldx=136), EINVAL, "leading dimension 136 of x"), (dict(xs=None), EINVAL, "the scales of x"),
+    (dict(ldx=136), EINVAL, "leading dimension 136 of x"), (dict(ldx=(1 << 24) + 16), EUNSUPPORTED, "ldx=16777232"), (dict(xs=None), EINVAL, "the scales of x"),
     (dict(y=None), EINVAL, "y NULL"), (dict(y=5 * P + 2), EINVAL, "y NULL or misaligned"), (dict(ldy=99), EINVAL, "ldy=99"),
     (dict(dt=2), EINVAL, "element type 2 of y"), (dict(ws=P + 64, wsb=1 << 30), EINVAL, "workspace of"),
-    (dict(n=(1 << 31) - 1, ldy=1 << 31, k=131071, ldx=131072), EUNSUPPORTED, "too many tiles"),
+    (dict(n=(1 << 31) - 1, m=1 << 20, ldy=1 << 31), EUNSUPPORTED, "too many tiles"),
 ])
 def test_product_says_what_it_refuses(lib, bad, code, text):
     assert _gemm(lib, m=0) == 0
@@ -143,7 +143,7 @@ def test_the_product_workspace_asked_for_is_the_one_that_is_checked(lib):
 ])
 def test_packing_says_what_it_refuses(lib, bad, code, text):
     need = lib.dspk_i8_tiled_bytes(100, 130, 2)
-    assert need == 2 * 7 * 3 * 1024 and lib.dspk_i8_tiled_bytes(1, 1, 1) == 1024
+    assert need == 2 * 7 * 4 * 1024 and lib.dspk_i8_tiled_bytes(1, 1, 1) == 2048
     a = dict(c=P + 1, ldc=130, n=100, k=130, count=2, t=2 * P, b=0)
     a.update(bad)
     got = lib.dspk_i8_pack(a["c"], a["ldc"], a["n"], a["k"], a["count"], a["t"], need + a["b"], None)
