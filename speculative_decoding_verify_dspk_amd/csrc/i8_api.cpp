@@ -107,16 +107,25 @@ I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
     return p;
 }
 
-MoePlan moe_plan(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k) {
+MoePlan moe_plan(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k, int cus) {
     MoePlan p{};
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     const size_t slots = (size_t)m * top_k;
     p.ldh = ((int64_t)inter + kI8Cols - 1) / kI8Cols * kI8Cols;
-    p.ldp = ((int64_t)hidden + kI8Cols - 1) / kI8Cols * kI8Cols;
     p.off_scores = up(kMoeHead);
     p.off_h = up(p.off_scores + (size_t)m * experts * sizeof(float));
-    p.off_part = up(p.off_h + slots * p.ldh * sizeof(float));
-    p.ws_bytes = up(p.off_part + slots * p.ldp * sizeof(float));
+    p.off_h8 = up(p.off_h + slots * p.ldh * sizeof(float));
+    p.off_h_scales = up(p.off_h8 + slots * p.ldh);
+    p.off_top = up(p.off_h_scales + slots * sizeof(float));
+    p.off_part = up(p.off_top + slots * (p.ldh / kI8Cols) * sizeof(uint32_t));
+    // Enough workgroups for the CUs, where one group of slots is all and each wave keeps
+    // two pieces of work or more (2048 columns, 8 / 48 slots of 768: one part 8.8 / 24.1
+    // us, two 9.4 / 19.4, four 13.3 / 22.9).
+    const int64_t tiles = i8_tiles(hidden), work = ((int64_t)slots < experts ? (int64_t)slots : experts) * ((i8_steps(inter) + 7) / 8);
+    p.parts = 1;
+    if (slots <= kMoeGroup && tiles <= kMoeSplitTiles)
+        while (p.parts < kMoeMaxParts && tiles * p.parts * 2 <= cus && work >= 32 * p.parts) p.parts *= 2;
+    p.ws_bytes = up(p.off_part + (p.parts > 1 ? tiles * p.parts * slots * 16 * sizeof(int32_t) : 0));
     return p;
 }
 
@@ -393,9 +402,9 @@ int dspk_i8_gemm(const dspk_i8_weight *w, const int8_t *x, int64_t ldx, const fl
 size_t dspk_moe_workspace_bytes(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k) {
     const char *who = "dspk_moe_workspace_bytes";
     if (check_moe(m, experts, top_k, who) || m < 1 || check_i8_shape(inter, hidden, experts, who) ||
-        check_i8_shape(hidden, inter, experts, who) || hidden > dspk::kMoeMaxHidden)
+        check_i8_shape(hidden, inter, experts, who))
         return 0;
-    return dspk::moe_plan(hidden, inter, experts, m, top_k).ws_bytes;
+    return dspk::moe_plan(hidden, inter, experts, m, top_k, dspk::device_cus()).ws_bytes;
 }
 
 int dspk_moe_route(const uint16_t *x, int64_t ldx, const uint16_t *router, int64_t ldr, int32_t m, int32_t k,
@@ -413,7 +422,7 @@ int dspk_moe_route(const uint16_t *x, int64_t ldx, const uint16_t *router, int64
     if (!pointer(ids, 4) || !pointer(weights, 4)) return fail(DSPK_EINVAL, "%s: ids or weights NULL or misaligned", who);
     if (!aligned(scores, 4) || (scores != nullptr && lds < experts))
         return fail(DSPK_EINVAL, "%s: scores misaligned, or lds=%lld < experts=%d", who, (long long)lds, experts);
-    const size_t at = dspk::moe_plan(1, 1, experts, m, top_k).off_scores, need = at + (size_t)m * experts * sizeof(float);
+    const size_t at = dspk::moe_plan(1, 1, experts, m, top_k, dspk::device_cus()).off_scores, need = at + (size_t)m * experts * sizeof(float);
     if ((rc = check_workspace(workspace, ws_bytes, need, who))) return rc;
     dspk::RouteArgs A{};
     A.x = x;
@@ -445,13 +454,11 @@ int dspk_moe_mlp(const dspk_i8_weight *gate, const dspk_i8_weight *up, const dsp
     if (up->n != inter || up->k != hidden || up->count != experts || down->n != hidden || down->k != inter ||
         down->count != experts)
         return fail(DSPK_EINVAL, "%s: gate, up and down of different sizes", who);
-    if (hidden > dspk::kMoeMaxHidden)
-        return fail(DSPK_EUNSUPPORTED, "%s: hidden=%d (at most %d)", who, hidden, dspk::kMoeMaxHidden);
     if ((rc = check_dtype(y_dtype, "y", who))) return rc;
     if (m == 0) return ok();
     if ((rc = check_codes(x, ldx, hidden, x_scales, "x", who)) || (rc = check_y(y, ldy, hidden, who))) return rc;
     if (!pointer(ids, 4) || !pointer(weights, 4)) return fail(DSPK_EINVAL, "%s: ids or weights NULL or misaligned", who);
-    const dspk::MoePlan p = dspk::moe_plan(hidden, inter, experts, m, top_k);
+    const dspk::MoePlan p = dspk::moe_plan(hidden, inter, experts, m, top_k, dspk::device_cus());
     if ((rc = check_workspace(workspace, ws_bytes, p.ws_bytes, who))) return rc;
     dspk::MoeArgs A{};
     A.gate = (const char *)gate->tiles;
@@ -475,12 +482,14 @@ int dspk_moe_mlp(const dspk_i8_weight *gate, const dspk_i8_weight *up, const dsp
     A.y_bf16 = y_dtype == DSPK_BF16;
     char *ws = (char *)workspace;
     A.ldh = p.ldh;
-    A.ldp = p.ldp;
     A.h = (float *)(ws + p.off_h);
-    A.part = (float *)(ws + p.off_part);
-    A.top = (uint32_t *)(ws + dspk::kMoeTop);
+    A.h8 = (int8_t *)(ws + p.off_h8);
+    A.h_scales = (float *)(ws + p.off_h_scales);
     A.ctr = (uint32_t *)(ws + dspk::kMoeCtr);
-    A.done = (uint32_t *)ws + 1;
+    A.top = (uint32_t *)(ws + p.off_top);
+    A.parts = p.parts;
+    A.part = (int32_t *)(ws + p.off_part);
+    A.down_ctr = (uint32_t *)(ws + dspk::kMoeDown);
     return launch_result(dspk::launch_moe_mlp(A, (hipStream_t)stream), who);
 }
 

@@ -48,6 +48,33 @@ __device__ __forceinline__ uint32_t codes8(float a, float b, float c, float d, c
     return code8(a, s) | code8(b, s) << 8 | code8(c, s) << 16 | code8(d, s) << 24;
 }
 
+// A value of every lane and that of the lane a DPP control names, 0 where there is none.
+template <int CTRL, int ROWS = 15>
+__device__ __forceinline__ uint32_t from_lane(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 15, false);
+}
+// The largest value of the wave, to every lane: within rows of 16 lanes, then from row
+// to row, by vector instructions alone (shuffles through LDS take ten times as long).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max(v, from_lane<0x111>(v));
+    v = max(v, from_lane<0x112>(v));
+    v = max(v, from_lane<0x114>(v));
+    v = max(v, from_lane<0x118>(v));
+    v = max(v, from_lane<0x142, 10>(v));
+    v = max(v, from_lane<0x143, 12>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// The sum of the wave, likewise.
+__device__ __forceinline__ float wave_sum(float v) {
+    v += __uint_as_float(from_lane<0x111>(__float_as_uint(v)));
+    v += __uint_as_float(from_lane<0x112>(__float_as_uint(v)));
+    v += __uint_as_float(from_lane<0x114>(__float_as_uint(v)));
+    v += __uint_as_float(from_lane<0x118>(__float_as_uint(v)));
+    v += __uint_as_float(from_lane<0x142, 10>(__float_as_uint(v)));
+    v += __uint_as_float(from_lane<0x143, 12>(__float_as_uint(v)));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
 // x / (1 + exp(-x)); exp overflows to infinity far below zero, which leaves -0.
 __device__ __forceinline__ float silu(float x) { return x / (1.f + expf(-x)); }
 

@@ -94,21 +94,22 @@ hipError_t launch_i8_gemm(const I8GemmArgs &a, const I8Plan &p, hipStream_t s);
 // ---- expert layers -----------------------------------------------------------
 constexpr int kMoeMaxRows = 64, kMoeMaxExperts = 1024, kMoeMaxTop = 32;
 constexpr int kMoeMaxSlots = kMoeMaxRows * kMoeMaxTop;
-constexpr int kMoeMaxHidden = 65536;
-constexpr int kMoeCols = 64;        // columns of a down workgroup
 // Workspace: what has to be zero between calls lies at fixed places in front, so
 // that calls of any sizes share one buffer:
-//   [0, 256)   arrivals of the router's workgroups, of the down columns
-//   kMoeTop    largest magnitudes of h's rows, as bits [kMoeMaxSlots]
-//   kMoeCtr    arrivals at each block of kMoeCols columns
-// then the router's scores, h and the down products, each written before it is read.
-constexpr size_t kMoeTop = 256, kMoeCtr = kMoeTop + 4 * kMoeMaxSlots,
-                 kMoeHead = kMoeCtr + 4 * (kMoeMaxHidden / kMoeCols);
+//   [0, 256)   arrivals of the router's workgroups
+//   kMoeCtr    arrivals of each expert's columns
+//   kMoeDown   arrivals at each 16 columns of y
+// then the router's scores, h, its codes and their scales, and the largest magnitude of
+// each row's tiles, the down workgroups' sums, each written before it is read.
+constexpr int kMoeGroup = 512;      // slots that a down workgroup has sums for at a time
+constexpr int kMoeMaxParts = 8, kMoeSplitTiles = 512;      // tiles of 16 columns whose sums are split
+constexpr size_t kMoeCtr = 256, kMoeDown = kMoeCtr + 4 * kMoeMaxExperts, kMoeHead = kMoeDown + 4 * kMoeSplitTiles;
 struct MoePlan {
-    int64_t ldh, ldp;               // floats of a row of h, of a down product
-    size_t off_scores, off_h, off_part, ws_bytes;
+    int64_t ldh;                    // floats of a row of h, bytes of a row of its codes
+    int32_t parts;                  // workgroups that share 16 columns of y
+    size_t off_scores, off_h, off_h8, off_h_scales, off_top, off_part, ws_bytes;
 };
-MoePlan moe_plan(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k);
+MoePlan moe_plan(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k, int cus);
 
 struct RouteArgs {
     const uint16_t *x, *router;
@@ -126,15 +127,20 @@ struct MoeArgs {
     const float *gate_scales, *up_scales, *down_scales;
     const int8_t *x;
     const float *x_scales;
-    int64_t ldx, ldy, ldh, ldp;
+    int64_t ldx, ldy, ldh;
     int32_t m, hidden, inter, experts, top_k;
     const int32_t *ids;
     const float *weights;
     void *y;
     int32_t y_bf16;
-    float *h, *part;                // [m * top_k][ldh], [m * top_k][ldp]
-    uint32_t *top;                  // [m * top_k]
-    uint32_t *ctr, *done;           // arrivals per column block, of column blocks
+    float *h;                       // [m * top_k][ldh]
+    int8_t *h8;                     // [m * top_k][ldh], with h_scales [m * top_k]
+    float *h_scales;
+    uint32_t *ctr;                  // arrivals of each expert's columns
+    uint32_t *top;                  // [m * top_k][tiles of 16 columns]: largest |h|, as bits
+    int32_t parts;                  // see MoePlan
+    int32_t *part;                  // their sums [tile][part][slot][16]
+    uint32_t *down_ctr;             // their arrivals
 };
 hipError_t launch_moe_mlp(const MoeArgs &a, hipStream_t s);
 

@@ -4,14 +4,12 @@
 //   route  scores of 16 experts per workgroup (bf16 matrix instructions, K split
 //          over its waves); the last workgroup to arrive chooses, a wave per row.
 //   up     a workgroup per chosen expert and 16 columns of gate and up, over the
-//          tokens that chose it: h = silu(gate) * up in fp32, the largest |h| of each
-//          row by atomic maximum (which no order changes).
-//   down   a workgroup per chosen expert and 64 columns of down: h's rows to codes
-//          in LDS, products, then the last workgroup of a column block adds
-//          the slots of each token in their order.
-// Which experts are chosen is found by every workgroup for itself from ids: the
-// launch has as many as could be, those past the chosen ones end.  Each expert's
-// weights are read once for up to 32 of its rows.
+//          tokens that chose it: h = silu(gate) * up in fp32; the expert's last
+//          workgroup to arrive turns h's rows into codes.
+//   down   a workgroup per 16 columns of y: its waves share out the chosen experts and
+//          their K, add whole-number sums in LDS (exact in any order), and then each
+//          token's slots in their order.
+// Each expert's weights are read once for up to 32 of its rows.
 #include <hip/hip_runtime.h>
 
 #include "i8_device.h"
@@ -24,82 +22,77 @@ using namespace i8;
 typedef __attribute__((ext_vector_type(4))) float f4;
 
 // ---------------------------------------------------------------------- route
-constexpr int kRouteWaves = 8;
+constexpr int kRouteWaves = 16;
 
 // Eight bf16 of a row from column r on, those at k and past it zeros.
 __device__ __forceinline__ bf16x8 bf16_piece(const uint16_t *row, int r, int k) {
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (r < k) {
-        v = *(const u32x4 *)(row + r);
+    u32x4 v = *(const u32x4 *)(row + (r < k ? r : 0));     // no branch: several are on their way
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (r + 2 * e >= k) v[e] = 0u;
-            else if (r + 2 * e + 1 >= k) v[e] &= 0xffffu;
-        }
-    }
+    for (int e = 0; e < 4; ++e)
+        v[e] = r + 2 * e + 1 < k ? v[e] : r + 2 * e < k ? v[e] & 0xffffu : 0u;
     return __builtin_bit_cast(bf16x8, v);
 }
 
-// Scores ordered as integers: larger score, larger key; NaN below all.  Zeros of
-// both signs are one score.
+// Scores ordered as integers above 0: larger score, larger key; NaN below all.  Zeros
+// of both signs are one score.
 __device__ __forceinline__ uint32_t score_key(float z) {
-    if (!(z == z)) return 0u;
+    if (!(z == z)) return 1u;
     const uint32_t b = __float_as_uint(z + 0.f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float key_score(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);    // 1 gives a NaN
+}
 
-// A wave's choice for one row: NV scores per lane, expert 64 i + lane.
-template <int NV>
-__device__ __forceinline__ void choose(const RouteArgs &A, int row, int lane) {
+// A wave's choice for one row: NV scores per lane, score(e) of expert e = 64 i + lane.
+template <int NV, class Score>
+__device__ __forceinline__ void choose_of(const RouteArgs &A, int row, int lane, const Score &score) {
     float z[NV];
-    uint64_t key[NV];
+    uint32_t key[NV];                              // 0: no expert, or taken; the others are larger
     bool bad = false;
-    float most = -__uint_as_float(0x7f800000u);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = 64 * i + lane;
-        z[i] = 0.f;
-        key[i] = 0;
-        if (e < A.experts) {
-            z[i] = __hip_atomic_load(A.part + (int64_t)row * A.experts + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            bad |= !(z[i] == z[i]);
-            most = fmaxf(most, z[i]);
-            // every expert's key is above 0; of equal scores the lower expert's is larger
-            key[i] = (uint64_t)score_key(z[i]) << 32 | (uint32_t)(kMoeMaxExperts - e);
-        }
+        z[i] = -__uint_as_float(0x7f800000u);
+        if (e < A.experts) z[i] = score(e);
+        bad |= !(z[i] == z[i]);
+        key[i] = e < A.experts ? score_key(z[i]) : 0u;
     }
+    uint32_t most = 0;
 #pragma unroll
-    for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+    for (int i = 0; i < NV; ++i) most = max(most, key[i]);
+    most = wave_max(most);
+    const float zmost = key_score(most);           // NaN: all are
     bad = __any(bad);
     float sum = 0.f;
     if (!A.normalize) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (64 * i + lane < A.experts) sum += expf(z[i] - most);
-#pragma unroll
-        for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+            if (64 * i + lane < A.experts) sum += expf(z[i] - zmost);
+        sum = wave_sum(sum);
     }
-    float mine = 0.f;                              // lane j's weight: slot j's
+    float mine = 0.f;                              // lane j's: slot j's
     int id = 0;
     for (int j = 0; j < A.top_k; ++j) {
-        uint64_t best = key[0];
-        float bz = z[0];
+        uint32_t best = key[0];
+        int at = 0;
 #pragma unroll
         for (int i = 1; i < NV; ++i)
-            if (key[i] > best) best = key[i], bz = z[i];
-        const uint64_t own = best;
-#pragma unroll
-        for (int o = 32; o; o >>= 1) {
-            const uint64_t other = (uint64_t)__shfl_xor((unsigned long long)best, o);
-            best = other > best ? other : best;
+            if (key[i] > best) best = key[i], at = i;
+        const uint32_t top = wave_max(best);
+        // of equal scores the lowest expert: the lowest i, then the lowest lane
+        uint64_t same = __ballot(best == top);
+        int e = 64 * __builtin_amdgcn_readlane(at, __ffsll((unsigned long long)same) - 1) + __ffsll((unsigned long long)same) - 1;
+        for (same &= same - 1; same; same &= same - 1) {
+            const int from = __ffsll((unsigned long long)same) - 1;
+            e = min(e, 64 * __builtin_amdgcn_readlane(at, from) + from);
         }
-        const int from = __ffsll((unsigned long long)__ballot(own == best)) - 1;
-        const float p = expf(__shfl(bz, from) - most);
+        const float p = expf(key_score(top) - zmost);
         if (A.normalize) sum += p;
-        if (lane == j) mine = p, id = kMoeMaxExperts - (int)(uint32_t)best;
+        if (lane == j) mine = p, id = e;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (key[i] == best) key[i] = 0;
+            if (64 * i + lane == e) key[i] = 0u;
     }
     if (lane < A.top_k) {
         A.ids[row * A.top_k + lane] = id;
@@ -107,280 +100,385 @@ __device__ __forceinline__ void choose(const RouteArgs &A, int row, int lane) {
     }
 }
 
+template <class Score>
+__device__ __forceinline__ void choose(const RouteArgs &A, int row, int lane, const Score &score) {
+    if (A.experts <= 128)
+        choose_of<2>(A, row, lane, score);
+    else if (A.experts <= 256)
+        choose_of<4>(A, row, lane, score);
+    else
+        choose_of<kMoeMaxExperts / 64>(A, row, lane, score);
+}
+
+// Small routers: a workgroup per row takes all experts, 16 of them to a wave and the
+// rest of the waves to parts of K, and nothing has to pass between workgroups (which
+// takes some 4 us).
+__global__ __launch_bounds__(64 * kRouteWaves) void route_row_kernel(const RouteArgs A) {
+    constexpr int U = 8;
+    __shared__ float part[kRouteWaves * 16 > kMoeMaxExperts ? kRouteWaves * 16 : kMoeMaxExperts];
+    const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4, row = blockIdx.x;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tiles = (A.experts + 15) / 16, ks = tiles >= kRouteWaves ? 1 : kRouteWaves / tiles;
+    const uint16_t *const xr = A.x + row * A.ldx;
+    for (int item = w; item < tiles * ks; item += kRouteWaves) {
+        const int k0 = item / tiles, tile = item - k0 * tiles;
+        const uint16_t *const rr = A.router + (int64_t)min(16 * tile + c, A.experts - 1) * A.ldr;
+        f4 acc = {0.f, 0.f, 0.f, 0.f};
+        for (int r0 = 32 * k0; r0 < A.k; r0 += 32 * ks * U) {
+            bf16x8 a[U], b[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                a[u] = bf16_piece(rr, r0 + 32 * ks * u + 8 * j, A.k);
+                b[u] = bf16_piece(xr, r0 + 32 * ks * u + 8 * j, A.k);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u], b[u], acc, 0, 0, 0);
+        }
+        if (c == 0)                                // every column of the product is this row
+#pragma unroll
+            for (int q = 0; q < 4; ++q) part[k0 * 16 * tiles + 16 * tile + 4 * j + q] = acc[q];
+    }
+    __syncthreads();
+    if (w != 0) return;
+    choose(A, row, lane, [&](int e) {
+        float z = part[e];
+        for (int i = 1; i < ks; ++i) z += part[i * 16 * tiles + e];
+        if (A.scores != nullptr) A.scores[row * A.lds + e] = z;
+        return z;
+    });
+}
+
+// Scores of 16 experts per workgroup, K by turns over its waves; the last to arrive
+// chooses.
 template <int MT>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs A) {
+    constexpr int U = MT == 1 ? 4 : 2;             // pieces on their way at a time
     __shared__ f4 part[kRouteWaves][MT][64];
     const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4, w = threadIdx.x >> 6;
-    const int e0 = blockIdx.x * 16;
+    const int e0 = blockIdx.x * 16, step = 32 * kRouteWaves;
     const uint16_t *rr = A.router + (int64_t)min(e0 + c, A.experts - 1) * A.ldr;
+    const uint16_t *xr[MT];
     f4 acc[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
-    for (int r0 = 32 * w; r0 < A.k; r0 += 32 * kRouteWaves) {
-        const bf16x8 a = bf16_piece(rr, r0 + 8 * j, A.k);
+    for (int i = 0; i < MT; ++i) {
+        acc[i] = f4{0.f, 0.f, 0.f, 0.f};
+        xr[i] = A.x + (int64_t)min(16 * i + c, A.m - 1) * A.ldx;
+    }
+    for (int r0 = 32 * w; r0 < A.k; r0 += step * U) {
+        bf16x8 a[U], b[U][MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const bf16x8 b = bf16_piece(A.x + (int64_t)min(16 * i + c, A.m - 1) * A.ldx, r0 + 8 * j, A.k);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc[i], 0, 0, 0);
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + step * u + 8 * j;
+            a[u] = bf16_piece(rr, r, A.k);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) b[u][i] = bf16_piece(xr[i], r, A.k);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u], b[u][i], acc[i], 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) part[w][i][lane] = acc[i];
     __syncthreads();
-    for (int q = threadIdx.x; q < MT * 64; q += blockDim.x) {
-        f4 z = part[0][q >> 6][q & 63];
-        for (int i = 1; i < kRouteWaves; ++i) z += part[i][q >> 6][q & 63];
-        const int row = 16 * (q >> 6) + (q & 15), e = e0 + 4 * ((q >> 4) & 3);
-        if (row < A.m)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (e + k < A.experts) {
-                    __hip_atomic_store(A.part + (int64_t)row * A.experts + e + k, z[k], __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-                    if (A.scores != nullptr) A.scores[row * A.lds + e + k] = z[k];
-                }
+    for (int q = threadIdx.x; q < MT * 256; q += blockDim.x) {
+        const int i = q >> 8, l = (q >> 2) & 63;
+        float z = part[0][i][l][q & 3];
+        for (int o = 1; o < kRouteWaves; ++o) z += part[o][i][l][q & 3];
+        const int row = 16 * i + (l & 15), e = e0 + 4 * (l >> 4) + (q & 3);
+        if (row < A.m && e < A.experts)
+            __hip_atomic_store(A.part + (int64_t)row * A.experts + e, z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     if (!last_to_arrive(A.counter, gridDim.x)) return;
-    for (int row = w; row < A.m; row += kRouteWaves) {
-        if (A.experts <= 128)
-            choose<2>(A, row, lane);
-        else if (A.experts <= 256)
-            choose<4>(A, row, lane);
-        else
-            choose<kMoeMaxExperts / 64>(A, row, lane);
-    }
+    for (int row = w; row < A.m; row += kRouteWaves)
+        choose(A, row, lane, [&](int e) {
+            const float z =
+                __hip_atomic_load(A.part + (int64_t)row * A.experts + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (A.scores != nullptr) A.scores[row * A.lds + e] = z;
+            return z;
+        });
 }
 
 // -------------------------------------------------------------------- experts
-constexpr int kMoeWaves = 4, kMoeThreads = 64 * kMoeWaves;
+constexpr int kDownWaves = 16;
 
-// What a workgroup knows of the choice: how many experts were chosen, which its own is
-// (-1: none), and the slots (token * top_k + j) that chose it.
-struct Chosen {
-    uint32_t map[kMoeMaxExperts / 32];
-    int32_t count;                                 // slots of this expert
-    uint16_t slots[kMoeMaxSlots];
-};
-__device__ __forceinline__ int find(Chosen &S, const MoeArgs &A, int index, int &active) {
-    const int slots = A.m * A.top_k, t = threadIdx.x;
-    if (t < kMoeMaxExperts / 32) S.map[t] = 0u;
-    if (t == 0) S.count = 0;
-    __syncthreads();
-    for (int i = t; i < slots; i += kMoeThreads) {
-        const uint32_t e = (uint32_t)A.ids[i];
-        if (e < (uint32_t)A.experts) atomicOr(&S.map[e >> 5], 1u << (e & 31));
+// The slots (token * top_k + j) of [first, last) that chose expert e, listed in `slots`
+// by every wave for itself (they write the same), and their number.
+__device__ __forceinline__ int slots_of(const int32_t *ids, int e, int first, int last, uint16_t *slots) {
+    const int lane = threadIdx.x & 63;
+    int count = 0;
+    for (int i0 = first; i0 < last; i0 += 64) {
+        const int i = i0 + lane;
+        const bool hit = i < last && ids[i] == e;
+        const uint64_t all = __ballot(hit);
+        if (hit) slots[count + __popcll(all & ((1ull << lane) - 1))] = (uint16_t)i;
+        count += __popcll(all);
     }
-    __syncthreads();
-    int mine = -1;
-    active = 0;
-    for (int i = 0; 32 * i < A.experts; ++i) {
-        uint32_t bits = S.map[i];
-        const int n = __popc(bits);
-        if (index >= active && index < active + n) {
-            for (int skip = index - active; skip; --skip) bits &= bits - 1;
-            mine = 32 * i + __ffs(bits) - 1;
-        }
-        active += n;
-    }
-    if (mine < 0) return -1;
-    // in any order: a row's result does not depend on its place
-    for (int i = t; i < slots; i += kMoeThreads)
-        if (A.ids[i] == mine) S.slots[atomicAdd(&S.count, 1)] = (uint16_t)i;
-    __syncthreads();
-    return mine;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");     // lanes read what others of the wave wrote
+    return count;
 }
 
-// Rows [base, base + 16 MT) of the expert's list.
-template <int MT>
-__device__ __forceinline__ void up_rows(const MoeArgs &A, const Chosen &S, int base, const char *gt, const char *ut,
-                                        const float *gs, const float *us, int steps, i32x4 (*part)[4][64]) {
-    constexpr int U = 4;
+// A wave's fragments s0, s0 + step, .. below `end` of T streams of weight tiles against
+// MT 16-row tiles of codes, through a ring of D register sets.
+template <int T, int MT, int D>
+__device__ __forceinline__ void stream(const char *const (&wt)[T], const int8_t *const (&xr)[MT], int k, int s0, int step,
+                                       int end, i32x4 (&acc)[T][MT]) {
+    const int lane = threadIdx.x & 63, j = lane >> 4;
+    struct Set {
+        i32x4 f[T], x[MT];
+    };
+    auto load = [&](int s, Set &o) __attribute__((always_inline)) {
+        const int at = min(s, end - 1), r = at * kI8K + 16 * j, in = r < k ? r : 0;      // past k: meets zeros
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+            o.f[t] = __builtin_nontemporal_load((const i32x4 *)(wt[t] + (int64_t)at * kI8Frag + 16 * lane));
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o.x[i] = *(const i32x4 *)(xr[i] + in);
+    };
+    auto multiply = [&](int s, const Set &o) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const i32x4 f = s < end ? o.f[t] : i32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[t][i] = mfma64(f, o.x[i], acc[t][i]);
+        }
+    };
+    if (s0 >= end) return;
+    Set ring[D];
+#pragma unroll
+    for (int u = 0; u < D; ++u) load(s0 + u * step, ring[u]);
+    __builtin_amdgcn_sched_barrier(0);
+    for (; s0 + D * step < end; s0 += D * step) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+            multiply(s0 + u * step, ring[u]);
+            load(s0 + (D + u) * step, ring[u]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < D; ++u) multiply(s0 + u * step, ring[u]);
+}
+
+// Rows [base, base + 16 MT) of the expert's list into h, CT tiles of 16 columns from
+// `tile0` on.
+template <int CT, int MT, int W>
+__device__ __forceinline__ void up_rows(const MoeArgs &A, const uint16_t *slots, int count, int base, int e, int tile0,
+                                        int tiles, i32x4 (*part)[2 * CT * 2][64]) {
     const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), steps = (int)i8_steps(A.hidden);
     const int8_t *xr[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        xr[i] = A.x + (int64_t)(S.slots[min(base + 16 * i + c, S.count - 1)] / (uint32_t)A.top_k) * A.ldx;
-    i32x4 g[MT], u[MT];
+        xr[i] = A.x + (int64_t)(slots[min(base + 16 * i + c, count - 1)] / (uint32_t)A.top_k) * A.ldx;
+    const char *wt[2 * CT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) g[i] = u[i] = i32x4{0, 0, 0, 0};
-    for (int s0 = w; s0 < steps; s0 += U * kMoeWaves) {
-        i32x4 fg[U], fu[U], x[U][MT];
-#pragma unroll
-        for (int q = 0; q < U; ++q) {
-            const int s = s0 + q * kMoeWaves, at = min(s, steps - 1);
-            fg[q] = *(const i32x4 *)(gt + (int64_t)at * kI8Frag);
-            fu[q] = *(const i32x4 *)(ut + (int64_t)at * kI8Frag);
-            if (s >= steps) fg[q] = fu[q] = i32x4{0, 0, 0, 0};
-            const int r = at * kI8K + 16 * j, rr = r < A.hidden ? r : 0;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) x[q][i] = *(const i32x4 *)(xr[i] + rr);
-        }
-#pragma unroll
-        for (int q = 0; q < U; ++q)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                g[i] = mfma64(fg[q], x[q][i], g[i]);
-                u[i] = mfma64(fu[q], x[q][i], u[i]);
-            }
+    for (int t = 0; t < CT; ++t) {
+        const int64_t at = ((int64_t)e * tiles + min(tile0 + t, tiles - 1)) * steps * kI8Frag;
+        wt[2 * t] = A.gate + at;
+        wt[2 * t + 1] = A.up + at;
     }
+    i32x4 acc[2 * CT][MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) part[w][2 * i][lane] = g[i], part[w][2 * i + 1][lane] = u[i];
+    for (int t = 0; t < 2 * CT; ++t)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[t][i] = i32x4{0, 0, 0, 0};
+    stream<2 * CT, MT, MT == 1 ? 4 : 2>(wt, xr, A.hidden, w, W, steps, acc);
+#pragma unroll
+    for (int t = 0; t < 2 * CT; ++t)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) part[w][t * MT + i][lane] = acc[t][i];
     __syncthreads();
-    if (w < MT && base + 16 * w < S.count) {       // wave w: row tile w
-        i32x4 a = part[0][2 * w][lane], b = part[0][2 * w + 1][lane];
+    // a wave per column tile and row tile
+    const int t = w / MT, i = w % MT, col = (tile0 + t) * kI8Cols + 4 * j;
+    if (t < CT && base + 16 * i < count && col < (int)A.ldh) {
+        i32x4 a = part[0][2 * t * MT + i][lane], b = part[0][(2 * t + 1) * MT + i][lane];
 #pragma unroll
-        for (int i = 1; i < kMoeWaves; ++i) a += part[i][2 * w][lane], b += part[i][2 * w + 1][lane];
-        const int at = base + 16 * w + c, slot = S.slots[min(at, S.count - 1)];
+        for (int q = 1; q < W; ++q) a += part[q][2 * t * MT + i][lane], b += part[q][(2 * t + 1) * MT + i][lane];
+        const int at = base + 16 * i + c, slot = slots[min(at, count - 1)];
         const float xs = A.x_scales[slot / (uint32_t)A.top_k];
-        const int col = blockIdx.x * kI8Cols + 4 * j;
-        f4 h;
+        const float *gs = A.gate_scales + (int64_t)e * A.inter, *us = A.up_scales + (int64_t)e * A.inter;
+        float h[4];
         uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            h[e] = col + e < A.inter ? silu((float)a[e] * xs * gs[col + e]) * ((float)b[e] * xs * us[col + e]) : 0.f;
-            top = max(top, magnitude(h[e]));
+        for (int q = 0; q < 4; ++q) {
+            h[q] = col + q < A.inter ? silu((float)a[q] * xs * gs[col + q]) * ((float)b[q] * xs * us[col + q]) : 0.f;
+            top = max(top, magnitude(h[q]));
         }
-        if (at < S.count) *(f4 *)(A.h + (int64_t)slot * A.ldh + col) = h;
         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        if (at < S.count && j == 0) atomicMax(A.top + slot, top);
+        if (at < count) {
+            float *p = A.h + (int64_t)slot * A.ldh + col;
+            share(p, h[0], h[1]);
+            share(p + 2, h[2], h[3]);
+            if (j == 0)
+                __hip_atomic_store(A.top + (int64_t)slot * tiles + tile0 + t, top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
     }
     __syncthreads();
 }
 
-__global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(const MoeArgs A) {
-    __shared__ Chosen S;
-    __shared__ i32x4 part[kMoeWaves][4][64];
-    int active;
-    const int e = find(S, A, blockIdx.y, active);
-    if (e < 0) return;
-    const int steps = (int)i8_steps(A.hidden), tiles = gridDim.x;
-    const int64_t tile = ((int64_t)e * tiles + blockIdx.x) * steps * kI8Frag + 16 * (threadIdx.x & 63);
-    const float *gs = A.gate_scales + (int64_t)e * A.inter, *us = A.up_scales + (int64_t)e * A.inter;
-    for (int base = 0; base < S.count; base += 32) {
-        if (S.count - base <= 16)
-            up_rows<1>(A, S, base, A.gate + tile, A.up + tile, gs, us, steps, part);
+// CT: tiles of 16 columns of a workgroup; W: its waves.
+template <int CT, int W>
+__global__ __launch_bounds__(64 * W, 4) void moe_up_kernel(const MoeArgs A) {
+    __shared__ uint16_t slots[kMoeMaxSlots];
+    __shared__ i32x4 part[W][2 * CT * 2][64];
+    const int all = A.m * A.top_k, tiles = (int)i8_tiles(A.inter), tile0 = blockIdx.x * CT;
+    // blockIdx.y: an expert, or where there are fewer slots than experts, a slot, whose
+    // expert is taken by the first one that names it
+    const bool by_slot = all < A.experts;
+    const int e = by_slot ? A.ids[blockIdx.y] : (int)blockIdx.y;
+    if ((uint32_t)e >= (uint32_t)A.experts) return;
+    const int count = slots_of(A.ids, e, 0, all, slots);
+    if (count == 0 || (by_slot && slots[0] != blockIdx.y)) return;
+    for (int base = 0; base < count; base += 32) {
+        if (count - base <= 16)
+            up_rows<CT, 1, W>(A, slots, count, base, e, tile0, tiles, part);
         else
-            up_rows<2>(A, S, base, A.gate + tile, A.up + tile, gs, us, steps, part);
+            up_rows<CT, 2, W>(A, slots, count, base, e, tile0, tiles, part);
     }
-}
-
-constexpr int kMoeChunk = 1024;     // K of h's codes in LDS at a time
-
-template <int MT>
-__device__ __forceinline__ void down_rows(const MoeArgs &A, const Chosen &S, int base, const char *dt, const float *ds,
-                                          int tile, int tiles, int steps, i32x4 *codes, const Step8 *st) {
-    constexpr int U = 4;
-    const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
-    const int rows = min(S.count - base, 16 * MT);
-    i32x4 acc[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = i32x4{0, 0, 0, 0};
-    for (int k0 = 0; k0 < A.inter; k0 += kMoeChunk) {
-        const int pieces = min(kMoeChunk, (int)A.ldh - k0) / 16;       // 16-column pieces of a row, ldh is whole ones
-        const int n = min(kMoeChunk / kI8K, steps - k0 / kI8K);
-        __syncthreads();                           // the chunk before has been read
-        for (int p = threadIdx.x; p < rows * pieces; p += kMoeThreads) {
-            const int r = p / pieces, q = p - r * pieces;
-            const f4 *src = (const f4 *)(A.h + (int64_t)S.slots[base + r] * A.ldh + k0 + 16 * q);
-            const Step8 s = st[r];
-            i32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const f4 h = src[e];
-                v[e] = (int32_t)codes8(h[0], h[1], h[2], h[3], s);
-            }
-            codes[((q >> 2) * MT + (r >> 4)) * 64 + (q & 3) * 16 + (r & 15)] = v;
+    if (!last_to_arrive(A.ctr + e, gridDim.x)) return;
+    // this expert's h is whole: 32 rows at a time, the largest magnitude of each from its
+    // tiles', then the codes
+    __shared__ Step8 st[32];
+    const int quads = (int)A.ldh / 4, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int base = 0; base < count; base += 32) {
+        const int rows = min(32, count - base), work = rows * quads;
+        for (int r = w; r < rows; r += W) {
+            const int slot = slots[base + r];
+            uint32_t top = 0;
+            for (int i = lane; i < tiles; i += 64)
+                top = max(top, __hip_atomic_load(A.top + (int64_t)slot * tiles + i, __ATOMIC_RELAXED,
+                                                 __HIP_MEMORY_SCOPE_AGENT));
+            st[r] = step8(wave_max(top));
+            if (lane == 0) A.h_scales[slot] = st[r].scale;
         }
         __syncthreads();
-        if (tile < tiles)
-            for (int s0 = 0; s0 < n; s0 += U) {
-                i32x4 f[U];
+        constexpr int U = 4;
+        for (int i0 = threadIdx.x; i0 < work; i0 += 64 * W * U) {
+            float2 a[U], b[U];
+            int64_t at[U];
+            int row[U];
 #pragma unroll
-                for (int q = 0; q < U; ++q)
-                    f[q] = *(const i32x4 *)(dt + (int64_t)(k0 / kI8K + min(s0 + q, n - 1)) * kI8Frag);
-#pragma unroll
-                for (int q = 0; q < U; ++q)
-                    if (s0 + q < n)
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            acc[i] = mfma64(f[q], codes[((s0 + q) * MT + i) * 64 + lane], acc[i]);
+            for (int u = 0; u < U; ++u) {
+                const int i = min(i0 + 64 * W * u, work - 1);
+                row[u] = i / quads;
+                at[u] = (int64_t)slots[base + row[u]] * A.ldh + 4 * (i - row[u] * quads);
+                a[u] = shared2(A.h + at[u]);
+                b[u] = shared2(A.h + at[u] + 2);
             }
-    }
-    if (tile >= tiles) return;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int r = 16 * i + c, col = tile * kI8Cols + 4 * j;
-        if (r >= rows) continue;
-        const float hs = st[r].scale;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = col + e < A.hidden ? (float)acc[i][e] * hs * ds[col + e] : 0.f;
-        float *p = A.part + (int64_t)S.slots[base + r] * A.ldp + col;
-        share(p, v[0], v[1]);
-        share(p + 2, v[2], v[3]);
+            for (int u = 0; u < U; ++u)            // past the end the last one again: the same bytes
+                *(uint32_t *)(A.h8 + at[u]) = codes8(a[u].x, a[u].y, b[u].x, b[u].y, st[row[u]]);
+        }
+        __syncthreads();
     }
 }
 
+// 16 columns of y, by the `parts` workgroups of blockIdx.y together: each takes every
+// so-many-th piece of work (an expert and a part of K); the last to arrive adds the
+// others' whole-number sums.  Slots go by groups of whole tokens that LDS has sums for
+// (parts = 1 where that takes more than one).
+constexpr int kDownChunk = 8;       // most fragments of a piece of work
+
 template <bool BF16>
-__global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(const MoeArgs A) {
-    __shared__ Chosen S;
-    __shared__ i32x4 codes[2 * kMoeChunk / kI8K * 64];
-    __shared__ Step8 st[32];
-    int active;
-    const int e = find(S, A, blockIdx.y, active);
-    // with no expert chosen at all the first row of workgroups still writes y
-    if (e < 0 && !(active == 0 && blockIdx.y == 0)) return;
-    const int steps = (int)i8_steps(A.inter), tiles = (int)i8_tiles(A.hidden);
-    if (e >= 0) {
-        const int tile = blockIdx.x * (kMoeCols / kI8Cols) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const char *dt = A.down + ((int64_t)e * tiles + min(tile, tiles - 1)) * steps * kI8Frag + 16 * (threadIdx.x & 63);
-        const float *ds = A.down_scales + (int64_t)e * A.hidden;
-        for (int base = 0; base < S.count; base += 32) {
+__global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeArgs A) {
+    __shared__ int32_t sums[kMoeGroup][16];
+    __shared__ int32_t ids[kMoeGroup];
+    __shared__ int32_t first[kMoeMaxExperts];      // the first slot of the group that chose an expert
+    __shared__ uint16_t chosen[kMoeGroup];
+    __shared__ uint16_t lists[kDownWaves][kMoeGroup];
+    const int t = threadIdx.x, lane = t & 63, c = lane & 15, j = lane >> 4, tile = blockIdx.x, parts = gridDim.y;
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int steps = (int)i8_steps(A.inter), tiles = gridDim.x, chunks = (steps + kDownChunk - 1) / kDownChunk;
+    const int each = (steps + chunks - 1) / chunks;
+    const int tokens = min(A.m, kMoeGroup / A.top_k);
+    for (int i0 = 0; i0 < A.m; i0 += tokens) {
+        const int lo = i0 * A.top_k, n = (min(i0 + tokens, A.m) - i0) * A.top_k;
+        for (int i = t; i < A.experts; i += 64 * kDownWaves) first[i] = kMoeGroup;
+        __syncthreads();
+        for (int i = t; i < n; i += 64 * kDownWaves) {
+            const int32_t e = A.ids[lo + i];
+            ids[i] = e;
+            if ((uint32_t)e < (uint32_t)A.experts) atomicMin(&first[e], i);
+        }
+        for (int i = t; i < n * 16; i += 64 * kDownWaves) (&sums[0][0])[i] = 0;
+        __syncthreads();
+        int active = 0;                            // the chosen experts, listed alike by every wave and part
+        for (int k0 = 0; k0 < n; k0 += 64) {
+            const int i = k0 + lane;
+            const uint32_t e = i < n ? (uint32_t)ids[i] : 0xffffffffu;
+            const bool names = e < (uint32_t)A.experts && first[e] == i;
+            const uint64_t all = __ballot(names);
+            if (names) chosen[active + __popcll(all & ((1ull << lane) - 1))] = (uint16_t)e;
+            active += __popcll(all);
+        }
+        __syncthreads();
+        for (int item = w * parts + blockIdx.y; item < active * chunks; item += kDownWaves * parts) {
+            const int chunk = item / active, e = chosen[item - chunk * active];
+            const int s0 = chunk * each, end = min(s0 + each, steps);
+            const char *const wt[1] = {A.down + ((int64_t)e * tiles + tile) * steps * kI8Frag};
+            const int count = slots_of(ids, e, 0, n, lists[w]);
+            for (int base = 0; base < count; base += 16) {
+                const int at = base + c, slot = lists[w][min(at, count - 1)];
+                const int8_t *const xr[1] = {A.h8 + (int64_t)(lo + slot) * A.ldh};
+                i32x4 acc[1][1] = {{i32x4{0, 0, 0, 0}}};
+                stream<1, 1, 8>(wt, xr, (int)A.ldh, s0, 1, end, acc);
+                if (at < count)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) atomicAdd(&sums[slot][4 * j + q], acc[0][0][q]);
+            }
+        }
+        __syncthreads();
+        if (parts > 1) {
+            int32_t *const p = A.part + (int64_t)tile * parts * n * 16;
+            for (int i = t; i < n * 8; i += 64 * kDownWaves)
+                share(p + (int64_t)blockIdx.y * n * 16 + 2 * i, (&sums[0][0])[2 * i], (&sums[0][0])[2 * i + 1]);
+            if (!last_to_arrive(A.down_ctr + tile, parts)) return;
+            for (int i = t; i < n * 8; i += 64 * kDownWaves) {
+                int2 v = make_int2((&sums[0][0])[2 * i], (&sums[0][0])[2 * i + 1]);
+                for (int o = 0; o < parts; ++o)
+                    if (o != (int)blockIdx.y) {
+                        const int2 u = shared2(p + (int64_t)o * n * 16 + 2 * i);
+                        v.x += u.x;
+                        v.y += u.y;
+                    }
+                (&sums[0][0])[2 * i] = v.x;
+                (&sums[0][0])[2 * i + 1] = v.y;
+            }
             __syncthreads();
-            if (threadIdx.x < 32) st[threadIdx.x] = step8(A.top[S.slots[min(base + (int)threadIdx.x, S.count - 1)]]);
-            __syncthreads();
-            if (S.count - base <= 16)
-                down_rows<1>(A, S, base, dt, ds, tile, tiles, steps, codes, st);
+        }
+        for (int i = t; i < n / A.top_k * 16; i += 64 * kDownWaves) {
+            const int row = i / 16, col = tile * kI8Cols + (i & 15);
+            if (col >= A.hidden) continue;
+            float y = 0.f;
+            for (int q = 0; q < A.top_k; ++q) {
+                const int slot = row * A.top_k + q, id = ids[slot];
+                if (id == -1) continue;
+                float p = __uint_as_float(0x7fc00000u);
+                if ((uint32_t)id < (uint32_t)A.experts)
+                    p = (float)sums[slot][i & 15] * A.h_scales[lo + slot] * A.down_scales[(int64_t)id * A.hidden + col];
+                y += A.weights[lo + slot] * p;
+            }
+            const int64_t at = (i0 + row) * A.ldy + col;
+            if constexpr (BF16)
+                ((uint16_t *)A.y)[at] = to_bf16(y);
             else
-                down_rows<2>(A, S, base, dt, ds, tile, tiles, steps, codes, st);
+                ((float *)A.y)[at] = y;
         }
+        __syncthreads();
     }
-    if (!last_to_arrive(A.ctr + blockIdx.x, max(active, 1))) return;
-    // this column block's products are all there: each token's slots in their order
-    for (int i = threadIdx.x; i < A.m * (kMoeCols / 2); i += kMoeThreads) {
-        const int row = i / (kMoeCols / 2), col = blockIdx.x * kMoeCols + 2 * (i % (kMoeCols / 2));
-        if (col >= A.hidden) continue;
-        float a = 0.f, b = 0.f;
-        for (int q = 0; q < A.top_k; ++q) {
-            const int slot = row * A.top_k + q, id = A.ids[slot];
-            if (id == -1) continue;
-            float2 p = make_float2(__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u));
-            if ((uint32_t)id < (uint32_t)A.experts) p = shared2(A.part + (int64_t)slot * A.ldp + col);
-            const float wt = A.weights[slot];
-            a += wt * p.x;
-            b += wt * p.y;
-        }
-        const int64_t at = row * A.ldy + col;
-        if constexpr (BF16) {
-            ((uint16_t *)A.y)[at] = to_bf16(a);
-            if (col + 1 < A.hidden) ((uint16_t *)A.y)[at + 1] = to_bf16(b);
-        } else {
-            ((float *)A.y)[at] = a;
-            if (col + 1 < A.hidden) ((float *)A.y)[at + 1] = b;
-        }
-    }
-    // the last column block: every workgroup has read the largest magnitudes
-    if (!last_to_arrive(A.done, gridDim.x)) return;
-    for (int i = threadIdx.x; i < A.m * A.top_k; i += kMoeThreads) A.top[i] = 0u;
 }
 
 }  // namespace
 
 hipError_t launch_moe_route(const RouteArgs &a, hipStream_t s) {
+    // 8 experts of 4096: a workgroup per row 6.8 us, one for all 14.5; 128 of 2048: 20.8, 7.5
     const dim3 grid((a.experts + 15) / 16), block(64 * kRouteWaves);
-    if (a.m <= 16)
+    if ((int64_t)a.experts * a.k <= 48 << 10)
+        hipLaunchKernelGGL(route_row_kernel, dim3(a.m), block, 0, s, a);
+    else if (a.m <= 16)
         hipLaunchKernelGGL((route_kernel<1>), grid, block, 0, s, a);
     else if (a.m <= 32)
         hipLaunchKernelGGL((route_kernel<2>), grid, block, 0, s, a);
@@ -391,12 +489,19 @@ hipError_t launch_moe_route(const RouteArgs &a, hipStream_t s) {
 
 hipError_t launch_moe_mlp(const MoeArgs &a, hipStream_t s) {
     const int slots = a.m * a.top_k, most = slots < a.experts ? slots : a.experts;
-    hipLaunchKernelGGL(moe_up_kernel, dim3((a.inter + kI8Cols - 1) / kI8Cols, most), dim3(kMoeThreads), 0, s, a);
-    const dim3 grid((a.hidden + kMoeCols - 1) / kMoeCols, most);
-    if (a.y_bf16)
-        hipLaunchKernelGGL((moe_down_kernel<true>), grid, dim3(kMoeThreads), 0, s, a);
+    // 32 columns of gate and up per workgroup; its waves take 8 fragments or more each
+    // (1 / 6 rows of 8 of 128 experts 2048 -> 768, 32 rows of 2 of 8 4096 -> 14336: four
+    // waves 9.5 / 27.4 / 179 us, eight 9.8 / 30.0 / 173; 16 columns and four 10.1 / 29.4 / 193)
+    const dim3 up((unsigned)((i8_tiles(a.inter) + 1) / 2), most);
+    if (i8_steps(a.hidden) >= 48)
+        hipLaunchKernelGGL((moe_up_kernel<2, 8>), up, dim3(512), 0, s, a);
     else
-        hipLaunchKernelGGL((moe_down_kernel<false>), grid, dim3(kMoeThreads), 0, s, a);
+        hipLaunchKernelGGL((moe_up_kernel<2, 4>), up, dim3(256), 0, s, a);
+    const dim3 down((unsigned)i8_tiles(a.hidden), a.parts), block(64 * kDownWaves);
+    if (a.y_bf16)
+        hipLaunchKernelGGL((moe_down_kernel<true>), down, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((moe_down_kernel<false>), down, block, 0, s, a);
     return hipGetLastError();
 }
 

@@ -109,11 +109,8 @@ __global__ __launch_bounds__(kRowMostThreads) void rows_kernel(const RowArgs A) 
         }
         float inv = 1.f;
         if (OP == kRowNorm || A.codes != nullptr) {
-#pragma unroll
-            for (int o = 32; o; o >>= 1) {
-                if constexpr (OP == kRowNorm) ss += __shfl_xor(ss, o);
-                top = max(top, (uint32_t)__shfl_xor((int)top, o));
-            }
+            if constexpr (OP == kRowNorm) ss = wave_sum(ss);
+            top = wave_max(top);
             if (waves > 1) {                       // two sets in turn: the next row's need no second barrier
                 if (lane == 0) sums[turn][wave] = ss, tops[turn][wave] = top;
                 __syncthreads();

@@ -114,7 +114,7 @@ class Layer:
             ws = _ws(self.hidden, self.inter, self.experts, self.m, ids.shape[1])
         binding.moe_mlp(self.moe, self.x, self.xs, self.m, dev(ids), dev(wt), y, ws)
         torch.cuda.synchronize()
-        assert not ws[:256 + 4 * 2048 + 4 * 1024].any(), "counters left"
+        assert not ws[:256 + 4 * 1024 + 4 * 512].any(), "counters left"
         assert (y[:, self.hidden:] == 7).all()
         return host(y)[:, :self.hidden]
 
