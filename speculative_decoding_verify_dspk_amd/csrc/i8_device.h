@@ -41,11 +41,15 @@ __device__ __forceinline__ Step8 step8(uint32_t top) {
     s.scale = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : s.held ? t / 127.f : 0.f;
     return s;
 }
-__device__ __forceinline__ uint32_t code8(float x, const Step8 &s) {
-    return s.held ? (uint32_t)(int)rintf(x * s.inv) & 0xffu : 0u;
-}
+// Four codes.  1.5 * 2^23 added to the (rounded) product leaves it rounded half to even
+// in the low bits, in two's complement.
 __device__ __forceinline__ uint32_t codes8(float a, float b, float c, float d, const Step8 &s) {
-    return code8(a, s) | code8(b, s) << 8 | code8(c, s) << 16 | code8(d, s) << 24;
+#pragma clang fp contract(off)
+    if (!s.held) return 0u;
+    const float k = 12582912.f;
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(b * s.inv + k), __float_as_uint(a * s.inv + k), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(d * s.inv + k), __float_as_uint(c * s.inv + k), 0x04000c0cu);
+    return lo | hi;
 }
 
 // A value of every lane and that of the lane a DPP control names, 0 where there is none.
@@ -75,8 +79,19 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// x / (1 + exp(-x)); exp overflows to infinity far below zero, which leaves -0.
-__device__ __forceinline__ float silu(float x) { return x / (1.f + expf(-x)); }
+// x / (1 + exp(-x)): exp as 2 to the rounded product with log2(e), times 1 + ln(2) times
+// what that rounding and the constant's lost; the hardware's power and reciprocal are
+// off by a step at most.  Where exp(-x) would pass fp32's largest number it counts as
+// infinite.  (expf and a division: 1500 rows of 9728 28 us instead of 21.)
+__device__ __forceinline__ float silu(float x) {
+#pragma clang fp contract(off)
+    const float y = fminf(fmaxf(x, -88.7f), 88.7f), hi = -1.44269504f, lo = -1.92596303e-8f;
+    const float t = y * hi, r = fmaf(y, lo, fmaf(y, hi, -t));
+    float e = __builtin_amdgcn_exp2f(t);
+    e = fmaf(e, r * 0.693147181f, e);
+    // a quarter of the denominator: its reciprocal is no subnormal number
+    return x < -88.7f ? x * 0.f : .25f * x * __builtin_amdgcn_rcpf(fmaf(e, .25f, .25f));
+}
 
 // Data that other workgroups of the same launch read goes by device-scope accesses,
 // which reach them without a cache flush; the writer waits for them before it counts

@@ -16,14 +16,16 @@ pytestmark = pytest.mark.gpu
 # square), all positive, halved by the root; then mean, eps, root, reciprocal and
 # the two products of y: 1 + 0.5 + (32 + 10 + 1) / 2 + 7 < 32 roundings.
 NORM = 32 * F32
-# silu: exp off by 2 ulp = 4 half steps, 1 + exp, the quotient, the product with up.
+# silu: exp by the hardware's power of 2, off by a step (two half steps), and the
+# correction of its argument (1); 1 + exp (1); the hardware's reciprocal, off by a step
+# (2); the products with gate and up (2).
 SILU = 8 * F32
 
 
 def far_below(gate, up):
-    """exp(-gate) passes fp32's largest number, below 2^128, for gates under -88.72, and the
-    activation is -0 there instead of gate * exp(gate) * up with exp(gate) < 2^-128; a
-    quotient below 2^-126 is off by half of 2^-149 times up, less than as much again."""
+    """exp(-gate) passes fp32's largest number, below 2^128, for gates under -88.7, and the
+    activation is -0 there instead of gate * exp(gate) * up with exp(gate) < 2^-127.96; a
+    quotient below 2^-126 is off by half of 2^-149 times up, less than the difference to 2^-127."""
     return 2.0 ** -127 * np.abs(np.asarray(gate, np.float64) * up)
 
 SHAPES = [(1, 1), (1, 2560), (2, 7), (3, 8), (5, 64), (4, 511), (6, 520), (3, 4097), (2, 8193), (2, 16390), (1, 32768),
