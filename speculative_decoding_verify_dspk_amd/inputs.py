@@ -298,3 +298,15 @@ def make_activations_device(m: int, k: int, *labels):
     g = device_generator(*labels, m, k, "act")
     x = torch.empty((m, k), dtype=torch.float32, device="cuda").normal_(0.0, 1.0, generator=g)
     return x.to(torch.bfloat16).view(torch.int16)
+
+
+def make_int8_device(shape, *labels):
+    """8-bit weights drawn on the GPU: codes of normal values (std 36, within +-127)
+    of the shape [..][n][k], and float32 scales [..][n] that give a channel's weights a
+    standard deviation of about 1 / sqrt(k)."""
+    import torch
+    g = device_generator(*labels, *shape)
+    codes = torch.empty(shape, dtype=torch.float32, device="cuda").normal_(0.0, 36.0, generator=g)
+    codes = codes.round_().clamp_(-127, 127).to(torch.int8)
+    scales = torch.empty(shape[:-1], dtype=torch.float32, device="cuda").uniform_(0.5, 1.5, generator=g)
+    return codes, scales / (36.0 * shape[-1] ** 0.5)

@@ -18,6 +18,11 @@ over it, and o reads what comes out; ``set_tree`` makes the rows a drafted tree
 instead of a chain, and ``launch_commit`` moves the accepted path's entries
 together after the acceptance.
 
+``Int8VerifyStack`` is the same round over 8-bit integer layers, rows and weights
+alike, with the parts between the projections: the residual stream and its norms, the
+activation or a router and its experts.  There a layer reads what the layer before it
+wrote.
+
 A round's launches can be captured once into HIP graphs (``capture_round``)
 and replayed every round: the kernels take no host-side work between calls
 (their workspaces come back zeroed), so a replay is the whole round in one
@@ -254,3 +259,132 @@ class VerifyStack:
         """HIP graphs (layers, head, accept) of one greedy round at width m, of a
         tree if one is set at the time."""
         return self.capture_calls(m, copy, lambda: self.launch_accept(m, draft_ids, accept_len, committed))
+
+
+@dataclass
+class Int8Layer:
+    qkv: binding.Int8Weight                      # q, k and v by columns
+    o: binding.Int8Weight
+    gate_up: binding.Int8Weight | None = None    # gate and up by columns: a dense layer
+    down: binding.Int8Weight | None = None
+    moe: binding.MoEWeights | None = None        # or a router and its experts
+    router: object = None
+    attn_norm: object = None                     # float32 [hidden]
+    mlp_norm: object = None
+
+
+@dataclass
+class Int8VerifyStack(VerifyStack):
+    """A stack of 8-bit integer layers with the model's head (``bits`` is the head's
+    format).  ``experts`` > 0: mixture layers, ``top_k`` of the experts for each row,
+    each of width ``expert_inter``.
+
+    A layer: residual += the rows before it, norm to 8 bits, q/k/v, the attention side
+    (with attach_cache; else o reads rows of its own), its rows to 8 bits, o, residual
+    and norm again, then gate and up, activation to 8 bits, down, or router and experts.
+    After the last layer residual and norm give the head its bf16 rows."""
+    experts: int = 0
+    top_k: int = 0
+    expert_inter: int = 0
+    norm_eps: float = 1e-6
+
+    def __post_init__(self):
+        import torch
+        s = inputs.LAYER_SHAPES[self.model]
+        self.hidden, self.qdim, self.kvdim, self.inter, self.vocab = (s["hidden"], s["q"], s["kv"], s["inter"],
+                                                                      s["vocab"])
+        H, Q, KV, F, V, M = self.hidden, self.qdim, self.kvdim, self.inter, self.vocab, self.max_m
+        if self.experts:
+            F = self.expert_inter
+            if not 1 <= self.top_k <= self.experts or F < 1:
+                raise ValueError("experts: top_k of 1 .. experts and expert_inter >= 1 are needed")
+        lab = (self.model, self.seed, "int8")
+        mk = lambda *z: binding.Int8Weight(*inputs.make_int8_device(z[0], *lab, *z[1:]))
+        f32 = dict(dtype=torch.float32, device="cuda")
+        for cp in range(self.copies):
+            ls = []
+            for li in range(self.n_layers):
+                g = inputs.device_generator(*lab, cp, li, "norm")
+                norm = lambda: torch.empty(H, **f32).uniform_(0.8, 1.2, generator=g)
+                L = Int8Layer(qkv=mk((Q + 2 * KV, H), cp, li, "qkv"), o=mk((H, Q), cp, li, "o"), attn_norm=norm(),
+                              mlp_norm=norm())
+                if self.experts:
+                    L.moe = binding.MoEWeights(*(mk((self.experts,) + z, cp, li, name) for name, z in
+                                                 (("gate", (F, H)), ("up", (F, H)), ("down", (H, F)))))
+                    L.router = torch.empty((self.experts, H), **f32).normal_(0.0, H ** -0.5, generator=g).bfloat16()
+                else:
+                    L.gate_up, L.down = mk((2 * F, H), cp, li, "gate_up"), mk((H, F), cp, li, "down")
+                ls.append(L)
+            self.layers.append(ls)
+            c, sc, bi = inputs.make_qweight_device(V, H, self.bits, *lab, cp, "lm_head")
+            self.heads.append(binding.DeviceQWeight(V, H, self.bits, c, sc, bi))
+        g = inputs.device_generator(*lab, "final_norm")
+        self.final_norm = torch.empty(H, **f32).uniform_(0.8, 1.2, generator=g)
+        act = lambda k, name: inputs.make_activations_device(M, k, self.model, self.seed, name).view(torch.bfloat16)
+        self.x_in, self.x_o = act(H, "embedded"), act(Q, "o_in")
+        bf, i8 = dict(dtype=torch.bfloat16, device="cuda"), dict(dtype=torch.int8, device="cuda")
+        codes = lambda k: (torch.zeros((M, -(-k // 16) * 16), **i8)[:, :k], torch.zeros(M, **f32))
+        self.residual, self.h, self.normed = (torch.zeros((M, H), **bf) for _ in range(3))
+        self.x8, self.o8, self.h8 = codes(H), codes(Q), codes(F)
+        qkv = torch.zeros((M, Q + 2 * KV), **f32)
+        self.qkv, self.y_qkv = qkv, [qkv[:, :Q], qkv[:, Q:Q + KV], qkv[:, Q + KV:]]
+        self.y_o, self.y_down = torch.zeros((M, H), **f32), torch.zeros((M, H), **f32)
+        self.gate_up = None if self.experts else torch.zeros((M, 2 * F), **bf)
+        self.argmax = torch.empty((M,), dtype=torch.int32, device="cuda")
+        self.logits = torch.empty((M, V), **f32)
+        if self.experts:
+            self.ids = torch.zeros((M, self.top_k), dtype=torch.int32, device="cuda")
+            self.expert_weights = torch.zeros((M, self.top_k), **f32)
+            self.ws_moe = binding.alloc_workspace(
+                max(binding.moe_workspace_bytes(H, F, self.experts, m, self.top_k) for m in range(1, M + 1)))
+        shapes = [(Q + 2 * KV, H), (H, Q)] + ([] if self.experts else [(2 * F, H), (H, F)])
+        self.ws_i8 = binding.alloc_workspace(
+            max(binding.i8_workspace_bytes(n, k, m) for n, k in shapes for m in range(1, M + 1)))
+        self.ws_head = binding.alloc_workspace(binding.lmhead_workspace_bytes(V, M))
+        self.caches = None
+        self.tree_mask = self.positions = None
+
+    def layer_weight_bytes(self) -> int:
+        L = self.layers[0][0]
+        dense = [L.moe] if self.experts else [L.gate_up, L.down]
+        return sum(w.nbytes for w in [L.qkv, L.o] + dense) + (0 if L.router is None else 2 * L.router.numel())
+
+    def layer_calls(self, li: int, m: int, copy: int = 0, stream=None) -> list:
+        """Layer li's calls at width m, their arguments marshalled."""
+        L, H, F, c, s = self.layers[copy][li], self.hidden, self.inter, self.x8, dict(stream=stream)
+        norm = dict(eps=self.norm_eps, codes=c[0], scales=c[1], **s)
+        # the first layer takes the embedded rows as the residual stream
+        x, r = (None, self.x_in) if li == 0 else (self.y_down, self.residual)
+        calls = [binding.prepare_add_rmsnorm(x, r, self.residual, L.attn_norm, m, H, **norm),
+                 binding.prepare_i8_gemm(L.qkv, *c, m, self.qkv, self.ws_i8, **s)]
+        if self.caches:
+            calls += self.attention_calls(li, m, stream)
+        calls += [binding.prepare_i8_quantize(self.attn_out if self.caches else self.x_o, m, self.qdim, *self.o8, **s),
+                  binding.prepare_i8_gemm(L.o, *self.o8, m, self.y_o, self.ws_i8, **s)]
+        if self.experts:
+            return calls + [
+                binding.prepare_add_rmsnorm(self.y_o, self.residual, self.residual, L.mlp_norm, m, H, out=self.normed,
+                                            **norm),
+                binding.prepare_moe_route(self.normed, L.router, m, self.ids, self.expert_weights, self.ws_moe, **s),
+                binding.prepare_moe_mlp(L.moe, *c, m, self.ids, self.expert_weights, self.y_down, self.ws_moe, **s)]
+        gate, up = self.gate_up[:, :F], self.gate_up[:, F:]
+        return calls + [
+            binding.prepare_add_rmsnorm(self.y_o, self.residual, self.residual, L.mlp_norm, m, H, **norm),
+            binding.prepare_i8_gemm(L.gate_up, *c, m, self.gate_up, self.ws_i8, **s),
+            binding.prepare_silu_mul(gate, up, m, F, codes=self.h8[0], scales=self.h8[1], **s),
+            binding.prepare_i8_gemm(L.down, *self.h8, m, self.y_down, self.ws_i8, **s)]
+
+    def final_call(self, m: int, stream=None):
+        """The last residual sum and norm: the head's rows."""
+        return binding.prepare_add_rmsnorm(self.y_down, self.residual, None, self.final_norm, m, self.hidden,
+                                           eps=self.norm_eps, out=self.h, stream=stream)
+
+    def launch_layers(self, m: int, copy: int = 0, stream=None) -> None:
+        for call in self.prepare_round(m, copy, stream=stream)[0]:
+            call()
+
+    def prepare_round(self, m: int, copy: int, want_logits: bool = False, stream=None):
+        layers = [call for li in range(self.n_layers) for call in self.layer_calls(li, m, copy, stream)]
+        head = binding.prepare_lmhead(self.heads[copy], self.h, m, self.argmax, self.logits if want_logits else None,
+                                      self.ws_head, stream)
+        return layers + [self.final_call(m, stream)], head
