@@ -39,45 +39,25 @@ I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
     I8Plan p{};
     const int64_t steps = i8_steps(k), stages = steps / 2, tiles = i8_tiles(n);
     const auto over = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    const int64_t weight = (int64_t)n * k;
-    const bool wide = tiles > cus, few = tiles <= cus + cus / 4 && weight >= 24 << 20;
     p.splits = 1;
-    // few: long sums over few columns, which streams read x too often for
-    const bool stream = m <= 16 || (m <= 32 && !few && (m <= 24 || weight < 24 << 20)) ||
-                        (m > 32 && m <= 48 && !few) || (m <= 64 && weight < 2 << 20);
-    if (stream) {
-        p.kind = m <= 16 ? (wide ? kI8Stream16x2 : kI8Stream16x1)
-                 : m <= 32 ? (wide ? kI8Stream32x2 : kI8Stream32x1) : (wide ? kI8Stream64x2 : kI8Stream64x1);
-        // 4 to 8 waves, so that their rings' last turns are full (40 fragments, rings
-        // of 4: 5 waves 11.9 us, 4 12.7)
-        const int ring = p.kind == kI8Stream16x1 ? 8 : p.kind == kI8Stream64x2 ? 2 : 4;
-        int64_t least = INT64_MAX;
-        for (int w = 4; w <= 8; ++w) {
-            const int64_t turns = over(steps, (int64_t)w * ring) * w * ring;
-            if (turns < least) least = turns, p.waves = w;
-        }
-        p.groups = over(tiles, wide ? 2 : 1);
-        p.fits = p.groups * 64 * p.waves <= UINT32_MAX;
-        return p;
-    }
     struct Shape {
         I8Kind kind;
         int rows, cols;
-        double kb, own;             // of a stage: KB loaded, us alone on a CU
+        double own;                 // us of a stage alone on a CU; two share it in 1.46 times that
     };
-    static const Shape shapes[] = {{kI8Tile32x64, 32, 64, 12, .25}, {kI8Tile64x64, 64, 64, 16, .26},
-                                   {kI8Tile64x128, 64, 128, 24, .45}, {kI8Tile128x128, 128, 128, 32, .8}};
+    static const Shape shapes[] = {{kI8Tile32x64, 32, 64, .3}, {kI8Tile64x64, 64, 64, .26},
+                                   {kI8Tile64x128, 64, 128, .4}, {kI8Tile128x128, 128, 128, .67}};
     double best = 1e300;
     for (const Shape &c : shapes) {
+        if (m <= 16) break;
         if (m <= 32 ? c.rows != 32 : c.rows == 32) continue;
         const int64_t of = over(m, c.rows) * over(n, c.cols);
         for (int s = 1; s <= 8; ++s) {
             if (s > 1 && (!split || stages < 4 * s || of * s > 4 * cus || of > kI8MaxSplitTiles)) break;
-            const int64_t all = of * s, at_once = all < 2 * cus ? all : 2 * cus;
-            const double loads = at_once * c.kb * 1.024e-3 / 16.5 * (256. / cus);
-            const double stage = at_once > cus ? 1.4 * c.own : c.own;
-            const double us = (double)over(all, 2 * cus) * (4 + (double)stages / s * (loads > stage ? loads : stage)) +
-                              (s > 1 ? 2 + .3e-6 * 4 * all * c.rows * c.cols : 0);
+            const int64_t all = of * s;
+            const double stage = all > cus ? 1.46 * c.own : c.own;
+            const double us = (double)over(all, 2 * cus) * (3.6 + (double)stages / s * stage) +
+                              (s > 1 ? 2.2 + .28e-6 * 4 * all * c.rows * c.cols : 0);
             if (us >= best) continue;
             best = us;
             p.kind = c.kind;
@@ -90,10 +70,32 @@ I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
             }
         }
     }
+    // Streams: a workgroup takes its columns and all rows of x past it at some 33 GB/s,
+    // which up to 16 rows is always the shorter (1 / 16 rows of 2560x9728 6.7 / 9.9 us,
+    // tiles 10.0 / 10.2; 32 rows 13.9 and 10.5; 32 rows of 4096x4096 7.1 and 10.2).
+    const bool wide = tiles > cus;
+    const int64_t groups = over(tiles, wide ? 2 : 1);
+    if (m <= 16 || (m <= 64 && 2 + 30e-6 * (m + (wide ? 32 : 16)) * k * over(groups, cus) <= best)) {
+        p = I8Plan{};
+        p.splits = 1;
+        p.kind = m <= 16 ? (wide ? kI8Stream16x2 : kI8Stream16x1)
+                 : m <= 32 ? (wide ? kI8Stream32x2 : kI8Stream32x1) : (wide ? kI8Stream64x2 : kI8Stream64x1);
+        // 4 to 8 waves, so that their rings' last turns are full (40 fragments, rings
+        // of 4: 5 waves 11.9 us, 4 12.7)
+        const int ring = p.kind == kI8Stream16x1 ? 8 : p.kind == kI8Stream64x2 ? 2 : 4;
+        int64_t least = INT64_MAX;
+        for (int w = 4; w <= 8; ++w) {
+            const int64_t turns = over(steps, (int64_t)w * ring) * w * ring;
+            if (turns < least) least = turns, p.waves = w;
+        }
+        p.groups = groups;
+        p.fits = p.groups * 64 * p.waves <= UINT32_MAX;
+        return p;
+    }
     // 256 x 256: whole rounds of one workgroup per CU, then the rest in quarters, if that
     // is the shorter
     const int64_t big = over(m, 256) * over(n, 256), rest = big % cus;
-    const double whole = 5 + 2.1 * stages, quarters = (double)over(4 * rest, cus) * (4 + .65 * stages);
+    const double whole = 7 + 1.67 * stages, quarters = (double)over(4 * rest, cus) * (4 + .57 * stages);
     const bool cut = rest != 0 && quarters < whole;
     const double us = (double)(cut ? big / cus : over(big, cus)) * whole + (cut ? quarters : 0);
     if (m > 64 && us < best) {
@@ -122,6 +124,7 @@ MoePlan moe_plan(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int3
     // two pieces of work or more (2048 columns, 8 / 48 slots of 768: one part 8.8 / 24.1
     // us, two 9.4 / 19.4, four 13.3 / 22.9).
     const int64_t tiles = i8_tiles(hidden), work = ((int64_t)slots < experts ? (int64_t)slots : experts) * ((i8_steps(inter) + 7) / 8);
+    p.inside = slots <= kDownWaves && (int64_t)slots * (p.ldh + 16) <= kMoeInside;
     p.parts = 1;
     if (slots <= kMoeGroup && tiles <= kMoeSplitTiles)
         while (p.parts < kMoeMaxParts && tiles * p.parts * 2 <= cus && work >= 32 * p.parts) p.parts *= 2;
@@ -488,6 +491,7 @@ int dspk_moe_mlp(const dspk_i8_weight *gate, const dspk_i8_weight *up, const dsp
     A.ctr = (uint32_t *)(ws + dspk::kMoeCtr);
     A.top = (uint32_t *)(ws + p.off_top);
     A.parts = p.parts;
+    A.inside = p.inside;
     A.part = (int32_t *)(ws + p.off_part);
     A.down_ctr = (uint32_t *)(ws + dspk::kMoeDown);
     return launch_result(dspk::launch_moe_mlp(A, (hipStream_t)stream), who);

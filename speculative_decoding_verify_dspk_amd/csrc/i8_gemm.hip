@@ -331,8 +331,8 @@ template <int WR, int WC, int TX, int TW, int KS, int NB, int OCC, bool BF16>
 __global__ __launch_bounds__(64 * WR * WC, OCC) void i8_tile_kernel(const I8GemmArgs A) {
     using T = Tile<WR, WC, TX, TW, KS, NB>;
     __shared__ __attribute__((aligned(1024))) char b0[T::STAGE], b1[T::STAGE], b2[NB > 2 ? T::STAGE : 16],
-        b3[NB > 3 ? T::STAGE : 16], b4[NB > 4 ? T::STAGE : 16];
-    char *const every[5] = {b0, b1, b2, b3, b4};
+        b3[NB > 3 ? T::STAGE : 16];
+    char *const every[4] = {b0, b1, b2, b3};
     Buffers ring[NB];
 #pragma unroll
     for (int u = 0; u < NB; ++u) ring[u] = {every[u], every[u] + T::XB};
@@ -402,10 +402,10 @@ hipError_t launch_i8_gemm(const I8GemmArgs &a, const I8Plan &p, hipStream_t s) {
         case kI8Stream32x2: return launch_stream<2, 2, 4>(a, p, s);
         case kI8Stream64x1: return launch_stream<4, 1, 4>(a, p, s);
         case kI8Stream64x2: return launch_stream<4, 2, 2>(a, p, s);
-        case kI8Tile32x64: return launch_tile<1, 4, 2, 1, 128, 5, 2>(a, p, s);
-        case kI8Tile64x64: return launch_tile<4, 1, 1, 4, 128, 5, 2>(a, p, s);
-        case kI8Tile64x128: return launch_tile<2, 2, 2, 4, 128, 3, 2>(a, p, s);
-        case kI8Tile128x128: return launch_tile<2, 2, 4, 4, 128, 2, 2>(a, p, s);
+        case kI8Tile32x64: return launch_tile<1, 4, 2, 1, 128, 4, 2>(a, p, s);
+        case kI8Tile64x64: return launch_tile<4, 2, 1, 2, 128, 4, 2>(a, p, s);
+        case kI8Tile64x128: return launch_tile<2, 4, 2, 2, 128, 3, 2>(a, p, s);
+        case kI8Tile128x128: return launch_tile<2, 4, 4, 2, 128, 2, 2>(a, p, s);
         case kI8Tile256x256: return launch_big(a, p, s);
     }
     return hipErrorInvalidValue;

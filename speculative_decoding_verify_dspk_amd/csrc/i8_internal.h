@@ -102,11 +102,14 @@ constexpr int kMoeMaxSlots = kMoeMaxRows * kMoeMaxTop;
 // then the router's scores, h, its codes and their scales, and the largest magnitude of
 // each row's tiles, the down workgroups' sums, each written before it is read.
 constexpr int kMoeGroup = 512;      // slots that a down workgroup has sums for at a time
+constexpr int kDownWaves = 16;      // of a down workgroup
+constexpr int kMoeInside = 48 << 10;        // codes of h that a down workgroup's LDS holds
 constexpr int kMoeMaxParts = 8, kMoeSplitTiles = 512;      // tiles of 16 columns whose sums are split
 constexpr size_t kMoeCtr = 256, kMoeDown = kMoeCtr + 4 * kMoeMaxExperts, kMoeHead = kMoeDown + 4 * kMoeSplitTiles;
 struct MoePlan {
     int64_t ldh;                    // floats of a row of h, bytes of a row of its codes
     int32_t parts;                  // workgroups that share 16 columns of y
+    bool inside;                    // h becomes codes in the down workgroups
     size_t off_scores, off_h, off_h8, off_h_scales, off_top, off_part, ws_bytes;
 };
 MoePlan moe_plan(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k, int cus);
@@ -138,7 +141,7 @@ struct MoeArgs {
     float *h_scales;
     uint32_t *ctr;                  // arrivals of each expert's columns
     uint32_t *top;                  // [m * top_k][tiles of 16 columns]: largest |h|, as bits
-    int32_t parts;                  // see MoePlan
+    int32_t parts, inside;          // see MoePlan
     int32_t *part;                  // their sums [tile][part][slot][16]
     uint32_t *down_ctr;             // their arrivals
 };

@@ -3,12 +3,14 @@
 //
 //   route  scores of 16 experts per workgroup (bf16 matrix instructions, K split
 //          over its waves); the last workgroup to arrive chooses, a wave per row.
-//   up     a workgroup per chosen expert and 16 columns of gate and up, over the
-//          tokens that chose it: h = silu(gate) * up in fp32; the expert's last
-//          workgroup to arrive turns h's rows into codes.
+//   up     a workgroup per chosen expert and 32 columns of gate and up, over the
+//          tokens that chose it: h = silu(gate) * up in fp32.
 //   down   a workgroup per 16 columns of y: its waves share out the chosen experts and
 //          their K, add whole-number sums in LDS (exact in any order), and then each
 //          token's slots in their order.
+// Between them h's rows become codes: where LDS holds them all, every down workgroup
+// does that for itself (some 1 us); else the last of an expert's up workgroups to arrive
+// does (some 3 us of stores, arrivals and loads that pass between dies).
 // Each expert's weights are read once for up to 32 of its rows.
 #include <hip/hip_runtime.h>
 
@@ -201,7 +203,6 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
 }
 
 // -------------------------------------------------------------------- experts
-constexpr int kDownWaves = 16;
 
 // The slots (token * top_k + j) of [first, last) that chose expert e, listed in `slots`
 // by every wave for itself (they write the same), and their number.
@@ -262,8 +263,8 @@ __device__ __forceinline__ void stream(const char *const (&wt)[T], const int8_t 
 }
 
 // Rows [base, base + 16 MT) of the expert's list into h, CT tiles of 16 columns from
-// `tile0` on.
-template <int CT, int MT, int W>
+// `tile0` on.  INSIDE: they become codes inside the down workgroups.
+template <int CT, int MT, int W, bool INSIDE>
 __device__ __forceinline__ void up_rows(const MoeArgs &A, const uint16_t *slots, int count, int base, int e, int tile0,
                                         int tiles, i32x4 (*part)[2 * CT * 2][64]) {
     const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
@@ -300,27 +301,30 @@ __device__ __forceinline__ void up_rows(const MoeArgs &A, const uint16_t *slots,
         const float xs = A.x_scales[slot / (uint32_t)A.top_k];
         const float *gs = A.gate_scales + (int64_t)e * A.inter, *us = A.up_scales + (int64_t)e * A.inter;
         float h[4];
-        uint32_t top = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 4; ++q)
             h[q] = col + q < A.inter ? silu((float)a[q] * xs * gs[col + q]) * ((float)b[q] * xs * us[col + q]) : 0.f;
-            top = max(top, magnitude(h[q]));
-        }
-        top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        if (at < count) {
-            float *p = A.h + (int64_t)slot * A.ldh + col;
-            share(p, h[0], h[1]);
-            share(p + 2, h[2], h[3]);
-            if (j == 0)
-                __hip_atomic_store(A.top + (int64_t)slot * tiles + tile0 + t, top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        float *p = A.h + (int64_t)slot * A.ldh + col;
+        if constexpr (INSIDE) {
+            if (at < count) *(f4 *)p = f4{h[0], h[1], h[2], h[3]};
+        } else {
+            uint32_t top = max(max(magnitude(h[0]), magnitude(h[1])), max(magnitude(h[2]), magnitude(h[3])));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+            if (at < count) {
+                share(p, h[0], h[1]);
+                share(p + 2, h[2], h[3]);
+                if (j == 0)
+                    __hip_atomic_store(A.top + (int64_t)slot * tiles + tile0 + t, top, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+            }
         }
     }
     __syncthreads();
 }
 
 // CT: tiles of 16 columns of a workgroup; W: its waves.
-template <int CT, int W>
+template <int CT, int W, bool INSIDE>
 __global__ __launch_bounds__(64 * W, 4) void moe_up_kernel(const MoeArgs A) {
     __shared__ uint16_t slots[kMoeMaxSlots];
     __shared__ i32x4 part[W][2 * CT * 2][64];
@@ -334,10 +338,11 @@ __global__ __launch_bounds__(64 * W, 4) void moe_up_kernel(const MoeArgs A) {
     if (count == 0 || (by_slot && slots[0] != blockIdx.y)) return;
     for (int base = 0; base < count; base += 32) {
         if (count - base <= 16)
-            up_rows<CT, 1, W>(A, slots, count, base, e, tile0, tiles, part);
+            up_rows<CT, 1, W, INSIDE>(A, slots, count, base, e, tile0, tiles, part);
         else
-            up_rows<CT, 2, W>(A, slots, count, base, e, tile0, tiles, part);
+            up_rows<CT, 2, W, INSIDE>(A, slots, count, base, e, tile0, tiles, part);
     }
+    if constexpr (INSIDE) return;
     if (!last_to_arrive(A.ctr + e, gridDim.x)) return;
     // this expert's h is whole: 32 rows at a time, the largest magnitude of each from its
     // tiles', then the codes
@@ -378,15 +383,73 @@ __global__ __launch_bounds__(64 * W, 4) void moe_up_kernel(const MoeArgs A) {
 
 // 16 columns of y, by the `parts` workgroups of blockIdx.y together: each takes every
 // so-many-th piece of work (an expert and a part of K); the last to arrive adds the
-// others' whole-number sums.  Slots go by groups of whole tokens that LDS has sums for
-// (parts = 1 where that takes more than one).
+// others' whole-number sums.
 constexpr int kDownChunk = 8;       // most fragments of a piece of work
+typedef int32_t Sums[16];
 
+// The n slots' sums of all parts; false for a workgroup that is not the last.
+__device__ __forceinline__ bool join_parts(const MoeArgs &A, Sums *sums, int n) {
+    const int tile = blockIdx.x, parts = gridDim.y;
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));             // addresses are computed here, not held through the products
+    if (parts == 1) return true;
+    int32_t *const p = A.part + (int64_t)tile * parts * n * 16;
+    for (int i = t; i < n * 8; i += 64 * kDownWaves)
+        share(p + (int64_t)blockIdx.y * n * 16 + 2 * i, sums[0][2 * i], sums[0][2 * i + 1]);
+    if (!last_to_arrive(A.down_ctr + tile, parts)) return false;
+    for (int i = t; i < n * 8; i += 64 * kDownWaves) {
+        int2 v = make_int2(sums[0][2 * i], sums[0][2 * i + 1]);
+        for (int o = 0; o < parts; ++o)
+            if (o != (int)blockIdx.y) {
+                const int2 u = shared2(p + (int64_t)o * n * 16 + 2 * i);
+                v.x += u.x;
+                v.y += u.y;
+            }
+        sums[0][2 * i] = v.x;
+        sums[0][2 * i + 1] = v.y;
+    }
+    __syncthreads();
+    return true;
+}
+
+// Rows i0 .. of y from their n slots' sums, all slots' scales in one go: sums become
+// values, weights those of the slots in use.  d: the scale of this thread's first value,
+// if it is loaded already.
+template <bool BF16, bool LOADED>
+__device__ __forceinline__ void add_slots(const MoeArgs &A, Sums *sums, const int32_t *ids, float *weights,
+                                          const float *scales, int i0, int n, float d) {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));             // as above
+    for (int i = t; i < n * 16; i += 64 * kDownWaves) {
+        const int slot = i / 16, id = ids[slot], col = blockIdx.x * kI8Cols + (i & 15);
+        float p = id == -1 ? 0.f : __uint_as_float(0x7fc00000u);
+        if ((uint32_t)id < (uint32_t)A.experts && col < A.hidden)
+            p = (float)sums[0][i] * scales[slot] * (LOADED ? d : A.down_scales[(int64_t)id * A.hidden + col]);
+        sums[0][i] = __float_as_int(p);
+    }
+    if (t < n) weights[t] = ids[t] == -1 ? 0.f : A.weights[(int64_t)i0 * A.top_k + t];
+    __syncthreads();
+    for (int i = t; i < n / A.top_k * 16; i += 64 * kDownWaves) {
+        const int row = i / 16, col = blockIdx.x * kI8Cols + (i & 15), slot = row * A.top_k;
+        if (col >= A.hidden) continue;
+        float y = 0.f;
+        for (int q = 0; q < A.top_k; ++q) y += weights[slot + q] * __int_as_float(sums[slot + q][i & 15]);
+        const int64_t at = (int64_t)(i0 + row) * A.ldy + col;
+        if constexpr (BF16)
+            ((uint16_t *)A.y)[at] = to_bf16(y);
+        else
+            ((float *)A.y)[at] = y;
+    }
+}
+
+// Slots go by groups of whole tokens that LDS has sums for (parts = 1 where that takes
+// more than one).
 template <bool BF16>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeArgs A) {
-    __shared__ int32_t sums[kMoeGroup][16];
+    __shared__ Sums sums[kMoeGroup];
     __shared__ int32_t ids[kMoeGroup];
     __shared__ int32_t first[kMoeMaxExperts];      // the first slot of the group that chose an expert
+    __shared__ float weights[kMoeGroup];
     __shared__ uint16_t chosen[kMoeGroup];
     __shared__ uint16_t lists[kDownWaves][kMoeGroup];
     const int t = threadIdx.x, lane = t & 63, c = lane & 15, j = lane >> 4, tile = blockIdx.x, parts = gridDim.y;
@@ -403,7 +466,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeArgs
             ids[i] = e;
             if ((uint32_t)e < (uint32_t)A.experts) atomicMin(&first[e], i);
         }
-        for (int i = t; i < n * 16; i += 64 * kDownWaves) (&sums[0][0])[i] = 0;
+        for (int i = t; i < n * 16; i += 64 * kDownWaves) sums[0][i] = 0;
         __syncthreads();
         int active = 0;                            // the chosen experts, listed alike by every wave and part
         for (int k0 = 0; k0 < n; k0 += 64) {
@@ -431,44 +494,105 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeArgs
             }
         }
         __syncthreads();
-        if (parts > 1) {
-            int32_t *const p = A.part + (int64_t)tile * parts * n * 16;
-            for (int i = t; i < n * 8; i += 64 * kDownWaves)
-                share(p + (int64_t)blockIdx.y * n * 16 + 2 * i, (&sums[0][0])[2 * i], (&sums[0][0])[2 * i + 1]);
-            if (!last_to_arrive(A.down_ctr + tile, parts)) return;
-            for (int i = t; i < n * 8; i += 64 * kDownWaves) {
-                int2 v = make_int2((&sums[0][0])[2 * i], (&sums[0][0])[2 * i + 1]);
-                for (int o = 0; o < parts; ++o)
-                    if (o != (int)blockIdx.y) {
-                        const int2 u = shared2(p + (int64_t)o * n * 16 + 2 * i);
-                        v.x += u.x;
-                        v.y += u.y;
-                    }
-                (&sums[0][0])[2 * i] = v.x;
-                (&sums[0][0])[2 * i + 1] = v.y;
-            }
-            __syncthreads();
-        }
-        for (int i = t; i < n / A.top_k * 16; i += 64 * kDownWaves) {
-            const int row = i / 16, col = tile * kI8Cols + (i & 15);
-            if (col >= A.hidden) continue;
-            float y = 0.f;
-            for (int q = 0; q < A.top_k; ++q) {
-                const int slot = row * A.top_k + q, id = ids[slot];
-                if (id == -1) continue;
-                float p = __uint_as_float(0x7fc00000u);
-                if ((uint32_t)id < (uint32_t)A.experts)
-                    p = (float)sums[slot][i & 15] * A.h_scales[lo + slot] * A.down_scales[(int64_t)id * A.hidden + col];
-                y += A.weights[lo + slot] * p;
-            }
-            const int64_t at = (i0 + row) * A.ldy + col;
-            if constexpr (BF16)
-                ((uint16_t *)A.y)[at] = to_bf16(y);
-            else
-                ((float *)A.y)[at] = y;
-        }
+        if (!join_parts(A, sums, n)) return;
+        add_slots<BF16, false>(A, sums, ids, weights, A.h_scales + lo, i0, n, 0.f);
         __syncthreads();
     }
+}
+
+// Up to 16 slots whose codes LDS holds: a wave turns a row of h into codes while its
+// first piece of the weights is on its way, and finds the pieces of work from the ids
+// in its registers.
+constexpr int kHeld = 4;            // quads of a row of h that a lane holds
+template <bool BF16>
+__global__ __launch_bounds__(64 * kDownWaves) void moe_down_few_kernel(const MoeArgs A) {
+    __shared__ __attribute__((aligned(16))) int8_t codes[kMoeInside];
+    __shared__ float scales[kDownWaves];
+    __shared__ Sums sums[kDownWaves];
+    __shared__ int32_t ids[kDownWaves];
+    __shared__ float weights[kDownWaves];
+    const int t = threadIdx.x, lane = t & 63, c = lane & 15, j = lane >> 4, tile = blockIdx.x, parts = gridDim.y;
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6), n = A.m * A.top_k;
+    const int steps = (int)i8_steps(A.inter), tiles = gridDim.x, chunks = (steps + kDownChunk - 1) / kDownChunk;
+    const int each = (steps + chunks - 1) / chunks;
+    const int stride = (int)A.ldh + 16, quads = (int)A.ldh / 4;          // rows of codes, 16 of them in different banks
+    const int id = lane < n ? A.ids[lane] : -1, own = t < 16 * n ? A.ids[t / 16] : -1;
+    const f4 *const row = (const f4 *)(A.h + (int64_t)min(w, n - 1) * A.ldh);
+    f4 v[kHeld];
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q) v[q] = row[min(64 * q + lane, quads - 1)];
+    __builtin_amdgcn_sched_barrier(0);
+    bool first = (uint32_t)id < (uint32_t)A.experts;       // no lane before has the same expert
+#pragma unroll
+    for (int q = 0; q < kDownWaves - 1; ++q) first &= (lane <= q) | (__builtin_amdgcn_readlane(id, q) != id);
+    const uint64_t experts = __ballot(first);
+    const int active = __popcll(experts), rank = __popcll(experts & ((1ull << lane) - 1));
+    const int all = active * chunks, by = kDownWaves * parts;
+    i32x4 f[kDownChunk];
+    int item = w * parts + blockIdx.y, e = 0, s0 = 0, end = 0;
+    const auto fetch = [&]() __attribute__((always_inline)) {
+        const int chunk = item / active, at = item - chunk * active;
+        e = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)__ballot(first && rank == at)) - 1);
+        s0 = chunk * each, end = min(s0 + each, steps);
+        const char *const wt = A.down + ((int64_t)e * tiles + tile) * steps * kI8Frag + 16 * lane;
+#pragma unroll
+        for (int u = 0; u < kDownChunk; ++u)
+            f[u] = __builtin_nontemporal_load((const i32x4 *)(wt + (int64_t)min(s0 + u, end - 1) * kI8Frag));
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (item < all) fetch();
+    // the scale of this thread's slot and column
+    const int col = tile * kI8Cols + (t & 15);
+    const float d = (uint32_t)own < (uint32_t)A.experts && col < A.hidden ? A.down_scales[(int64_t)own * A.hidden + col] : 0.f;
+    if (w == 0 && lane < n) ids[lane] = id;
+    if (t < 16 * kDownWaves) sums[0][t] = 0;
+    if (w < n) {
+        uint32_t top = 0;
+        const auto most = [&](const f4 &x) {
+            top = max(top, max(max(magnitude(x[0]), magnitude(x[1])), max(magnitude(x[2]), magnitude(x[3]))));
+        };
+#pragma unroll
+        for (int q = 0; q < kHeld; ++q) most(v[q]);
+        for (int q = 64 * kHeld + lane; q < quads; q += 64) most(row[q]);
+        const Step8 st = step8(wave_max(top));
+        uint32_t *const out = (uint32_t *)(codes + w * stride);
+#pragma unroll
+        for (int q = 0; q < kHeld; ++q)
+            if (64 * q + lane < quads) out[64 * q + lane] = codes8(v[q][0], v[q][1], v[q][2], v[q][3], st);
+        for (int q = 64 * kHeld + lane; q < quads; q += 64) {
+            const f4 x = row[q];
+            out[q] = codes8(x[0], x[1], x[2], x[3], st);
+        }
+        if (lane == 0) scales[w] = st.scale;
+    }
+    __syncthreads();
+    while (item < all) {
+        // column c of the product is the c-th slot that chose e
+        const uint64_t mine = __ballot(id == e);
+        const int count = __popcll(mine);
+        int slot = 0, seen = 0;
+#pragma unroll
+        for (int q = 0; q < kDownWaves; ++q)
+            if (mine >> q & 1) {
+                slot = seen == c ? q : slot;
+                ++seen;
+            }
+        const int8_t *const x = codes + slot * stride + 16 * j;
+        i32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < kDownChunk; ++u) {
+            const int r = (s0 + u) * kI8K;                 // past ldh, where the weights are zeros, the first codes
+            if (s0 + u < end) acc = mfma64(f[u], *(const i32x4 *)(x + (r + 16 * j < (int)A.ldh ? r : 0)), acc);
+        }
+        item += by;
+        if (item < all) fetch();
+        if (c < count)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) atomicAdd(&sums[slot][4 * j + q], acc[q]);
+    }
+    __syncthreads();
+    if (!join_parts(A, sums, n)) return;
+    add_slots<BF16, true>(A, sums, ids, weights, scales, 0, n, d);
 }
 
 }  // namespace
@@ -487,22 +611,31 @@ hipError_t launch_moe_route(const RouteArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_moe_mlp(const MoeArgs &a, hipStream_t s) {
+template <bool INSIDE>
+hipError_t launch_inside(const MoeArgs &a, hipStream_t s) {
     const int slots = a.m * a.top_k, most = slots < a.experts ? slots : a.experts;
     // 32 columns of gate and up per workgroup; its waves take 8 fragments or more each
     // (1 / 6 rows of 8 of 128 experts 2048 -> 768, 32 rows of 2 of 8 4096 -> 14336: four
     // waves 9.5 / 27.4 / 179 us, eight 9.8 / 30.0 / 173; 16 columns and four 10.1 / 29.4 / 193)
     const dim3 up((unsigned)((i8_tiles(a.inter) + 1) / 2), most);
     if (i8_steps(a.hidden) >= 48)
-        hipLaunchKernelGGL((moe_up_kernel<2, 8>), up, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((moe_up_kernel<2, 8, INSIDE>), up, dim3(512), 0, s, a);
     else
-        hipLaunchKernelGGL((moe_up_kernel<2, 4>), up, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((moe_up_kernel<2, 4, INSIDE>), up, dim3(256), 0, s, a);
     const dim3 down((unsigned)i8_tiles(a.hidden), a.parts), block(64 * kDownWaves);
-    if (a.y_bf16)
+    if (INSIDE && a.y_bf16)
+        hipLaunchKernelGGL((moe_down_few_kernel<true>), down, block, 0, s, a);
+    else if (INSIDE)
+        hipLaunchKernelGGL((moe_down_few_kernel<false>), down, block, 0, s, a);
+    else if (a.y_bf16)
         hipLaunchKernelGGL((moe_down_kernel<true>), down, block, 0, s, a);
     else
         hipLaunchKernelGGL((moe_down_kernel<false>), down, block, 0, s, a);
     return hipGetLastError();
+}
+
+hipError_t launch_moe_mlp(const MoeArgs &a, hipStream_t s) {
+    return a.inside ? launch_inside<true>(a, s) : launch_inside<false>(a, s);
 }
 
 }  // namespace dspk
