@@ -266,8 +266,8 @@ __device__ __forceinline__ void stream(const char *const (&wt)[T], const int8_t 
 // `tile0` on.  INSIDE: they become codes inside the down workgroups.
 template <int CT, int MT, int W, bool INSIDE>
 __device__ __forceinline__ void up_rows(const MoeArgs &A, const uint16_t *slots, int count, int base, int e, int tile0,
-                                        int tiles, i32x4 (*part)[2 * CT * 2][64]) {
-    const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
+                                        int tiles, i32x4 (*part)[2 * CT * 2][64], float *scales) {
+    int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), steps = (int)i8_steps(A.hidden);
     const int8_t *xr[MT];
 #pragma unroll
@@ -285,7 +285,20 @@ __device__ __forceinline__ void up_rows(const MoeArgs &A, const uint16_t *slots,
     for (int t = 0; t < 2 * CT; ++t)
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[t][i] = i32x4{0, 0, 0, 0};
+    // the scales of the columns of gate and up (wave 0) and of the rows (wave 1), on their
+    // way into LDS from here
+    constexpr int COLS = 16 * CT;
+    static_assert(2 * COLS <= 64 && W > 1, "a lane each");
+    const float *const mine = w == 0 ? (lane < COLS ? A.gate_scales : A.up_scales) + (int64_t)e * A.inter +
+                                           min(tile0 * kI8Cols + lane % COLS, A.inter - 1)
+                                     : A.x_scales + slots[min(base + lane, count - 1)] / (uint32_t)A.top_k;
+    if (w < 2)
+        __builtin_amdgcn_global_load_lds(mine, (__attribute__((address_space(3))) void *)(scales + 64 * w), 4, 0, 0);
     stream<2 * CT, MT, MT == 1 ? 4 : 2>(wt, xr, A.hidden, w, W, steps, acc);
+    __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));          // vmcnt(0): they are there
+    lane = threadIdx.x;
+    asm volatile("" : "+v"(lane));          // addresses are computed here, not held through the products
+    lane &= 63, c = lane & 15, j = lane >> 4;
 #pragma unroll
     for (int t = 0; t < 2 * CT; ++t)
 #pragma unroll
@@ -298,12 +311,11 @@ __device__ __forceinline__ void up_rows(const MoeArgs &A, const uint16_t *slots,
 #pragma unroll
         for (int q = 1; q < W; ++q) a += part[q][2 * t * MT + i][lane], b += part[q][(2 * t + 1) * MT + i][lane];
         const int at = base + 16 * i + c, slot = slots[min(at, count - 1)];
-        const float xs = A.x_scales[slot / (uint32_t)A.top_k];
-        const float *gs = A.gate_scales + (int64_t)e * A.inter, *us = A.up_scales + (int64_t)e * A.inter;
+        const float xs = scales[64 + 16 * i + c], *const gs = scales + 16 * t + 4 * j, *const us = gs + COLS;
         float h[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            h[q] = col + q < A.inter ? silu((float)a[q] * xs * gs[col + q]) * ((float)b[q] * xs * us[col + q]) : 0.f;
+            h[q] = col + q < A.inter ? silu((float)a[q] * xs * gs[q]) * ((float)b[q] * xs * us[q]) : 0.f;
         float *p = A.h + (int64_t)slot * A.ldh + col;
         if constexpr (INSIDE) {
             if (at < count) *(f4 *)p = f4{h[0], h[1], h[2], h[3]};
@@ -328,6 +340,7 @@ template <int CT, int W, bool INSIDE>
 __global__ __launch_bounds__(64 * W, 4) void moe_up_kernel(const MoeArgs A) {
     __shared__ uint16_t slots[kMoeMaxSlots];
     __shared__ i32x4 part[W][2 * CT * 2][64];
+    __shared__ float scales[128];
     const int all = A.m * A.top_k, tiles = (int)i8_tiles(A.inter), tile0 = blockIdx.x * CT;
     // blockIdx.y: an expert, or where there are fewer slots than experts, a slot, whose
     // expert is taken by the first one that names it
@@ -338,9 +351,9 @@ __global__ __launch_bounds__(64 * W, 4) void moe_up_kernel(const MoeArgs A) {
     if (count == 0 || (by_slot && slots[0] != blockIdx.y)) return;
     for (int base = 0; base < count; base += 32) {
         if (count - base <= 16)
-            up_rows<CT, 1, W, INSIDE>(A, slots, count, base, e, tile0, tiles, part);
+            up_rows<CT, 1, W, INSIDE>(A, slots, count, base, e, tile0, tiles, part, scales);
         else
-            up_rows<CT, 2, W, INSIDE>(A, slots, count, base, e, tile0, tiles, part);
+            up_rows<CT, 2, W, INSIDE>(A, slots, count, base, e, tile0, tiles, part, scales);
     }
     if constexpr (INSIDE) return;
     if (!last_to_arrive(A.ctr + e, gridDim.x)) return;
