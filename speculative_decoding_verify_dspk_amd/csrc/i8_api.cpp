@@ -80,11 +80,11 @@ I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
         p.splits = 1;
         p.kind = m <= 16 ? (wide ? kI8Stream16x2 : kI8Stream16x1)
                  : m <= 32 ? (wide ? kI8Stream32x2 : kI8Stream32x1) : (wide ? kI8Stream64x2 : kI8Stream64x1);
-        // 4 to 8 waves, so that their rings' last turns are full (40 fragments, rings
-        // of 4: 5 waves 11.9 us, 4 12.7)
+        // 4 to 7 waves (8 never have fewer turns than 4 have), so that their rings' last
+        // turns are full (40 fragments, rings of 4: 5 waves 11.9 us, 4 12.7)
         const int ring = p.kind == kI8Stream16x1 ? 8 : p.kind == kI8Stream64x2 ? 2 : 4;
         int64_t least = INT64_MAX;
-        for (int w = 4; w <= 8; ++w) {
+        for (int w = 4; w <= 7; ++w) {
             const int64_t turns = over(steps, (int64_t)w * ring) * w * ring;
             if (turns < least) least = turns, p.waves = w;
         }

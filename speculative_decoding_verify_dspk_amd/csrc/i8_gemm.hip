@@ -99,21 +99,30 @@ __global__ __launch_bounds__(1024, 4) void i8_stream_kernel(const I8GemmArgs A) 
 #pragma unroll
     for (int u = 0; u < D; ++u) multiply(s0 + u * waves, ring[u]);
 
+    // each thread's four columns of a row; their scales on their way while the sums meet
+    int row, col;
+    float xs, ws[4];
+    auto take = [&](int q) __attribute__((always_inline)) {
+        row = 16 * ((q >> 6) % MT) + (q & 15);
+        col = (tile0 + (q >> 6) / MT) * kI8Cols + 4 * ((q >> 4) & 3);
+        xs = A.x_scales[min(row, A.m - 1)];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ws[e] = A.w_scales[min(col + e, A.n - 1)];
+    };
+    take(threadIdx.x);
 #pragma unroll
     for (int t = 0; t < CT; ++t)
 #pragma unroll
         for (int i = 0; i < MT; ++i) part[((w * CT + t) * MT + i) * 64 + lane] = acc[t][i];
     __syncthreads();
     for (int q = threadIdx.x; q < CT * MT * 64; q += blockDim.x) {
+        if (q != (int)threadIdx.x) take(q);
         i32x4 sum = part[q];
         for (int i = 1; i < waves; ++i) sum += part[i * CT * MT * 64 + q];
-        const int row = 16 * ((q >> 6) % MT) + (q & 15);
-        const int col = (tile0 + (q >> 6) / MT) * kI8Cols + 4 * ((q >> 4) & 3);
         if (row >= A.m || col >= A.n) continue;
-        const float xs = A.x_scales[row];
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = col + e < A.n ? (float)sum[e] * xs * A.w_scales[col + e] : 0.f;
+        for (int e = 0; e < 4; ++e) v[e] = (float)sum[e] * xs * ws[e];
         store4<BF16>(A.y, row * A.ldy + col, col, A.n, A.vec, v);
     }
 }
@@ -188,7 +197,7 @@ struct Buffers {
 template <int WR, int WC, int TX, int TW, int KS, int NB, bool SPLIT, bool BF16>
 __device__ __forceinline__ void tile_work(const I8GemmArgs &A, int row0, int tile0, const Buffers (&ring)[NB]) {
     using T = Tile<WR, WC, TX, TW, KS, NB>;
-    static_assert(NB >= 2 && NB <= 5, "ring");
+    static_assert(NB >= 2 && NB <= 4, "ring");
     constexpr int L = T::XI + T::WI;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wr = w / WC, wc = w % WC;
@@ -234,6 +243,20 @@ __device__ __forceinline__ void tile_work(const I8GemmArgs &A, int row0, int til
     };
     const int xrow = 16 * TX * wr + (lane & 15), j = lane >> 4;
     const int wat = TW * wc * (KS * kI8Cols) + 16 * lane;
+    // Lane l ends with row l % 16 and columns 4 (l / 16) .. + 3 of each 16 x 16 product.
+    // Their scales: small waves' at once, where the registers hold them.
+    constexpr bool EARLY = TX * TW <= 4;
+    float xs[TX], ws[TW][4];
+    auto scales = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < TX; ++i) xs[i] = A.x_scales[min(row0 + xrow + 16 * i, A.m - 1)];
+#pragma unroll
+        for (int t = 0; t < TW; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                ws[t][e] = A.w_scales[min((tile0 + TW * wc + t) * kI8Cols + 4 * j + e, A.n - 1)];
+    };
+    if constexpr (EARLY) scales();
     struct Operands {
         i32x4 a[TW], b[TX];
     };
@@ -306,22 +329,18 @@ __device__ __forceinline__ void tile_work(const I8GemmArgs &A, int row0, int til
                     }
             }
         }
-    // lane l holds row l % 16 and columns 4 (l / 16) .. + 3 of each 16 x 16 product
+    if constexpr (!EARLY) scales();
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
         const int c = (tile0 + TW * wc + t) * kI8Cols + 4 * j;
         if (c >= A.n) continue;
-        float ws[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ws[e] = c + e < A.n ? A.w_scales[c + e] : 0.f;
 #pragma unroll
         for (int i = 0; i < TX; ++i) {
             const int row = row0 + xrow + 16 * i;
             if (row >= A.m) continue;
-            const float xs = A.x_scales[row];
             float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][t][e] * xs * ws[e];
+            for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][t][e] * xs[i] * ws[t][e];
             store4<BF16>(A.y, row * A.ldy + c, c, A.n, A.vec, v);
         }
     }
