@@ -14,27 +14,24 @@ namespace dspk {
 //
 // Streams read each weight fragment once into registers and all of x for every 16 or
 // 32 columns: best while x is small beside the weight.  Tiles stage both through
-// LDS, so x is read once per 64 to 256 columns.  Measured (us, weights in memory;
-// tile splits in brackets), n x k:
-//            19456x2560       2560x9728        34816x5120       5120x17408
-//   rows   stream  tile     stream  tile     stream  tile     stream  tile
-//      1    10.0  13.0        6.9   9.6 [4]   29.8  40.7       15.9  20.4 [6]
-//     16    11.9  13.9       10.0   9.8 [4]   34.6  41.2       20.6  20.9 [6]
-//     17    12.3  14.2       10.2  10.0 [4]   34.9  41.7       22.5  21.2 [6]
-//     32    15.7  15.1       13.8  10.1 [4]   46.7  42.4       30.3  21.3 [6]
-//     33    16.5  21.8       15.1  12.1 [6]   50.2  52.8       30.7  24.2 [3]
-//     64    23.6  24.1       22.6  12.5 [4]   67.9  58.5       45.7  25.8 [3]
+// LDS, so x is read once per 64 to 256 columns.  Measured (us, weights in memory,
+// tiles with their best splits of K), n x k:
+//            4096x4096       2560x9728       19456x2560      5120x17408
+//   rows   stream  tile    stream  tile    stream  tile    stream  tile
+//      1     4.7    9.9      6.7   10.0      9.8   12.4     15.9   20.8
+//     16     5.7   10.0      9.9   10.2     11.8   13.2     20.9   21.2
+//     18     5.8   10.2     10.3   10.4     12.6   13.7     23.2   21.4
+//     32     7.1   10.2     13.9   10.5     15.7   14.4     30.2   21.6
+//     36     8.1    9.0     15.8   10.9     17.8   15.1     33.0   23.1
+//     64    11.0    9.1     22.6   11.3     23.7   16.2     45.5   24.2
 // Two column tiles per stream workgroup where there are more tiles than CUs (16
 // rows, 384 tiles: 6.4 -> 5.8 us), one where there are not (160 tiles: 6.2 / 5.3).
 //
-// Tiles and their K splits are chosen by an estimate fitted to measured launches: a
-// workgroup's start and end take 4 us, a stage of 128 K takes the longer of the time
-// that all resident workgroups' loads need of the caches (16.5 TB/s) and the stage's
-// own time (1.4 times that for two on a CU), a split costs 2 us and .3 us per MB of
-// sums that change hands.  E.g. 301 rows of 6144x4096: 64x128 18.4 us (estimated 18.4),
-// split in two 19.7 (22.2), 128x128 in three 24.3 (26.6); 512 rows of 2560x9728: 64x128
-// in three 24.2 (28.8), 128x128 in three 29.7 (31.0); 1024 rows of 19456x2560: 256x256
-// 69.2 (64), 128x128 83.2 (79).
+// The choice is by estimates fitted to some 800 measured launches of 240 products, 17
+// to 8190 rows, and is 1 to 2% behind the best of them on average, 15% at worst.  A
+// round of tiles takes 3.6 us and a time per stage of 128 K (1.46 times that for two
+// workgroups on a CU), a split 2.2 us and .28 us per MB of sums that change hands; a
+// stream moves its columns and all rows of x past a CU at some 33 GB/s.
 I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
     I8Plan p{};
     const int64_t steps = i8_steps(k), stages = steps / 2, tiles = i8_tiles(n);
@@ -70,9 +67,6 @@ I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
             }
         }
     }
-    // Streams: a workgroup takes its columns and all rows of x past it at some 33 GB/s,
-    // which up to 16 rows is always the shorter (1 / 16 rows of 2560x9728 6.7 / 9.9 us,
-    // tiles 10.0 / 10.2; 32 rows 13.9 and 10.5; 32 rows of 4096x4096 7.1 and 10.2).
     const bool wide = tiles > cus;
     const int64_t groups = over(tiles, wide ? 2 : 1);
     if (m <= 16 || (m <= 64 && 2 + 30e-6 * (m + (wide ? 32 : 16)) * k * over(groups, cus) <= best)) {
@@ -120,11 +114,14 @@ MoePlan moe_plan(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int3
     p.off_h_scales = up(p.off_h8 + slots * p.ldh);
     p.off_top = up(p.off_h_scales + slots * sizeof(float));
     p.off_part = up(p.off_top + slots * (p.ldh / kI8Cols) * sizeof(uint32_t));
+    // h's codes made by each down workgroup, a row per wave: the layer's two launches for 8
+    // slots of 768 values 17.7 -> 14.6 us, for 16 of 2048 40.8 -> 39.3, but for 2 of 14336 46.6
+    // -> 56.4, which a wave alone turns into codes.
+    p.inside = slots <= kDownWaves && p.ldh <= kMoeInside;
     // Enough workgroups for the CUs, where one group of slots is all and each wave keeps
-    // two pieces of work or more (2048 columns, 8 / 48 slots of 768: one part 8.8 / 24.1
-    // us, two 9.4 / 19.4, four 13.3 / 22.9).
+    // two pieces of work or more (2048 columns, 8 / 16 / 48 slots of 768, both launches: one
+    // part 14.6 / 21.8 / 48.6 us, two 15.8 / 22.0 / 42.9, four 19.7 / 25.7 / 46.3).
     const int64_t tiles = i8_tiles(hidden), work = ((int64_t)slots < experts ? (int64_t)slots : experts) * ((i8_steps(inter) + 7) / 8);
-    p.inside = slots <= kDownWaves && (int64_t)slots * (p.ldh + 16) <= kMoeInside;
     p.parts = 1;
     if (slots <= kMoeGroup && tiles <= kMoeSplitTiles)
         while (p.parts < kMoeMaxParts && tiles * p.parts * 2 <= cus && work >= 32 * p.parts) p.parts *= 2;

@@ -4,13 +4,13 @@
 // and orders of K all give the same bits; i8_plan chooses among them by time alone.
 //
 // Few rows (streams) are bound by the weight's way from memory: 19456x2560 over one
-// row 9.6-10 us (5.0-5.2 TB/s), 34816x5120 29.8 (6.0), 5120x17408 15.9 (5.6); a large
+// row 9.1-9.8 us (5.1-5.5 TB/s), 40960x2560 16.7 (6.3), 5120x17408 15.9 (5.6); a large
 // copy moves 5.1 TB/s on this card.  Many rows (tiles) are bound by the matrix units'
 // power: with every operand in registers random codes reach 3.96 POP/s (zeros 4.8), with
 // operands from LDS 3.3, the kernel 2.4 (8192^3, 455 us).  32x32x32 instructions
 // need more of it: 3.3 POP/s from registers, 2.9 from LDS, 2.2 in the kernel.  In between
 // the caches' rate to the CUs (some 16 TB/s) decides: it is why 301 rows of 6144x4096
-// take 18.4 us, with weights and rows read again by every tile.
+// take 16.5 us, with weights and rows read again by every tile.
 #include <hip/hip_runtime.h>
 
 #include "i8_device.h"
@@ -145,6 +145,10 @@ hipError_t launch_stream(const I8GemmArgs &a, const I8Plan &p, hipStream_t s) {
 // Rows of x lie KS bytes apart, 16-byte piece p of row r at a place of its line that
 // depends on r, so that 16 neighbouring rows' pieces, which an LDS cycle reads, are
 // in different banks; weight fragments lie as in memory.
+// Waves take 16 or 32 rows x 32 columns (64 x 32 of a 128 x 128 tile), eight of them: with
+// four waves of 32 x 64 a 64 x 128 tile's products take 19.1 us instead of 16.6 (301 rows of
+// 6144x4096), a 64 x 64 tile's with five buffers, of which one workgroup fits a CU, 24.1
+// instead of 14.9 (320 of 4096x4096); deeper rings and 256 K per stage are slower.
 template <int WR, int WC, int TX, int TW, int KS, int NB>
 struct Tile {
     static constexpr int WAVES = WR * WC, BM = 16 * WR * TX, BN = 16 * WC * TW;

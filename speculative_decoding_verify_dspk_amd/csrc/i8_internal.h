@@ -103,7 +103,7 @@ constexpr int kMoeMaxSlots = kMoeMaxRows * kMoeMaxTop;
 // each row's tiles, the down workgroups' sums, each written before it is read.
 constexpr int kMoeGroup = 512;      // slots that a down workgroup has sums for at a time
 constexpr int kDownWaves = 16;      // of a down workgroup
-constexpr int kMoeInside = 48 << 10;        // codes of h that a down workgroup's LDS holds
+constexpr int kMoeInside = 2048;    // longest row of h whose codes are made inside the down workgroups
 constexpr int kMoeMaxParts = 8, kMoeSplitTiles = 512;      // tiles of 16 columns whose sums are split
 constexpr size_t kMoeCtr = 256, kMoeDown = kMoeCtr + 4 * kMoeMaxExperts, kMoeHead = kMoeDown + 4 * kMoeSplitTiles;
 struct MoePlan {

@@ -8,10 +8,16 @@
 //   down   a workgroup per 16 columns of y: its waves share out the chosen experts and
 //          their K, add whole-number sums in LDS (exact in any order), and then each
 //          token's slots in their order.
-// Between them h's rows become codes: where LDS holds them all, every down workgroup
-// does that for itself (some 1 us); else the last of an expert's up workgroups to arrive
-// does (some 3 us of stores, arrivals and loads that pass between dies).
+// Between them h's rows become codes: few and short ones in every down workgroup for
+// itself, while its weights are on their way; else in the last of an expert's up
+// workgroups to arrive (some 3 us of stores, arrivals and loads that pass between dies).
 // Each expert's weights are read once for up to 32 of its rows.
+//
+// Bound by the chosen experts' way from memory where there are many, by chains of
+// dependent accesses where there are few.  Measured (us): 1 / 6 rows of 8 of 128 experts
+// 2048 -> 768 (38 / some 190 MB): route 7.2 / 8.2, up 7.7 / 27.0, down 6.9 / 16.7; 32 rows of 2 of
+// 8, 4096 -> 14336 (1409 MB): route 6.8, up 167 (5.6 TB/s), down 76 (6.2; a large copy
+// moves 5.1, half of it stores).
 #include <hip/hip_runtime.h>
 
 #include "i8_device.h"
@@ -513,13 +519,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(const MoeArgs
     }
 }
 
-// Up to 16 slots whose codes LDS holds: a wave turns a row of h into codes while its
+// Up to 16 slots of short rows: a wave turns a row of h into codes while its
 // first piece of the weights is on its way, and finds the pieces of work from the ids
 // in its registers.
 constexpr int kHeld = 4;            // quads of a row of h that a lane holds
 template <bool BF16>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_down_few_kernel(const MoeArgs A) {
-    __shared__ __attribute__((aligned(16))) int8_t codes[kMoeInside];
+    __shared__ __attribute__((aligned(16))) int8_t codes[kDownWaves * (kMoeInside + 16)];
     __shared__ float scales[kDownWaves];
     __shared__ Sums sums[kDownWaves];
     __shared__ int32_t ids[kDownWaves];
@@ -628,8 +634,9 @@ template <bool INSIDE>
 hipError_t launch_inside(const MoeArgs &a, hipStream_t s) {
     const int slots = a.m * a.top_k, most = slots < a.experts ? slots : a.experts;
     // 32 columns of gate and up per workgroup; its waves take 8 fragments or more each
-    // (1 / 6 rows of 8 of 128 experts 2048 -> 768, 32 rows of 2 of 8 4096 -> 14336: four
-    // waves 9.5 / 27.4 / 179 us, eight 9.8 / 30.0 / 173; 16 columns and four 10.1 / 29.4 / 193)
+    // (with h's codes made here, 1 / 6 rows of 8 of 128 experts 2048 -> 768, 32 rows of 2 of
+    // 8 4096 -> 14336: four waves 9.5 / 27.4 / 179 us, eight 9.8 / 30.0 / 173; 16 columns and
+    // four 10.1 / 29.4 / 193)
     const dim3 up((unsigned)((i8_tiles(a.inter) + 1) / 2), most);
     if (i8_steps(a.hidden) >= 48)
         hipLaunchKernelGGL((moe_up_kernel<2, 8, INSIDE>), up, dim3(512), 0, s, a);
