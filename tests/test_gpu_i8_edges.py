@@ -22,6 +22,14 @@ def test_few_slots(hidden, inter, experts, m, top, kind):
     L.check(*L.choice(top), dtype=torch.float32 if kind == "f32" else torch.bfloat16)
 
 
+@pytest.mark.parametrize("hidden,inter,experts,m,top", [
+    (33, 48, 40, 64, 32), (48, 31, 33, 64, 9),       # slots past what LDS holds at a time
+    (16, 16, 1024, 20, 32), (8200, 40, 6, 9, 2)])    # the most experts; more columns than parts are numbered for
+def test_many_slots_experts_and_columns(hidden, inter, experts, m, top):
+    L = Layer(hidden, inter, experts, m, seed=hidden + inter)
+    L.check(*L.choice(top))
+
+
 def test_few_slots_unused_twice_or_no_expert():
     L = Layer(80, 300, 5, 4, seed=2)
     ids = np.array([[2, 2, 2, 2], [-1, 0, -1, 3], [4, 5, 0, 1], [-1, -1, -1, -1]], dtype=np.int32)
