@@ -27,11 +27,12 @@ namespace dspk {
 // Two column tiles per stream workgroup where there are more tiles than CUs (16
 // rows, 384 tiles: 6.4 -> 5.8 us), one where there are not (160 tiles: 6.2 / 5.3).
 //
-// The choice is by estimates fitted to some 800 measured launches of 240 products, 17
-// to 8190 rows, and is 1 to 2% behind the best of them on average, 15% at worst.  A
-// round of tiles takes 3.6 us and a time per stage of 128 K (1.46 times that for two
-// workgroups on a CU), a split 2.2 us and .28 us per MB of sums that change hands; a
-// stream moves its columns and all rows of x past a CU at some 33 GB/s.
+// The choice is by estimates fitted to some 2000 measured launches of 170 products, 20
+// to 3000 rows: it is .9% behind the best of them on average, 14% at worst.  A
+// round of tiles takes 3.4 us and a time per stage of 128 K (1.55 times that for two
+// workgroups on a CU), but no less than the weight's way from memory; a split 1.75 us and
+// .35 us per MB of sums that change hands; a stream moves its columns and all rows of x
+// past a CU at some 32 GB/s.
 I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
     I8Plan p{};
     const int64_t steps = i8_steps(k), stages = steps / 2, tiles = i8_tiles(n);
@@ -40,10 +41,10 @@ I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
     struct Shape {
         I8Kind kind;
         int rows, cols;
-        double own;                 // us of a stage alone on a CU; two share it in 1.46 times that
+        double own;                 // us of a stage alone on a CU; two share it in 1.55 times that
     };
-    static const Shape shapes[] = {{kI8Tile32x64, 32, 64, .3}, {kI8Tile64x64, 64, 64, .26},
-                                   {kI8Tile64x128, 64, 128, .4}, {kI8Tile128x128, 128, 128, .67}};
+    static const Shape shapes[] = {{kI8Tile32x64, 32, 64, .19}, {kI8Tile64x64, 64, 64, .225},
+                                   {kI8Tile64x128, 64, 128, .345}, {kI8Tile128x128, 128, 128, .66}};
     double best = 1e300;
     for (const Shape &c : shapes) {
         if (m <= 16) break;
@@ -52,9 +53,10 @@ I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
         for (int s = 1; s <= 8; ++s) {
             if (s > 1 && (!split || stages < 4 * s || of * s > 4 * cus || of > kI8MaxSplitTiles)) break;
             const int64_t all = of * s;
-            const double stage = all > cus ? 1.46 * c.own : c.own;
-            const double us = (double)over(all, 2 * cus) * (3.6 + (double)stages / s * stage) +
-                              (s > 1 ? 2.2 + .28e-6 * 4 * all * c.rows * c.cols : 0);
+            const double stage = all > cus ? 1.55 * c.own : c.own;
+            const double tiled = (double)over(all, 2 * cus) * (3.4 + (double)stages / s * stage);
+            const double read = 3.4 + 1e-6 / 7.3 * n * k;
+            const double us = (tiled > read ? tiled : read) + (s > 1 ? 1.75 + .35e-6 * 4 * all * c.rows * c.cols : 0);
             if (us >= best) continue;
             best = us;
             p.kind = c.kind;
@@ -69,7 +71,7 @@ I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
     }
     const bool wide = tiles > cus;
     const int64_t groups = over(tiles, wide ? 2 : 1);
-    if (m <= 16 || (m <= 64 && 2 + 30e-6 * (m + (wide ? 32 : 16)) * k * over(groups, cus) <= best)) {
+    if (m <= 16 || (m <= 64 && 1.4 + 31e-6 * (m + (wide ? 32 : 16)) * k * over(groups, cus) <= best)) {
         p = I8Plan{};
         p.splits = 1;
         p.kind = m <= 16 ? (wide ? kI8Stream16x2 : kI8Stream16x1)
@@ -89,7 +91,7 @@ I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
     // 256 x 256: whole rounds of one workgroup per CU, then the rest in quarters, if that
     // is the shorter
     const int64_t big = over(m, 256) * over(n, 256), rest = big % cus;
-    const double whole = 7 + 1.67 * stages, quarters = (double)over(4 * rest, cus) * (4 + .57 * stages);
+    const double whole = 8 + 1.5 * stages, quarters = (double)over(4 * rest, cus) * (4 + .5 * stages);
     const bool cut = rest != 0 && quarters < whole;
     const double us = (double)(cut ? big / cus : over(big, cus)) * whole + (cut ? quarters : 0);
     if (m > 64 && us < best) {

@@ -10,7 +10,7 @@
 // operands from LDS 3.3, the kernel 2.4 (8192^3, 455 us).  32x32x32 instructions
 // need more of it: 3.3 POP/s from registers, 2.9 from LDS, 2.2 in the kernel.  In between
 // the caches' rate to the CUs (some 16 TB/s) decides: it is why 301 rows of 6144x4096
-// take 16.5 us, with weights and rows read again by every tile.
+// take 15.7 us, with weights and rows read again by every tile.
 #include <hip/hip_runtime.h>
 
 #include "i8_device.h"

@@ -17,9 +17,9 @@ ROCM_INC = "/opt/rocm/include"
 # or in quarters (2)
 PLANS = {(7, 130, 300): (0, False, 0), (5, 4112, 96): (1, False, 0), (18, 130, 150): (2, False, 0),
          (18, 4100, 150): (3, False, 0), (40, 130, 150): (4, False, 0), (40, 4100, 150): (5, False, 0),
-         (31, 8200, 2100): (6, False, 0), (18, 130, 6500): (6, True, 0), (130, 130, 150): (7, False, 0),
-         (64, 130, 2100): (7, True, 0), (200, 8200, 150): (8, False, 0), (40, 8200, 9000): (8, True, 0),
-         (1560, 2570, 150): (9, False, 0), (200, 4100, 13000): (9, True, 0), (390, 20500, 150): (10, False, 1),
+         (31, 8200, 1100): (6, False, 0), (18, 130, 6500): (6, True, 0), (130, 130, 150): (7, False, 0),
+         (64, 130, 2100): (7, True, 0), (200, 4100, 150): (8, False, 0), (130, 1500, 9000): (8, True, 0),
+         (1560, 2570, 150): (9, False, 0), (200, 8200, 9000): (9, True, 0), (390, 20500, 300): (10, False, 1),
          (200, 8200, 4200): (10, False, 2), (1560, 10300, 150): (10, False, 3)}
 
 
