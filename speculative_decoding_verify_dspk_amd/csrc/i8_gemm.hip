@@ -140,16 +140,17 @@ hipError_t launch_stream(const I8GemmArgs &a, const I8Plan &p, hipStream_t s) {
 
 // ------------------------------------------------------------------- many rows
 // A workgroup of WR x WC waves takes BM rows x BN columns, a wave 16 TX rows x 16 TW
-// columns of it.  K goes by stages of KS = 64 or 128 through a
-// ring of NB buffers in LDS, filled by direct global-to-LDS loads NB - 1 stages ahead.
+// columns of it.  K goes by stages of KS through a ring of NB buffers in LDS, filled by
+// direct global-to-LDS loads NB - 1 stages ahead.
 // Rows of x lie KS bytes apart, 16-byte piece p of row r at a place of its line that
 // depends on r, so that 16 neighbouring rows' pieces, which an LDS cycle reads, are
 // in different banks; weight fragments lie as in memory.
-// Waves take 16 or 32 rows x 32 columns (64 x 32 of a 128 x 128 tile), eight of them: with
-// four waves of 32 x 64 a 64 x 128 tile's products take 19.1 us instead of 16.6 (301 rows of
-// 6144x4096), a 64 x 64 tile's with five buffers, of which one workgroup fits a CU, 24.1
+// Eight waves take 16 or 32 rows x 32 columns each (64 x 32 of a 128 x 128 tile; a 32 x 64
+// tile has four of 32 x 16): with four waves of 32 x 64 the 64 x 128 tiles take 19.1 us
+// instead of 16.6 (301 rows of 6144x4096), the 64 x 64 tile's with five buffers, of which one workgroup fits a CU, 24.1
 // instead of 14.9 (320 of 4096x4096); deeper rings and 256 K per stage are slower.
-template <int WR, int WC, int TX, int TW, int KS, int NB>
+constexpr int KS = 128;
+template <int WR, int WC, int TX, int TW, int NB>
 struct Tile {
     static constexpr int WAVES = WR * WC, BM = 16 * WR * TX, BN = 16 * WC * TW;
     static constexpr int XB = BM * KS, WB = BN * KS, STAGE = XB + WB;       // bytes of a stage
@@ -158,8 +159,8 @@ struct Tile {
     static_assert(NB * STAGE <= 160 * 1024, "LDS");
     static constexpr int P = KS / 16, R = 64 / P;      // pieces of a row, rows of a load
     // the line of row r and the place of its piece p
-    static __device__ __forceinline__ int line(int r) { return KS == 128 ? r ^ (r >> 3 & 1) : r; }
-    static __device__ __forceinline__ int place(int r, int p) { return KS == 128 ? p ^ (r & 7) : p ^ (r >> 2 & 3); }
+    static __device__ __forceinline__ int line(int r) { return r ^ (r >> 3 & 1); }
+    static __device__ __forceinline__ int place(int r, int p) { return p ^ (r & 7); }
 };
 
 __device__ __forceinline__ void to_lds(const void *src, char *dst) {
@@ -198,9 +199,9 @@ struct Buffers {
 // The tile at row0 and 16-column tile tile0, over a ring of NB buffers.
 // SPLIT: workgroup blockIdx.y of A.splits takes its part of K; the last of them to
 // arrive adds the others' sums (whole numbers: in any order the same).
-template <int WR, int WC, int TX, int TW, int KS, int NB, bool SPLIT, bool BF16>
+template <int WR, int WC, int TX, int TW, int NB, bool SPLIT, bool BF16>
 __device__ __forceinline__ void tile_work(const I8GemmArgs &A, int row0, int tile0, const Buffers (&ring)[NB]) {
-    using T = Tile<WR, WC, TX, TW, KS, NB>;
+    using T = Tile<WR, WC, TX, TW, NB>;
     static_assert(NB >= 2 && NB <= 4, "ring");
     constexpr int L = T::XI + T::WI;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -350,9 +351,9 @@ __device__ __forceinline__ void tile_work(const I8GemmArgs &A, int row0, int til
     }
 }
 
-template <int WR, int WC, int TX, int TW, int KS, int NB, int OCC, bool BF16>
+template <int WR, int WC, int TX, int TW, int NB, int OCC, bool BF16>
 __global__ __launch_bounds__(64 * WR * WC, OCC) void i8_tile_kernel(const I8GemmArgs A) {
-    using T = Tile<WR, WC, TX, TW, KS, NB>;
+    using T = Tile<WR, WC, TX, TW, NB>;
     __shared__ __attribute__((aligned(1024))) char b0[T::STAGE], b1[T::STAGE], b2[NB > 2 ? T::STAGE : 16],
         b3[NB > 3 ? T::STAGE : 16];
     char *const every[4] = {b0, b1, b2, b3};
@@ -362,17 +363,17 @@ __global__ __launch_bounds__(64 * WR * WC, OCC) void i8_tile_kernel(const I8Gemm
     const int rows = (A.m + T::BM - 1) / T::BM, cols = (A.n + T::BN - 1) / T::BN;
     int r, c;
     tile_of(on_die(blockIdx.x, rows * cols), rows, cols, r, c);
-    tile_work<WR, WC, TX, TW, KS, NB, true, BF16>(A, r * T::BM, c * (T::BN / kI8Cols), ring);
+    tile_work<WR, WC, TX, TW, NB, true, BF16>(A, r * T::BM, c * (T::BN / kI8Cols), ring);
 }
 
-template <int WR, int WC, int TX, int TW, int KS, int NB, int OCC>
+template <int WR, int WC, int TX, int TW, int NB, int OCC>
 hipError_t launch_tile(const I8GemmArgs &a, const I8Plan &p, hipStream_t s) {
-    using T = Tile<WR, WC, TX, TW, KS, NB>;
+    using T = Tile<WR, WC, TX, TW, NB>;
     const dim3 grid((unsigned)p.groups, a.splits), block(64 * T::WAVES);
     if (a.y_bf16)
-        hipLaunchKernelGGL((i8_tile_kernel<WR, WC, TX, TW, KS, NB, OCC, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((i8_tile_kernel<WR, WC, TX, TW, NB, OCC, true>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((i8_tile_kernel<WR, WC, TX, TW, KS, NB, OCC, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((i8_tile_kernel<WR, WC, TX, TW, NB, OCC, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -382,22 +383,22 @@ hipError_t launch_tile(const I8GemmArgs &a, const I8Plan &p, hipStream_t s) {
 // (8192^3 470 against 458 us), 128 x 64 wave tiles turned the other way too (463).
 template <bool BF16>
 __global__ __launch_bounds__(512, 2) void i8_big_kernel(const I8GemmArgs A) {
-    using B = Tile<4, 2, 4, 8, 128, 2>;
-    using Q = Tile<2, 4, 4, 2, 128, 4>;
+    using B = Tile<4, 2, 4, 8, 2>;
+    using Q = Tile<2, 4, 4, 2, 4>;
     static_assert(B::XB == Q::STAGE && B::WB == Q::STAGE, "a quarter's stage takes half a whole one's");
     __shared__ __attribute__((aligned(1024))) char b0[Q::STAGE], b1[Q::STAGE], b2[Q::STAGE], b3[Q::STAGE];
     const int rows = (A.m + B::BM - 1) / B::BM, cols = (A.n + B::BN - 1) / B::BN, i = blockIdx.x;
     int r, c;
     if (i < A.whole) {
         tile_of(on_die(i, A.whole), rows, cols, r, c);
-        tile_work<4, 2, 4, 8, 128, 2, false, BF16>(A, r * B::BM, c * (B::BN / kI8Cols), {{b0, b1}, {b2, b3}});
+        tile_work<4, 2, 4, 8, 2, false, BF16>(A, r * B::BM, c * (B::BN / kI8Cols), {{b0, b1}, {b2, b3}});
         return;
     }
     const int at = on_die(i - A.whole, gridDim.x - A.whole);
     tile_of(A.whole + at / 4, rows, cols, r, c);
     const int row0 = r * B::BM + (at & 1) * (B::BM / 2), tile0 = (2 * c + (at >> 1 & 1)) * (B::BN / kI8Cols / 2);
     if (row0 >= A.m || tile0 >= A.tiles_n) return;
-    tile_work<2, 4, 4, 2, 128, 4, false, BF16>(
+    tile_work<2, 4, 4, 2, 4, false, BF16>(
         A, row0, tile0, {{b0, b0 + Q::XB}, {b1, b1 + Q::XB}, {b2, b2 + Q::XB}, {b3, b3 + Q::XB}});
 }
 hipError_t launch_big(const I8GemmArgs &a, const I8Plan &p, hipStream_t s) {
@@ -425,10 +426,10 @@ hipError_t launch_i8_gemm(const I8GemmArgs &a, const I8Plan &p, hipStream_t s) {
         case kI8Stream32x2: return launch_stream<2, 2, 4>(a, p, s);
         case kI8Stream64x1: return launch_stream<4, 1, 4>(a, p, s);
         case kI8Stream64x2: return launch_stream<4, 2, 2>(a, p, s);
-        case kI8Tile32x64: return launch_tile<1, 4, 2, 1, 128, 4, 2>(a, p, s);
-        case kI8Tile64x64: return launch_tile<4, 2, 1, 2, 128, 4, 2>(a, p, s);
-        case kI8Tile64x128: return launch_tile<2, 4, 2, 2, 128, 3, 2>(a, p, s);
-        case kI8Tile128x128: return launch_tile<2, 4, 4, 2, 128, 2, 2>(a, p, s);
+        case kI8Tile32x64: return launch_tile<1, 4, 2, 1, 4, 2>(a, p, s);
+        case kI8Tile64x64: return launch_tile<4, 2, 1, 2, 4, 2>(a, p, s);
+        case kI8Tile64x128: return launch_tile<2, 4, 2, 2, 3, 2>(a, p, s);
+        case kI8Tile128x128: return launch_tile<2, 4, 4, 2, 2, 2>(a, p, s);
         case kI8Tile256x256: return launch_big(a, p, s);
     }
     return hipErrorInvalidValue;
