@@ -147,8 +147,9 @@ hipError_t launch_stream(const I8GemmArgs &a, const I8Plan &p, hipStream_t s) {
 // in different banks; weight fragments lie as in memory.
 // Eight waves take 16 or 32 rows x 32 columns each (64 x 32 of a 128 x 128 tile; a 32 x 64
 // tile has four of 32 x 16): with four waves of 32 x 64 the 64 x 128 tiles take 19.1 us
-// instead of 16.6 (301 rows of 6144x4096), the 64 x 64 tile's with five buffers, of which one workgroup fits a CU, 24.1
-// instead of 14.9 (320 of 4096x4096); deeper rings and 256 K per stage are slower.
+// instead of 16.6 (301 rows of 6144x4096); 64 x 64 tiles with five buffers, of which one
+// workgroup fits a CU, 24.1 instead of 14.9 (320 of 4096x4096).  Deeper rings and 256 K per
+// stage are slower.
 constexpr int KS = 128;
 template <int WR, int WC, int TX, int TW, int NB>
 struct Tile {
