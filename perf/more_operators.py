@@ -172,7 +172,9 @@ def _calls(s):
     if op == "mlp":
         f = c["f"]
         gu, dn = binding.Int8Weight(s["gu8"], s["gus"]), binding.Int8Weight(s["dn8"], s["dns"])
-        need = max(binding.i8_workspace_bytes(2 * f, n, m), binding.i8_workspace_bytes(n, f, m))
+        # of the products that are issued below
+        wide = 2 * f if f % 8 == 0 else f
+        need = max(binding.i8_workspace_bytes(wide, n, m), binding.i8_workspace_bytes(n, f, m))
         ws, (h8, hs) = binding.alloc_workspace(need), codes(f)
         # one product for both where up's columns start at a whole 16-byte piece
         if f % 8 == 0:
