@@ -91,7 +91,7 @@ __global__ __launch_bounds__(kRowMostThreads) void rows_kernel(const RowArgs A) 
                 if (A.r != nullptr) r[p].load(A.r, row * A.ldr + col, left);
         }
     };
-    int row = blockIdx.x;
+    uint32_t row = blockIdx.x;
     fetch(row);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -99,7 +99,7 @@ __global__ __launch_bounds__(kRowMostThreads) void rows_kernel(const RowArgs A) 
         if constexpr (OP == kRowNorm)
             if (A.w != nullptr) w[p].load(A.w, col, A.n - col);
     }
-    for (int turn = 0; row < A.m; turn ^= 1) {
+    for (int turn = 0;; turn ^= 1) {               // the grid has no more workgroups than rows
         float v[P][8];
         float ss = 0.f;
         uint32_t top = 0;
@@ -122,8 +122,9 @@ __global__ __launch_bounds__(kRowMostThreads) void rows_kernel(const RowArgs A) 
             if constexpr (OP == kRowNorm)
                 if (A.r_out != nullptr) store8<RF>(A.r_out, row * A.ldro + col, left, s);
         }
-        const int next = row + (int)gridDim.x;     // both below 2^31: the grid is a few rows per CU
-        if (next < A.m) fetch(next);
+        const uint32_t next = row + gridDim.x;     // below 2^32: rows and workgroups are below 2^31
+        const bool more = next < (uint32_t)A.m;
+        if (more) fetch(next);
         float inv = 1.f;
         if (OP == kRowNorm || A.codes != nullptr) {
             if constexpr (OP == kRowNorm) ss = wave_sum(ss);
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(kRowMostThreads) void rows_kernel(const RowArgs A) 
             }
         }
         if (A.codes != nullptr && t == 0) A.scales[row] = st.scale;
-        if (next >= A.m) break;                    // also where next has passed 2^31
+        if (!more) break;
         row = next;
     }
 }
