@@ -32,8 +32,10 @@ typedef __attribute__((ext_vector_type(4))) float f4;
 // ---------------------------------------------------------------------- route
 constexpr int kRouteWaves = 16;
 
-// Eight bf16 of a row from column r on, those at k and past it zeros.
-__device__ __forceinline__ bf16x8 bf16_piece(const uint16_t *row, int r, int k) {
+// Eight bf16 of a row from column r on, those at k and past it zeros.  Columns are numbered
+// in 32 unsigned bits: k is below 2^31, and the router's waves stop within a few thousand
+// columns of it.
+__device__ __forceinline__ bf16x8 bf16_piece(const uint16_t *row, uint32_t r, uint32_t k) {
     u32x4 v = *(const u32x4 *)(row + (r < k ? r : 0));     // no branch: several are on their way
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -132,7 +134,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_row_kernel(const Route
         const int k0 = item / tiles, tile = item - k0 * tiles;
         const uint16_t *const rr = A.router + (int64_t)min(16 * tile + c, A.experts - 1) * A.ldr;
         f4 acc = {0.f, 0.f, 0.f, 0.f};
-        for (int r0 = 32 * k0; r0 < A.k; r0 += 32 * ks * U) {
+        for (uint32_t r0 = 32 * k0; r0 < (uint32_t)A.k; r0 += 32 * ks * U) {
             bf16x8 a[U], b[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -172,11 +174,11 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
         acc[i] = f4{0.f, 0.f, 0.f, 0.f};
         xr[i] = A.x + (int64_t)min(16 * i + c, A.m - 1) * A.ldx;
     }
-    for (int r0 = 32 * w; r0 < A.k; r0 += step * U) {
+    for (uint32_t r0 = 32 * w; r0 < (uint32_t)A.k; r0 += step * U) {
         bf16x8 a[U], b[U][MT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + step * u + 8 * j;
+            const uint32_t r = r0 + step * u + 8 * j;
             a[u] = bf16_piece(rr, r, A.k);
 #pragma unroll
             for (int i = 0; i < MT; ++i) b[u][i] = bf16_piece(xr[i], r, A.k);

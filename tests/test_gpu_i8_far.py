@@ -1,5 +1,5 @@
-"""Row calls of the 8-bit integer side at the largest row counts that they take, whose last
-rows' numbers are within a launch's workgroups of 2^31."""
+"""Calls of the 8-bit integer side at the largest sizes that they take: row calls whose last
+rows' numbers are within a launch's workgroups of 2^31, the router over rows as long."""
 import numpy as np
 import pytest
 
@@ -71,3 +71,24 @@ def test_the_most_rows_through_norm_and_activation():
         torch.cuda.synchronize()
         assert torch.equal(out[:TAIL], wants[0]) and torch.equal(out[MOST - TAIL:MOST], wants[1])
         assert torch.equal(x[:TAIL], alone[0]) and torch.equal(x[-TAIL:], alone[1]) and (out[MOST] == 9).all()
+
+
+@pytest.mark.parametrize("k", [2 ** 31 - 1, 2 ** 31 - 2049, 2 ** 31 - 8])
+def test_router_over_the_longest_rows(k):
+    """Scores of a few whole numbers at the front, in the middle and up to the last column."""
+    import torch
+    _room(24)
+    x = torch.zeros(1, 2 ** 31, dtype=torch.bfloat16, device="cuda")
+    router = torch.zeros(2, 2 ** 31, dtype=torch.bfloat16, device="cuda")
+    x[:, k:], router[:, k:] = float("nan"), float("nan")
+    rng, want = np.random.default_rng(k % 1000), np.zeros(2)
+    for at in (0, 2 ** 30 - 700, k - 3000):
+        a, r = rng.integers(-3, 4, (1, 3000)), rng.integers(-3, 4, (2, 3000))
+        x[:, at:at + 3000] = torch.from_numpy(a).bfloat16().cuda()
+        router[:, at:at + 3000] = torch.from_numpy(r).bfloat16().cuda()
+        want += (a @ r.T)[0]
+    ids, wt = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, device="cuda")
+    z, ws = torch.zeros(1, 2, device="cuda"), binding.alloc_workspace(binding.moe_workspace_bytes(16, 16, 2, 1, 1))
+    binding.moe_route(x[:, :k], router[:, :k], 1, ids, wt, ws, scores=z)
+    torch.cuda.synchronize()
+    assert z[0].tolist() == want.tolist() and ids.tolist() == [[int(want[1] > want[0])]] and wt.tolist() == [[1.0]]
