@@ -64,7 +64,7 @@ I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus) {
             p.groups = of;
             p.off_part = p.ws_bytes = 0;
             if (s > 1) {
-                p.off_part = kI8MaxSplitTiles * sizeof(uint32_t);
+                p.off_part = kMoeHead;
                 p.ws_bytes = p.off_part + (size_t)all * c.rows * c.cols * sizeof(int32_t);
             }
         }

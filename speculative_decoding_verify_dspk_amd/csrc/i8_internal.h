@@ -85,7 +85,7 @@ struct I8Plan {
     int32_t splits;                 // tile: of K
     int64_t whole, groups;          // 256 x 256 tiles that are not cut, workgroups
     bool fits;
-    size_t off_part, ws_bytes;      // workspace: arrivals, then sums
+    size_t off_part, ws_bytes;      // workspace: arrivals, then from kMoeHead on sums
 };
 constexpr int kI8MaxSplitTiles = 1024;
 I8Plan i8_plan(int32_t n, int32_t k, int32_t m, bool split, int cus);
@@ -94,8 +94,8 @@ hipError_t launch_i8_gemm(const I8GemmArgs &a, const I8Plan &p, hipStream_t s);
 // ---- expert layers -----------------------------------------------------------
 constexpr int kMoeMaxRows = 64, kMoeMaxExperts = 1024, kMoeMaxTop = 32;
 constexpr int kMoeMaxSlots = kMoeMaxRows * kMoeMaxTop;
-// Workspace: what has to be zero between calls lies at fixed places in front, so
-// that calls of any sizes share one buffer:
+// Workspace: what has to be zero between calls lies at fixed places below kMoeHead, the
+// products' arrivals too, so that calls of any sizes and of both families share one buffer:
 //   [0, 256)   arrivals of the router's workgroups
 //   kMoeCtr    arrivals of each expert's columns
 //   kMoeDown   arrivals at each 16 columns of y
@@ -106,6 +106,7 @@ constexpr int kDownWaves = 16;      // of a down workgroup
 constexpr int kMoeInside = 2048;    // longest row of h whose codes are made inside the down workgroups
 constexpr int kMoeMaxParts = 8, kMoeSplitTiles = 512;      // tiles of 16 columns whose sums are split
 constexpr size_t kMoeCtr = 256, kMoeDown = kMoeCtr + 4 * kMoeMaxExperts, kMoeHead = kMoeDown + 4 * kMoeSplitTiles;
+static_assert(4 * kI8MaxSplitTiles <= kMoeHead && kMoeHead % 256 == 0, "the products' sums lie behind all arrivals");
 struct MoePlan {
     int64_t ldh;                    // floats of a row of h, bytes of a row of its codes
     int32_t parts;                  // workgroups that share 16 columns of y
