@@ -845,7 +845,10 @@ int dspk_i8_pack(const int8_t *codes, int64_t ldc, int32_t n, int32_t k, int32_t
  *              zero, so one buffer of the largest size serves any sequence of these
  *              and the expert layers' calls ordered on one stream.  With it, calls
  *              with few columns and many rows split their sums over several
- *              workgroups (the result is the same).
+ *              workgroups (the result is the same).  Sizes do not grow with m, n
+ *              or k throughout, a call of fewer rows may need more: "the largest"
+ *              is that of every (n, k, m) the buffer is used with, not of the
+ *              largest m.
  * Errors: DSPK_EINVAL, DSPK_EUNSUPPORTED (k > DSPK_I8_MAX_K, ldx > 2^24, more tiles
  * than one launch numbers), DSPK_EDEVICE.
  */
@@ -885,8 +888,9 @@ int dspk_moe_route(const uint16_t *x, int64_t ldx, const uint16_t *router, int64
 
 /* Workspace of dspk_moe_route and dspk_moe_mlp (one buffer serves both, and
  * dspk_i8_gemm): zero-fill it once before its first use; every call leaves its
- * counters at zero, so one buffer of the largest size serves any sequence of these
- * calls ordered on one stream.  0 if a size is not supported. */
+ * counters at zero, so one buffer of the largest size (of every set of sizes it is
+ * used with: fewer rows may need more) serves any sequence of these calls ordered on
+ * one stream.  0 if a size is not supported. */
 size_t dspk_moe_workspace_bytes(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int32_t top_k);
 
 /*

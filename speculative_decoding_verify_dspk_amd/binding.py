@@ -957,6 +957,8 @@ def i8_read(codes, scales, m: int, n: int, y, stream=None) -> None:
 
 
 def i8_workspace_bytes(n: int, k: int, m: int) -> int:
+    """Bytes of this one call's workspace; fewer rows may need more, so a buffer for
+    several calls takes the largest over each of them."""
     return lib().dspk_i8_workspace_bytes(n, k, m)
 
 
@@ -965,6 +967,7 @@ def i8_gemm(w: Int8Weight, x, x_scales, m: int, y, workspace=None, stream=None) 
 
 
 def moe_workspace_bytes(hidden: int, inter: int, experts: int, m: int, top_k: int) -> int:
+    """As i8_workspace_bytes, of the router and the experts."""
     return lib().dspk_moe_workspace_bytes(hidden, inter, experts, m, top_k)
 
 

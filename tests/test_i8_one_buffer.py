@@ -1,5 +1,6 @@
 """One workspace for 8-bit products and expert layers in turn: neither leaves anything in the
 other's arrival counters."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -61,3 +62,16 @@ def test_products_and_expert_layers_in_turn():
             assert not ws[:6400].any(), "counters left"
     torch.cuda.synchronize()
     assert host(ws[:6400]).sum() == 0
+
+
+def test_the_largest_over_every_call_is_what_a_buffer_needs():
+    """Fewer rows may need more, for products and for expert layers: a buffer of the largest
+    m's size is refused for a smaller one, which names the size it needs."""
+    lib, P, n, k = binding.lib(), 0x100000, 2560, 4096
+    sizes = {m: binding.i8_workspace_bytes(n, k, m) for m in range(1, 600)}
+    most = max(sizes, key=sizes.get)
+    assert sizes[most] > sizes[599]
+    w = binding.Int8WeightDesc(n, k, 1, P, P)
+    got = lib.dspk_i8_gemm(ctypes.byref(w), P, k, P, most, P, 0, n, P, sizes[599], None)
+    assert got == -1 and f"workspace of {sizes[most]} bytes" in lib.dspk_last_error().decode()
+    assert binding.moe_workspace_bytes(2048, 768, 128, 16, 32) > binding.moe_workspace_bytes(2048, 768, 128, 17, 32)
