@@ -216,6 +216,17 @@ def _stream(stream) -> int | None:
     return s.cuda_stream
 
 
+def _hand_over(stream, *tensors) -> None:
+    """Memory of the current stream that work on `stream` uses: that work waits for what
+    the current stream still does with it, and the memory's reuse for that work."""
+    import torch
+    if stream is None or stream == torch.cuda.current_stream():
+        return
+    stream.wait_stream(torch.cuda.current_stream())
+    for t in tensors:
+        t.record_stream(stream)
+
+
 def _rows(t, name: str) -> int:
     """Leading dimension of a row-major 2-D tensor (unit column stride)."""
     if t.dim() != 2 or t.stride(1) != 1:
@@ -431,7 +442,9 @@ def i8_tiled_bytes(n: int, k: int, count: int = 1) -> int:
 class Int8Weight:
     """Weights in 8-bit codes with a scale per output channel, packed into the
     library's tiled layout: codes int8 [n][k] and scales float32 [n], or for
-    the experts of a mixture layer [count][n][k] and [count][n]."""
+    the experts of a mixture layer [count][n][k] and [count][n].  With a stream the
+    work is done there, after what the current one has been given, and the codes
+    may be released at once."""
 
     def __init__(self, codes, scales, stream=None):
         import torch
@@ -450,6 +463,7 @@ class Int8Weight:
             raise DspkError(-2, lib().dspk_last_error().decode())
         ldc = codes.stride(-2) if self.n > 1 or self.count > 1 else max(codes.stride(-2), self.k)
         self.tiles = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        _hand_over(stream, codes, self.tiles)
         _check(lib().dspk_i8_pack(codes.data_ptr(), ldc, self.n, self.k, self.count, self.tiles.data_ptr(), nbytes,
                                   _stream(stream)))
         self.desc = Int8WeightDesc(self.n, self.k, self.count, self.tiles.data_ptr(), scales.data_ptr())
@@ -463,6 +477,7 @@ class Int8Weight:
         ld = -(-k // 16) * 16
         codes = torch.empty((rows.shape[0], ld), dtype=torch.int8, device=w.device)[:, :k]
         scales = torch.empty(rows.shape[0], dtype=torch.float32, device=w.device)
+        _hand_over(stream, rows, codes, scales)
         i8_quantize(rows, rows.shape[0], k, codes, scales, stream)
         return cls(codes.view(w.shape) if ld == k else codes.unflatten(0, w.shape[:-1]), scales.view(w.shape[:-1]), stream)
 
