@@ -783,7 +783,8 @@ typedef struct dspk_rows_out {
  *   out          : y (rows, codes or both).
  * Leading dimensions: >= n, multiples of 4 (fp32) or 8 (bf16), rows 16-byte
  * aligned.  Outputs may not overlap inputs otherwise than as said.  The squares
- * are summed in fp32: magnitudes up to 1e18.
+ * are summed in fp32: magnitudes of s up to 1e18, at any length (the squares of
+ * larger ones may pass fp32's largest number, and their row come out as zeros).
  * Errors: DSPK_EINVAL, DSPK_EUNSUPPORTED (n > DSPK_MAX_WIDTH), DSPK_EDEVICE.
  */
 int dspk_add_rmsnorm(const void *x, int64_t ldx, int32_t x_dtype, const void *residual, int64_t ldr, int32_t r_dtype,

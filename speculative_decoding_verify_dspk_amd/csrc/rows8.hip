@@ -127,16 +127,33 @@ __global__ __launch_bounds__(kRowMostThreads) void rows_kernel(const RowArgs A) 
         if (more) fetch(next);
         float inv = 1.f;
         if (OP == kRowNorm || A.codes != nullptr) {
-            if constexpr (OP == kRowNorm) ss = wave_sum(ss);
+            float all = OP == kRowNorm ? wave_sum(ss) : 0.f;
             top = wave_max(top);
             if (waves > 1) {                       // two sets in turn: the next row's need no second barrier
-                if (lane == 0) sums[turn][wave] = ss, tops[turn][wave] = top;
+                if (lane == 0) sums[turn][wave] = all, tops[turn][wave] = top;
                 __syncthreads();
-                ss = 0.f, top = 0;
-                for (int i = 0; i < waves; ++i) ss += sums[turn][i], top = max(top, tops[turn][i]);
+                all = 0.f, top = 0;
+                for (int i = 0; i < waves; ++i) all += sums[turn][i], top = max(top, tops[turn][i]);
             }
             if constexpr (OP == kRowNorm) {
-                inv = 1.f / sqrtf(ss / (float)A.n + A.eps);
+                float mean = all / (float)A.n;
+                // Squares of 1e18 pass fp32's largest number from 341 of them on, a lane's 32 do
+                // not: the lanes' sums are added up again, 2^-8 times as large.
+                // (Said to be rare where nothing spills: 6 rows of 2560 2.77 -> 2.74 us, but two of
+                // 32768 15.9 -> 17.0.)
+                const bool far = __float_as_uint(all) == 0x7f800000u;
+                if (P == 4 ? far : __builtin_expect(far, 0)) {
+                    all = wave_sum(ss * 0x1p-8f);
+                    if (waves > 1) {
+                        __syncthreads();
+                        if (lane == 0) sums[turn][wave] = all;
+                        __syncthreads();
+                        all = 0.f;
+                        for (int i = 0; i < waves; ++i) all += sums[turn][i];
+                    }
+                    mean = all / (float)A.n * 0x1p8f;
+                }
+                inv = 1.f / sqrtf(mean + A.eps);
                 top = magnitude(__uint_as_float(top) * inv);
             }
         }
