@@ -261,6 +261,7 @@ class DeviceQWeight:
         if nbytes == 0:
             raise ValueError(f"invalid weight shape n={n} k={k} bits={bits}")
         self.tiles = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        _hand_over(stream, *(t for t in (codes, scales, biases, self.tiles) if t is not None))
         _check(lib().dspk_qweight_pack(ctypes.byref(src), self.tiles.data_ptr(), nbytes, _stream(stream)))
         self.desc = TiledDesc(n, k, bits, 64, self.tiles.data_ptr())
 
