@@ -861,7 +861,9 @@ size_t dspk_i8_workspace_bytes(int32_t n, int32_t k, int32_t m);
  * A mixture-of-experts layer for a few tokens
  * -------------------------------------------
  * Each token goes through the top_k experts that its router scores highest, and
- * each expert that any token chose is read once for all of them.
+ * an expert that tokens chose is read for them together: gate and up once for up to
+ * 32 of its rows, down once for up to 16 of them (of every 512 slots of the call);
+ * more rows read it again.
  */
 #define DSPK_MOE_MAX_ROWS    64
 #define DSPK_MOE_MAX_EXPERTS 1024

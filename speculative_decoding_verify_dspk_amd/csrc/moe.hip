@@ -11,7 +11,8 @@
 // Between them h's rows become codes: few and short ones in every down workgroup for
 // itself, while its weights are on their way; else in the last of an expert's up
 // workgroups to arrive (some 3 us of stores, arrivals and loads that pass between dies).
-// Each expert's weights are read once for up to 32 of its rows.
+// An expert's gate and up are read once for up to 32 of its rows, its down once for up to
+// 16 of those in a group of slots; more rows read them again.
 //
 // Bound by the chosen experts' way from memory where there are many, by chains of
 // dependent accesses where there are few.  Measured (us): 1 / 6 rows of 8 of 128 experts
