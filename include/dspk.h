@@ -730,7 +730,8 @@ int dspk_kv_commit(int32_t count, const dspk_kv_cache *caches, const dspk_attn_b
  * Rows and weights in signed 8-bit codes with one fp32 scale per row (token) and
  * per output channel.  Sums of 8-bit products are exact in 32-bit integers, so
  * a row's result is the same bits whatever rows it is computed with, alone or in
- * a prompt: verifying drafts gives exactly what one-token decoding gives.  Per
+ * a prompt: in these calls verifying drafts gives exactly what one-token decoding
+ * gives (the attention side's sums go by its splits, and so by the rows).  Per
  * layer: dspk_add_rmsnorm, dspk_i8_gemm over q, k and v, the attention side's
  * calls, dspk_i8_quantize, dspk_i8_gemm over o, dspk_add_rmsnorm, then either
  * dspk_i8_gemm over gate and up, dspk_silu_mul and dspk_i8_gemm over down, or

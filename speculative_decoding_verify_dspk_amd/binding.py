@@ -471,7 +471,8 @@ class Int8Weight:
 
     @classmethod
     def quantize(cls, w, stream=None) -> "Int8Weight":
-        """From rows of float32 or bf16, [n][k] or [count][n][k]: each output channel in 8 bits."""
+        """From rows of float32 or bf16, [n][k] or [count][n][k]: each output channel in 8
+        bits.  k up to 32768, rows 16-byte aligned."""
         import torch
         k = w.shape[-1]
         rows = w.reshape(-1, k)

@@ -116,9 +116,10 @@ MoePlan moe_plan(int32_t hidden, int32_t inter, int32_t experts, int32_t m, int3
     p.off_h_scales = up(p.off_h8 + slots * p.ldh);
     p.off_top = up(p.off_h_scales + slots * sizeof(float));
     p.off_part = up(p.off_top + slots * (p.ldh / kI8Cols) * sizeof(uint32_t));
-    // h's codes made by each down workgroup, a row per wave: the layer's two launches for 8
-    // slots of 768 values 17.7 -> 14.6 us, for 16 of 2048 40.8 -> 39.3, but for 2 of 14336 46.6
-    // -> 56.4, which a wave alone turns into codes.
+    // h's codes made by each down workgroup, a row per wave: the layer's two launches (2048
+    // columns) for 8 slots of 768 values 17.6 -> 14.6 us, of 1536 23.4 -> 20.7, of 2048 27.1 -> 24.8, of
+    // 4096 42.5 -> 42.1; for 2 slots of 2048 15.6 -> 13.7, of 4096 21.1 -> 20.1 (4096 columns 27.4 ->
+    // 28.3), but of 14336 46.6 -> 56.4, which a wave alone turns into codes.
     p.inside = slots <= kDownWaves && p.ldh <= kMoeInside;
     // Enough workgroups for the CUs, where one group of slots is all and each wave keeps
     // two pieces of work or more (2048 columns, 8 / 16 / 48 slots of 768, both launches: one

@@ -380,7 +380,7 @@ hipError_t launch_tile(const I8GemmArgs &a, const I8Plan &p, hipStream_t s) {
 
 // Tiles of 256 x 256, one workgroup per CU; the last of them, where they would leave
 // CUs without work, as four of 128 x 128 each (4096 rows of 17408x5120, 1088 tiles:
-// 379 -> 350 us; 2.09 POP/s).  Two buffers of 128 K each: four of 64 measure the same
+// 8% less time than without; 334 to 340 us, 2.15 POP/s).  Two buffers of 128 K each: four of 64 measure the same
 // (8192^3 470 against 458 us), 128 x 64 wave tiles turned the other way too (463).
 template <bool BF16>
 __global__ __launch_bounds__(512, 2) void i8_big_kernel(const I8GemmArgs A) {

@@ -620,7 +620,11 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_few_kernel(const Moe
 }  // namespace
 
 hipError_t launch_moe_route(const RouteArgs &a, hipStream_t s) {
-    // 8 experts of 4096: a workgroup per row 6.8 us, one for all 14.5; 128 of 2048: 20.8, 7.5
+    // A workgroup per row against one per 16 experts, 1 / 8 / 64 rows (us): 8 experts of 2048
+    // 5.8 / 6.1 / 6.3 against 4.8 / 5.8 / 15.5, of 4096 5.8 / 6.1 / 6.3 against 6.3 / 8.0 / 23.6; 16 of 4096
+    // 7.0 / 7.4 / 7.5 against 7.7 / 9.1 / 24.7; 32 of 2048 7.0 / 7.2 / 7.4 against 5.7 / 6.6 / 16.6; 64 of
+    // 4096 19.8 / 20.2 / 20.2 against 7.9 / 9.3 / 25.2; 128 of 2048 19.8 / 20.2 / 20.2 against
+    // 6.0 / 7.0 / 17.7.  One bound for all row counts, so some us are left at either side of it.
     const dim3 grid((a.experts + 15) / 16), block(64 * kRouteWaves);
     if ((int64_t)a.experts * a.k <= 48 << 10)
         hipLaunchKernelGGL(route_row_kernel, dim3(a.m), block, 0, s, a);

@@ -12,8 +12,13 @@
 // Bound by memory for many rows, by the chain of load, reduction and store (and the
 // launch) for few.  Measured: norm of 8190 bf16 rows of 5120 with the residual, 8-bit
 // out 66 us (293 MB, 4.4 TB/s; a large copy reaches 5.1), one row of 2560 2.6 us;
-// activation of 1500 rows of 9728 21 us (73 MB); 8190 rows of 5120 from codes to bf16
-// 22 us (126 MB).  Without the next row on its way the norm takes 88 us.
+// activation of 1500 rows of 9728 21 us (73 MB); 8190 rows of 5120 from bf16 to codes 31 us
+// (4.0 TB/s), from fp32 41 (5.2), one of 4096 2.0; from codes to bf16 22 us (126 MB).
+// Without the next row on its way the norm takes 88 us.
+// Rows over 16384 values take four pieces per lane, for which a lane has no registers where
+// an input is fp32: the norm then holds 74 to 266 of them in scratch, the activation 107.
+// 2000 rows of 32768: norm of bf16 rows 96 us (4.7 TB/s), of fp32 rows with a bf16 residual
+// 172 (3.4); activation of bf16 rows 84 (3.9), of fp32 rows 199 (3.0).
 #include <hip/hip_runtime.h>
 
 #include "i8_device.h"
