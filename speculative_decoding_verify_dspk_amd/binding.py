@@ -405,6 +405,18 @@ def _floats(t, name: str, need: int):
     return t
 
 
+def _slots(ids, weights, m: int) -> int:
+    """top_k of a choice: ids [>= m][top_k], weights alike or flat."""
+    if ids.dim() != 2 or ids.shape[0] < m:
+        raise ValueError(f"ids: expected [{m}][top_k]")
+    top_k = ids.shape[1]
+    if weights.dim() > 1 and weights.shape[-1] not in (1, top_k):
+        raise ValueError(f"weights: expected [{m}][{top_k}], as ids, got {tuple(weights.shape)}")
+    _int32(ids, "ids", m * top_k)
+    _floats(weights, "weights", m * top_k)
+    return top_k
+
+
 def _sized_rows(t, name: str, m: int, n: int):
     """(address, leading dimension, element type) of rows [>= m][ld] with n columns at least."""
     at = _row_array(t, name, m)
@@ -761,15 +773,13 @@ def prepare_moe_route(x, router, m: int, ids, weights, workspace, normalize: boo
     xp, ldx, dx = _sized_rows(x, "x", m, k)
     if dx != DSPK_BF16 or dr != DSPK_BF16:
         raise ValueError("x and router: expected bf16 rows (2-byte elements)")
-    if ids.dim() != 2 or ids.shape[0] < m:
-        raise ValueError(f"ids: expected [{m}][top_k]")
-    top_k, zp, ldz = ids.shape[1], None, 0
+    top_k, zp, ldz = _slots(ids, weights, m), None, 0
     if scores is not None:
         zp, ldz, dz = _sized_rows(scores, "scores", m, experts)
         if dz != DSPK_F32:
             raise ValueError("scores: expected float32 rows")
     return Prepared("dspk_moe_route", xp, ldx, rp, ldr, m, k, experts, top_k, int(normalize),
-                    _int32(ids, "ids", m * top_k).data_ptr(), _floats(weights, "weights", m * top_k).data_ptr(), zp, ldz,
+                    ids.data_ptr(), weights.data_ptr(), zp, ldz,
                     workspace.data_ptr(), workspace.numel(),
                     _stream(stream)).holding(x, router, ids, weights, scores, workspace)
 
@@ -778,12 +788,9 @@ def prepare_moe_mlp(moe: MoEWeights, x, x_scales, m: int, ids, weights, y, works
     """x: int8 rows [>= m][hidden] with x_scales; ids and weights [m][top_k], as moe_route gives them."""
     xp, ldx, sp = _code_rows(x, x_scales, m, moe.hidden, "x")
     yp, ldy, dy = _sized_rows(y, "y", m, moe.hidden)
-    if ids.dim() != 2 or ids.shape[0] < m:
-        raise ValueError(f"ids: expected [{m}][top_k]")
-    top_k = ids.shape[1]
+    top_k = _slots(ids, weights, m)
     return Prepared("dspk_moe_mlp", ctypes.byref(moe.gate.desc), ctypes.byref(moe.up.desc), ctypes.byref(moe.down.desc),
-                    xp, ldx, sp, m, _int32(ids, "ids", m * top_k).data_ptr(),
-                    _floats(weights, "weights", m * top_k).data_ptr(), top_k, yp, dy, ldy, workspace.data_ptr(),
+                    xp, ldx, sp, m, ids.data_ptr(), weights.data_ptr(), top_k, yp, dy, ldy, workspace.data_ptr(),
                     workspace.numel(), _stream(stream)).holding(moe, x, x_scales, ids, weights, y, workspace)
 
 
